@@ -348,6 +348,112 @@ ql_status quantize_weight_block_asym_u8(const float* w, int64_t K, int64_t N, in
 ql_status quantize_weight_int4_grouped(const float* w, int64_t K, int64_t N, int64_t group,
                                        int32_t* wq_packed, void* scales, void* stream);
 
+/*
+ * Root-mean-square norm with the residual's addition, written as int8 codes with one scale per
+ * row: the activations of gemm_w8a8_per_channel. Per row m, in fp32:
+ *   h[k] = residual[m,k] + x[m,k]              (x[m,k] without a residual)
+ *   t[k] = h[k] * gamma[k],  s = max(max_k |t[k]|, 1e-10) / 127
+ *   xq[m,k] = clamp(round_half_even(t[k] / s), -127, 127)      (t / s correctly rounded)
+ *   x_scale[m] = s / sqrt(mean_k h[k]^2 + eps)
+ * so that x_scale * xq ~ h / sqrt(mean h^2 + eps) * gamma: the row's norm is common to all its
+ * values and enters the scale only.
+ *
+ * x        [M,K] row-major, fp32 (x_dtype QL_F32) or fp16 (QL_F16)
+ * residual [M,K] row-major, fp32 or fp16 (res_dtype), or NULL for none (res_dtype is then not
+ *          looked at)
+ * gamma    [K] fp32, 16-byte aligned
+ * eps      finite and > 0, else QL_ERR_SHAPE
+ * res_out  [M,K] of res_dtype: h rounded to it (out); it may be the residual itself. NULL with
+ *          a NULL residual, else required
+ * xq       [M,K] int8 row-major (out);  x_scale [M] fp32 (out)
+ * Requires K > 0 and K % 16 == 0.
+ */
+ql_status rms_norm_quantize_int8(const void* x, ql_dtype x_dtype, const void* residual, ql_dtype res_dtype,
+                                 const float* gamma, float eps, int64_t M, int64_t K, void* res_out,
+                                 int8_t* xq, float* x_scale, void* stream);
+
+/*
+ * The same with OCP E4M3 codes, the activations of gemm_e4m3_per_channel:
+ *   s = max(max_k |t[k]|, 1e-10) / 448,  xq[m,k] = e4m3(clamp(t[k] / s, -448, 448))
+ */
+ql_status rms_norm_quantize_e4m3(const void* x, ql_dtype x_dtype, const void* residual, ql_dtype res_dtype,
+                                 const float* gamma, float eps, int64_t M, int64_t K, void* res_out,
+                                 uint8_t* xq, float* x_scale, void* stream);
+
+/*
+ * A paged K/V cache in 4 bits. `cache` is [num_pages][kv_heads][page_size * (D + 8 D / group)]
+ * bytes: each page holds page_size tokens of one head, K and V, as 4-bit codes with an fp16
+ * scale and an fp16 low for each token, head and group of `group` values along the head's D:
+ *   low = fp16(min x),  scale = max(fp16((max x - low) / 15), 2^-24)     (fp16 saturates)
+ *   code = clamp(round_half_even((x - low) / scale), 0, 15),  x ~ scale * code + low
+ * (The order of the bytes in a page is stated in csrc/kv4.h.)
+ *
+ * The three calls below share these arguments:
+ * cache       num_pages * kv_heads * page bytes, 16-byte aligned
+ * page_size   a power of two from 16 to 4096
+ * D, group    D 64, 128 or 256; group 32, 64 or 128 and at most D
+ * block_table int32 [batch][table_width]: page of positions i * page_size .. of each sequence;
+ *             only the entries that a sequence's length reaches are read
+ * seq_lens    int32 [batch]: length of each sequence, the rows of this call included. Less than
+ *             0 counts as 0, more than table_width * page_size as that
+ * starts      int32 [batch + 1], starts[0] = 0, never decreasing, starts[batch] = rows: rows
+ *             starts[b] .. starts[b+1] - 1 are the last positions of sequence b. Where a
+ *             sequence is shorter than its rows, its first rows have no position.
+ * No page may be shared by two sequences that a kv4_append call writes. Page numbers outside
+ * [0, num_pages) are a caller's error that no call turns into an access outside the cache.
+ * QL_ERR_SHAPE also for sizes outside what is stated, num_pages == 0 with rows, and
+ * q_heads not a multiple of kv_heads.
+ */
+
+/*
+ * Writes rows of K and V into the cache; rows without a position are skipped.
+ * k, v  [rows][kv_heads][D], fp32 or fp16 (dtype), row r at k + r * k_stride elements (slices of
+ *       a wider projection are taken as they are); 16-byte aligned, strides multiples of 16
+ *       bytes and at least kv_heads * D
+ */
+ql_status kv4_append(const void* k, const void* v, ql_dtype dtype, int64_t k_stride, int64_t v_stride,
+                     int64_t rows, uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads,
+                     int64_t D, int64_t group, const int32_t* block_table, int64_t table_width,
+                     const int32_t* seq_lens, const int32_t* starts, int64_t batch, void* stream);
+
+/*
+ * Reads rows back: scale * code + low in fp32, rounded once to dtype; zeros for rows without a
+ * position.
+ * k_out, v_out  [rows][kv_heads][D] contiguous, fp32 or fp16 (dtype) (out)
+ */
+ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
+                   int64_t group, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                   const int32_t* starts, int64_t batch, int64_t rows, ql_dtype dtype, void* k_out,
+                   void* v_out, void* stream);
+
+/*
+ * Causal attention of the last rows of each sequence over the cache:
+ *   out[r,h] = sum_j softmax_j(scale * q[r,h] . k[j,h']) v[j,h'],  h' = h / (q_heads / kv_heads)
+ * over the positions j that row r sees: j <= p for a row at position p, and j > p - window if
+ * window > 0. Keys of the call's own rows have to be in the cache already. A row without a
+ * position sees nothing and gives zeros; what the cache holds at positions that a row does not
+ * see (stale values, NaN) does not reach it. Products in fp16 on the matrix cores with fp32
+ * sums, softmax statistics in fp32.
+ *
+ * q       [rows][q_heads][D] fp16, row r at q + r * q_stride elements; 16-byte aligned,
+ *         q_stride a multiple of 8 and at least q_heads * D
+ * out     [rows][q_heads][D] fp16 contiguous (out)
+ * max_q   the most rows of a sequence, max_len the longest length: they shape the launch, and
+ *         wrong ones cost speed only. Both >= 1.
+ * scale   finite; window >= 0, 0 for none
+ * workspace, workspace_bytes  at least what attention_kv4_workspace_bytes says for the same
+ *         sizes (else QL_ERR_SHAPE), 16-byte aligned; may be NULL if that is 0. Its contents
+ *         need not be set, and are not kept.
+ */
+ql_status attention_kv4(const void* q, int64_t q_stride, void* out, int64_t rows, int64_t q_heads,
+                        const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads,
+                        int64_t D, int64_t group, const int32_t* block_table, int64_t table_width,
+                        const int32_t* seq_lens, const int32_t* starts, int64_t batch, int64_t max_q,
+                        int64_t max_len, float scale, int64_t window, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+ql_status attention_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t D,
+                                        int64_t batch, int64_t max_q, int64_t max_len, int64_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

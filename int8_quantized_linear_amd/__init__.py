@@ -23,6 +23,8 @@ __all__ = [
     "quantize_per_row_int8_asym", "weight_column_sums_i8", "gemm_w8a8_asym", "linear_w8a8_asym",
     "quantize_per_row_e4m3", "quantize_weight_per_channel_e4m3", "gemm_e4m3_per_channel",
     "linear_e4m3", "quantize_per_tensor_int8", "gemm_w8a8_requant",
+    "rms_norm_quantize_int8", "rms_norm_quantize_e4m3", "kv4_page_bytes", "kv4_append", "kv4_read",
+    "attention_kv4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,6 +40,7 @@ lib = ctypes.CDLL(library_path)
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
+_F = ctypes.c_float
 
 QL_F32, QL_F16 = 0, 1
 # ql_activation: applied by the epilogue after the scales and the bias
@@ -64,6 +67,13 @@ _SIGS = {
     "gemm_e4m3_per_channel": [_P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P],
     "quantize_weight_block_asym_u8": [_P, _I64, _I64, _I64, _P, _P, _P, _P],
     "quantize_weight_int4_grouped": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "rms_norm_quantize_int8": [_P, _I, _P, _I, _P, _F, _I64, _I64, _P, _P, _P, _P],
+    "rms_norm_quantize_e4m3": [_P, _I, _P, _I, _P, _F, _I64, _I64, _P, _P, _P, _P],
+    "kv4_append": [_P, _P, _I, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P],
+    "kv4_read": [_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _P],
+    "attention_kv4": [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64,
+                      _I64, _F, _I64, _P, _I64, _P],
+    "attention_kv4_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
@@ -233,6 +243,150 @@ def quantize_weight_int4_grouped(w_nk: torch.Tensor, group: int = 128):
     s = torch.empty((N, K // group), dtype=torch.float16, device=dev)
     _call("quantize_weight_int4_grouped", _ptr(w_nk), K, N, group, _ptr(p), _ptr(s), _stream(w_nk))
     return p, s
+
+
+# ------------------------------------------------- norm, and the 4-bit K/V cache
+
+def rms_norm_quantize_int8(x, gamma, residual=None, eps: float = 1e-6, res_out=None):
+    """Root-mean-square norm of residual + x as int8 codes per row: x [M, K] (fp16 or fp32), gamma
+    fp32 [K], residual [M, K] (fp16 or fp32) or None. Returns (xq int8 [M, K], x_scale fp32 [M])
+    with x_scale * xq ~ h / sqrt(mean(h^2) + eps) * gamma, and with a residual also h = residual +
+    x in the residual's dtype, written to res_out (which may be the residual) or a new tensor."""
+    return _rms_norm(x, gamma, residual, eps, res_out, "rms_norm_quantize_int8", torch.int8)
+
+
+def rms_norm_quantize_e4m3(x, gamma, residual=None, eps: float = 1e-6, res_out=None):
+    """rms_norm_quantize_int8 with fp8 (E4M3) codes: xq is float8_e4m3fn [M, K]."""
+    return _rms_norm(x, gamma, residual, eps, res_out, "rms_norm_quantize_e4m3", torch.float8_e4m3fn)
+
+
+_FLOATS = (torch.float16, torch.float32)
+
+
+def _rms_norm(x, gamma, residual, eps, res_out, fn, code_dtype):
+    _check(x, "x", _FLOATS)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    dev = x.device
+    _check(gamma, "gamma", (torch.float32,), (K,), dev)
+    rdt = QL_F32
+    if residual is not None:
+        _check(residual, "residual", _FLOATS, (M, K), dev)
+        rdt = QL_F16 if residual.dtype == torch.float16 else QL_F32
+        res_out = _out(res_out, "res_out", (M, K), residual.dtype, dev)
+    elif res_out is not None:
+        raise ValueError("res_out needs a residual")
+    xq = torch.empty((M, K), dtype=code_dtype, device=dev)
+    xs = torch.empty((M,), dtype=torch.float32, device=dev)
+    _call(fn, _ptr(x), QL_F16 if x.dtype == torch.float16 else QL_F32, _ptr(residual), rdt, _ptr(gamma), eps, M, K,
+          _ptr(res_out), _ptr(xq), _ptr(xs), _stream(x))
+    return (xq, xs) if residual is None else (xq, xs, res_out)
+
+
+def kv4_page_bytes(page_size: int, head_dim: int, group: int) -> int:
+    """Bytes of one page and kv head of the 4-bit K/V cache, which is a uint8 tensor
+    [num_pages, kv_heads, kv4_page_bytes(...)]. Its contents need not be set before use."""
+    return page_size * (head_dim + 8 * (head_dim // group))
+
+
+def _check_kv4(cache, block_table, seq_lens, starts, head_dim, page_size, group):
+    _check(cache, "cache", (torch.uint8,))
+    if group <= 0 or head_dim % group:
+        raise ValueError("group must divide the head size")
+    if cache.dim() != 3 or cache.shape[2] != kv4_page_bytes(page_size, head_dim, group):
+        raise ValueError("cache has shape %s, expected [num_pages, kv_heads, %d]"
+                         % (tuple(cache.shape), kv4_page_bytes(page_size, head_dim, group)))
+    dev = cache.device
+    _check(block_table, "block_table", (torch.int32,), None, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [batch, pages of a sequence]")
+    batch = block_table.shape[0]
+    _check(seq_lens, "seq_lens", (torch.int32,), (batch,), dev)
+    _check(starts, "starts", (torch.int32,), (batch + 1,), dev)
+    return dev, batch
+
+
+def _rows3(t, name, dtypes, heads, head_dim, device):
+    """A [rows, heads, head_dim] tensor whose rows may lie apart (a slice of a wider projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s has shape %s, expected [rows, %s, %d]"
+                         % (name, tuple(t.shape), "heads" if heads is None else heads, head_dim))
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim)):
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim
+
+
+def kv4_append(k, v, cache, block_table, seq_lens, starts, page_size: int, group: int = 64):
+    """Quantizes rows of k and v [rows, kv_heads, head_dim] (fp16 or fp32; rows may lie apart) into
+    the 4-bit cache. Sequence b owns rows starts[b] to starts[b + 1], its last positions;
+    seq_lens (int32 [batch]) are the lengths with these rows, block_table (int32 [batch, n]) each
+    sequence's pages."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be 3-D [rows, kv_heads, head_dim]")
+    T, H, D = k.shape
+    dev, batch = _check_kv4(cache, block_table, seq_lens, starts, D, page_size, group)
+    ks = _rows3(k, "k", _FLOATS, cache.shape[1], D, dev)
+    vs = _rows3(v, "v", (k.dtype,), H, D, dev)
+    if v.shape[0] != T:
+        raise ValueError("k and v have different numbers of rows")
+    _call("kv4_append", _ptr(k), _ptr(v), QL_F16 if k.dtype == torch.float16 else QL_F32, ks, vs, T, _ptr(cache),
+          cache.shape[0], page_size, H, D, group, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+          _ptr(starts), batch, _stream(cache))
+
+
+def kv4_read(cache, block_table, seq_lens, starts, rows: int, head_dim: int, page_size: int, group: int = 64,
+             dtype=torch.float16):
+    """The last starts[b + 1] - starts[b] positions of each sequence, `rows` in all, as k and v
+    [rows, kv_heads, head_dim] in dtype (fp16 or fp32)."""
+    dev, batch = _check_kv4(cache, block_table, seq_lens, starts, head_dim, page_size, group)
+    if dtype not in _FLOATS:
+        raise TypeError("dtype must be float16 or float32")
+    k = torch.empty((rows, cache.shape[1], head_dim), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    _call("kv4_read", _ptr(cache), cache.shape[0], page_size, cache.shape[1], head_dim, group, _ptr(block_table),
+          block_table.shape[1], _ptr(seq_lens), _ptr(starts), batch, rows,
+          QL_F16 if dtype == torch.float16 else QL_F32, _ptr(k), _ptr(v), _stream(cache))
+    return k, v
+
+
+def attention_kv4(q, cache, block_table, seq_lens, starts, page_size: int, group: int = 64,
+                  max_q: Optional[int] = None, max_len: Optional[int] = None, scale: Optional[float] = None,
+                  window: int = 0, out=None):
+    """Causal attention of q [rows, q_heads, head_dim] (fp16; rows may lie apart) over the 4-bit
+    cache, which already holds the rows' own keys: fp16 [rows, q_heads, head_dim]. Rows, lengths
+    and pages as for kv4_append; q_heads is a multiple of the cache's heads. scale defaults to
+    head_dim ** -0.5; window > 0 keeps the last `window` positions of each row. max_q and max_len,
+    the most rows of a sequence and the longest length, shape the launch; they default to what the
+    tensors' sizes allow."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be 3-D [rows, q_heads, head_dim]")
+    T, HQ, D = q.shape
+    dev, batch = _check_kv4(cache, block_table, seq_lens, starts, D, page_size, group)
+    H = cache.shape[1]
+    qs = _rows3(q, "q", (torch.float16,), None, D, dev)
+    if H == 0 or HQ == 0 or HQ % H:
+        raise ValueError("q has %d heads, not a multiple of the cache's %d" % (HQ, H))
+    if max_q is None:
+        max_q = max(1, T - batch + 1)
+    if max_len is None:
+        max_len = max(1, block_table.shape[1] * page_size)
+    if scale is None:
+        scale = D ** -0.5
+    out = _out(out, "out", (T, HQ, D), torch.float16, dev)
+    need = _I64(0)
+    _call("attention_kv4_workspace_bytes", T, HQ, H, D, batch, max_q, max_len, ctypes.byref(need))
+    ws = torch.empty((need.value,), dtype=torch.uint8, device=dev) if need.value else None
+    _call("attention_kv4", _ptr(q), qs, _ptr(out), T, HQ, _ptr(cache), cache.shape[0], page_size, H, D, group,
+          _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(starts), batch, max_q, max_len, scale,
+          window, _ptr(ws), need.value, _stream(cache))
+    return out
 
 
 # --------------------------------------------------------------------- GEMMs

@@ -3,7 +3,9 @@
 // path can be exercised on a machine without a GPU. Contracts are stated in ql.h.
 #include <stdint.h>
 
-#include "ql_internal.h"
+#include <cmath>
+
+#include "kv4.h"
 
 namespace {
 
@@ -359,6 +361,176 @@ ql_status quantize_weight_int4_grouped(const float* w, int64_t K, int64_t N, int
     if (!aligned(w, 16) || !aligned(wq_packed, 16) || !aligned(scales, 2))
         return QL_ERR_ALIGN;
     return ql::launch_quant_int4_group(w, K, N, group, wq_packed, scales, as_stream(stream));
+}
+
+static ql_status check_rms_norm(const void* x, ql_dtype x_dtype, const void* residual, ql_dtype res_dtype,
+                                const float* gamma, float eps, int64_t M, int64_t K, const void* res_out,
+                                const void* xq, const float* x_scale) {
+    if ((x_dtype != QL_F32 && x_dtype != QL_F16) || (residual && res_dtype != QL_F32 && res_dtype != QL_F16))
+        return QL_ERR_DTYPE;
+    if (bad_dims(M, 1, K) || K % 16 != 0 || !(eps > 0.0f) || !std::isfinite(eps))
+        return QL_ERR_SHAPE;
+    if (M == 0)
+        return QL_OK;
+    if (!x || !gamma || !xq || !x_scale || (residual != nullptr) != (res_out != nullptr))
+        return QL_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(res_out, 16) ||
+        !aligned(xq, 16) || !aligned(x_scale, 4))
+        return QL_ERR_ALIGN;
+    return QL_OK;
+}
+
+ql_status rms_norm_quantize_int8(const void* x, ql_dtype x_dtype, const void* residual, ql_dtype res_dtype,
+                                 const float* gamma, float eps, int64_t M, int64_t K, void* res_out,
+                                 int8_t* xq, float* x_scale, void* stream) {
+    ql_status st = check_rms_norm(x, x_dtype, residual, res_dtype, gamma, eps, M, K, res_out, xq, x_scale);
+    if (st != QL_OK || M == 0)
+        return st;
+    return ql::launch_rms_norm_quant(x, x_dtype == QL_F16, residual, res_dtype == QL_F16, gamma, eps, M, K,
+                                     res_out, xq, false, x_scale, as_stream(stream));
+}
+
+ql_status rms_norm_quantize_e4m3(const void* x, ql_dtype x_dtype, const void* residual, ql_dtype res_dtype,
+                                 const float* gamma, float eps, int64_t M, int64_t K, void* res_out,
+                                 uint8_t* xq, float* x_scale, void* stream) {
+    ql_status st = check_rms_norm(x, x_dtype, residual, res_dtype, gamma, eps, M, K, res_out, xq, x_scale);
+    if (st != QL_OK || M == 0)
+        return st;
+    return ql::launch_rms_norm_quant(x, x_dtype == QL_F16, residual, res_dtype == QL_F16, gamma, eps, M, K,
+                                     res_out, xq, true, x_scale, as_stream(stream));
+}
+
+// Sizes that the three calls on the 4-bit cache share. Rows and heads are passed to kernels as
+// int, and rows * kv_heads (at most 2^30, as rows * q_heads) sizes grids.
+static bool bad_kv4(int64_t rows, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D, int64_t group,
+                    int64_t table_width, int64_t batch) {
+    return rows < 0 || rows > (1 << 24) || num_pages < 0 || num_pages >= kMaxDim || page_size < 16 ||
+           page_size > 4096 || (page_size & (page_size - 1)) != 0 || kv_heads < 1 || kv_heads > 4096 ||
+           (D != 64 && D != 128 && D != 256) || (group != 32 && group != 64 && group != 128) || group > D ||
+           table_width < 0 || table_width >= kMaxDim || table_width * page_size >= kMaxDim || batch < 0 ||
+           batch > (1 << 20) || rows * kv_heads > ((int64_t)1 << 30) || (rows > 0 && (batch == 0 || num_pages == 0));
+}
+
+static ql::Kv4Cache kv4_cache(const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
+                              int64_t group) {
+    return {const_cast<uint8_t*>(cache), page_size * (D + 8 * (D / group)), (int)num_pages, (int)kv_heads,
+            __builtin_ctzll((unsigned long long)page_size)};
+}
+
+static ql::Kv4Batch kv4_batch(const int32_t* table, int64_t width, const int32_t* lens, const int32_t* starts,
+                              int64_t batch) {
+    return {table, lens, starts, (int)batch, (int)width};
+}
+
+static ql_status check_kv4_arrays(const uint8_t* cache, const int32_t* table, int64_t width, const int32_t* lens,
+                                  const int32_t* starts) {
+    if (!cache || (width > 0 && !table) || !lens || !starts)
+        return QL_ERR_NULL;
+    if (!aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4))
+        return QL_ERR_ALIGN;
+    return QL_OK;
+}
+
+ql_status kv4_append(const void* k, const void* v, ql_dtype dtype, int64_t k_stride, int64_t v_stride,
+                     int64_t rows, uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads,
+                     int64_t D, int64_t group, const int32_t* block_table, int64_t table_width,
+                     const int32_t* seq_lens, const int32_t* starts, int64_t batch, void* stream) {
+    if (dtype != QL_F32 && dtype != QL_F16)
+        return QL_ERR_DTYPE;
+    if (bad_kv4(rows, num_pages, page_size, kv_heads, D, group, table_width, batch) || k_stride < kv_heads * D ||
+        v_stride < kv_heads * D || k_stride >= kMaxDim || v_stride >= kMaxDim)
+        return QL_ERR_SHAPE;
+    if (rows == 0)
+        return QL_OK;
+    if (!k || !v)
+        return QL_ERR_NULL;
+    ql_status st = check_kv4_arrays(cache, block_table, table_width, seq_lens, starts);
+    if (st != QL_OK)
+        return st;
+    const int64_t unit = dtype == QL_F16 ? 8 : 4;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % unit != 0 || v_stride % unit != 0)
+        return QL_ERR_ALIGN;
+    return ql::launch_kv4_append(k, v, dtype == QL_F16, k_stride, v_stride, rows,
+                                 kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
+                                 kv4_batch(block_table, table_width, seq_lens, starts, batch), as_stream(stream));
+}
+
+ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
+                   int64_t group, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                   const int32_t* starts, int64_t batch, int64_t rows, ql_dtype dtype, void* k_out,
+                   void* v_out, void* stream) {
+    if (dtype != QL_F32 && dtype != QL_F16)
+        return QL_ERR_DTYPE;
+    if (bad_kv4(rows, num_pages, page_size, kv_heads, D, group, table_width, batch))
+        return QL_ERR_SHAPE;
+    if (rows == 0)
+        return QL_OK;
+    if (!k_out || !v_out)
+        return QL_ERR_NULL;
+    ql_status st = check_kv4_arrays(cache, block_table, table_width, seq_lens, starts);
+    if (st != QL_OK)
+        return st;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16))
+        return QL_ERR_ALIGN;
+    return ql::launch_kv4_read(kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
+                               kv4_batch(block_table, table_width, seq_lens, starts, batch), rows, k_out, v_out,
+                               dtype == QL_F16, as_stream(stream));
+}
+
+static bool bad_kv4_attention(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t max_q, int64_t max_len) {
+    return q_heads < 1 || q_heads > 4096 || kv_heads < 1 || q_heads % kv_heads != 0 || rows < 0 ||
+           rows > (1 << 24) || rows * q_heads > ((int64_t)1 << 30) || max_q < 1 || max_q >= kMaxDim || max_len < 1 ||
+           max_len >= kMaxDim;
+}
+
+ql_status attention_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t batch,
+                                        int64_t max_q, int64_t max_len, int64_t* bytes) {
+    if (bad_kv4_attention(rows, q_heads, kv_heads, max_q, max_len) || (D != 64 && D != 128 && D != 256) || batch < 0 ||
+        batch > (1 << 20))
+        return QL_ERR_SHAPE;
+    if (!bytes)
+        return QL_ERR_NULL;
+    *bytes = 4 * ql::attention_kv4_workspace(rows, (int)q_heads, (int)kv_heads, (int)D, (int)batch, (int)max_q,
+                                             (int)max_len);
+    return QL_OK;
+}
+
+ql_status attention_kv4(const void* q, int64_t q_stride, void* out, int64_t rows, int64_t q_heads,
+                        const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads,
+                        int64_t D, int64_t group, const int32_t* block_table, int64_t table_width,
+                        const int32_t* seq_lens, const int32_t* starts, int64_t batch, int64_t max_q,
+                        int64_t max_len, float scale, int64_t window, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+    if (bad_kv4(rows, num_pages, page_size, kv_heads, D, group, table_width, batch) ||
+        bad_kv4_attention(rows, q_heads, kv_heads, max_q, max_len) || q_stride < q_heads * D || q_stride >= kMaxDim ||
+        !std::isfinite(scale) || window < 0 || window >= kMaxDim || workspace_bytes < 0)
+        return QL_ERR_SHAPE;
+    if (rows == 0)
+        return QL_OK;
+    if (workspace_bytes < 4 * ql::attention_kv4_workspace(rows, (int)q_heads, (int)kv_heads, (int)D, (int)batch,
+                                                          (int)max_q, (int)max_len))
+        return QL_ERR_SHAPE;
+    if (!q || !out || (workspace_bytes > 0 && !workspace))
+        return QL_ERR_NULL;
+    ql_status st = check_kv4_arrays(cache, block_table, table_width, seq_lens, starts);
+    if (st != QL_OK)
+        return st;
+    if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(workspace, 16))
+        return QL_ERR_ALIGN;
+    ql::Kv4Attn a = {};
+    a.q = reinterpret_cast<const _Float16*>(q);
+    a.q_stride = q_stride;
+    a.out = reinterpret_cast<_Float16*>(out);
+    a.rows = (int)rows;
+    a.q_heads = (int)q_heads;
+    a.max_q = (int)max_q;
+    a.max_len = (int)max_len;
+    a.scale = scale;
+    a.window = (int)window;
+    a.ws = reinterpret_cast<float*>(workspace);
+    a.ws_floats = workspace_bytes / 4;
+    return ql::launch_attention_kv4(a, kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
+                                    kv4_batch(block_table, table_width, seq_lens, starts, batch), as_stream(stream));
 }
 
 }  // extern "C"

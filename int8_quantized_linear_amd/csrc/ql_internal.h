@@ -92,6 +92,9 @@ ql_status launch_gemm_w8a8_mid(const int8_t* xq, const float* x_scale, const int
                                const float* x_zero, const int32_t* colsum, const float* out_scale,
                                int out_scale_n, int64_t M, int64_t N, int64_t K, hipStream_t stream,
                                bool e4m3 = false);
+ql_status launch_rms_norm_quant(const void* x, bool x_f16, const void* residual, bool res_f16, const float* gamma,
+                                float eps, int64_t M, int64_t K, void* res_out, void* q, bool e4m3, float* scale,
+                                hipStream_t stream);
 ql_status launch_wonly(const void* x, const void* codes, int fmt, const void* scale,
                        const uint8_t* zp, int64_t group, const float* bias, void* y, int64_t M,
                        int64_t N, int64_t K, int act, hipStream_t stream);

@@ -13,6 +13,7 @@
 //   absmax along the row, clamp_min(1e-10), torch.round (half to even)
 //       hotelren.com "量化算法的本质", per_channel_quant_int8
 #include "ql_internal.h"
+#include "quant_codes.h"
 
 namespace ql {
 namespace {
@@ -38,20 +39,6 @@ __device__ inline float block_max(float v, float* red) {
     for (int i = 1; i < QT / WAVE; ++i)
         r = fmaxf(r, red[i]);
     return r;
-}
-
-// rint(x / s) clamped to [-127, 127], as (code + 128) in the byte `sel` of `acc`.
-// x / s is taken as q0 = RN(x * y), r = x - q0 * s (exact, one fma), RN(q0 + r * y) with
-// y = RN(1 / s) divided once per row: Markstein's theorem on division through a correctly
-// rounded reciprocal makes that the correctly rounded quotient (a zero may change sign,
-// which no code sees), so the code is the one the IEEE quotient gives, at three
-// operations instead of a full division.
-__device__ inline uint32_t code_u8_biased(float x, float s, float y, uint32_t sel, uint32_t acc) {
-    const float q0 = __fmul_rn(x, y);
-    const float r = fmaf(-q0, s, x);
-    const float q = rintf(fmaf(r, y, q0));
-    const float c = __builtin_amdgcn_fmed3f(q, -127.0f, 127.0f) + 128.0f;
-    return __builtin_amdgcn_cvt_pk_u8_f32(c, sel, acc);
 }
 
 // Asymmetric: rint(x / s + z) clamped to [-128, 127], as (code + 128) in the byte `sel` of
@@ -120,32 +107,6 @@ struct Chunk {
             hi = fmaxf(hi, v[i]);
         }
     }
-    // fp8 (OCP E4M3) codes: the correctly rounded quotient (as code_u8_biased), kept within
-    // +-448 (it cannot pass it: s = absmax / 448), then v_cvt_pk_fp8_f32, which rounds to
-    // nearest even into E4M3 (gfx950 converts to the OCP format).
-    __device__ inline void store_codes_e4m3(uint8_t* q, float s, float y) const {
-        uint32_t w[E / 4];
-#pragma unroll
-        for (int j = 0; j < E / 4; ++j) {
-            float t[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = v[4 * j + i];
-                const float q0 = __fmul_rn(x, y);
-                const float r = fmaf(-q0, s, x);
-                // s > 0, so the quotient has x's sign; the refinement alone would turn
-                // x = -0 into +0 (r = +0 + -0), and fp8 keeps the sign of zero.
-                t[i] = __builtin_amdgcn_fmed3f(copysignf(fmaf(r, y, q0), x), -448.0f, 448.0f);
-            }
-            int b = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-            b = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], b, true);
-            w[j] = (uint32_t)b;
-        }
-        if constexpr (E == 8)
-            *reinterpret_cast<u32x2*>(q) = u32x2{w[0], w[1]};
-        else
-            *reinterpret_cast<uint32_t*>(q) = w[0];
-    }
     // Asymmetric codes; y = 1 / s correctly rounded, z the row's zero point.
     __device__ inline void store_codes_asym(int8_t* q, float s, float y, float z) const {
         uint32_t w[E / 4];
@@ -156,22 +117,6 @@ struct Chunk {
             for (int i = 0; i < 4; ++i)
                 b = code_u8_asym(v[4 * j + i], s, y, z, i, b);
             w[j] = b ^ 0x80808080u;
-        }
-        if constexpr (E == 8)
-            *reinterpret_cast<u32x2*>(q) = u32x2{w[0], w[1]};
-        else
-            *reinterpret_cast<uint32_t*>(q) = w[0];
-    }
-    // y = 1 / s, correctly rounded.
-    __device__ inline void store_codes(int8_t* q, float s, float y) const {
-        uint32_t w[E / 4];
-#pragma unroll
-        for (int j = 0; j < E / 4; ++j) {
-            uint32_t b = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                b = code_u8_biased(v[4 * j + i], s, y, i, b);
-            w[j] = b ^ 0x80808080u;   // code + 128 -> two's complement code
         }
         if constexpr (E == 8)
             *reinterpret_cast<u32x2*>(q) = u32x2{w[0], w[1]};
@@ -189,14 +134,14 @@ template <bool F16, bool E4M3, int QMAXC>
 __global__ __launch_bounds__(QT) void quant_rows_i8_kernel(const void* __restrict__ x, int64_t K,
                                                           int8_t* __restrict__ q,
                                                           float* __restrict__ scale) {
+    using C = Chunk<F16>;
     constexpr float QMAX = E4M3 ? 448.0f : 127.0f;
     auto codes = [&](const Chunk<F16>& c, int8_t* dst, float s, float y) {
         if constexpr (E4M3)
-            c.store_codes_e4m3(reinterpret_cast<uint8_t*>(dst), s, y);
+            store_codes_e4m3<C::E>(reinterpret_cast<uint8_t*>(dst), c.v, s, y);
         else
-            c.store_codes(dst, s, y);
+            store_codes_i8<C::E>(dst, c.v, s, y);
     };
-    using C = Chunk<F16>;
     __shared__ float red[QT / WAVE];
     const int64_t row = blockIdx.x;
     const char* xr = reinterpret_cast<const char*>(x) + row * K * (F16 ? 2 : 4);
@@ -307,7 +252,7 @@ __global__ __launch_bounds__(QT) void tensor_codes_kernel(const void* __restrict
 #pragma unroll
         for (int i = 0; i < TCH; ++i)
             if (base + i * QT < nch)
-                c[i].store_codes(q + (base + i * QT) * C::E, s, y);
+                store_codes_i8<C::E>(q + (base + i * QT) * C::E, c[i].v, s, y);
     }
 }
 
