@@ -4,99 +4,534 @@
 //   max(0, p - window + 1) <= j <= p for a row at position p (from 0 without a window)
 //
 // in one pass with a running maximum and sum. A row that sees nothing gives zeros.
+//
+// Decode kernel (few rows of a sequence): bound by reading the cache. The rows of one sequence
+// that share a kv head, (row, head) pairs in order, make tiles of 16 columns. A workgroup of four
+// waves takes one tile and one stretch of the sequence; each wave steps through every fourth
+// block of 32 tokens on its own (no barrier in the loop), and the four partial results are
+// joined through LDS at the end, the stretches' by a second kernel.
+//   S^T = K Q^T   16x16x32 fp16: rows are tokens, columns the tile's rows. K's codes enter as
+//                 fp16 integers (the masked nibbles are fp16 subnormals c 2^-24 or 16 c 2^-24,
+//                 which the matrix cores take exactly; q's slots carry the 1/16), one product
+//                 for each group of G values, and scale and low are applied to the fp32 product:
+//                 s_t sum_d c q_d + low_t sum_d q_d.
+//   O^T = V^T P^T the products' layout hands each lane the weights of 8 consecutive tokens for
+//                 one column, which is the layout of the next product's operand: P never
+//                 crosses lanes. V becomes fp16 values scale * code + low (one rounding), since
+//                 its scales lie along the summed axis; folding them into P would tie P's fp16
+//                 range to V's magnitude.
+// The running maximum is raised only when a score exceeds it by 2^8 (weights up to 2^14, sums
+// in fp32), so most steps have neither a reduction across lanes nor a rescaling of O.
 #include "kv4.h"
 
 namespace ql {
 namespace {
 
-constexpr int AT = 256;   // threads per workgroup, tokens per step
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+constexpr int AT = 256, AW = AT / WAVE;   // threads and waves of a decode workgroup
+constexpr int TB = 32;                    // tokens of a step
+constexpr float M_NONE = -1e30f;          // running maximum before the first score
+constexpr float P_SHIFT = 6.0f;           // weights are 2^(score - max + P_SHIFT)
+constexpr float M_SLACK = 8.0f;           // and may exceed 2^P_SHIFT by 2^M_SLACK before a rescale
+
+__device__ inline f16x2 as_f16x2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
+__device__ inline uint32_t as_u32(f16x2 h) { return __builtin_bit_cast(uint32_t, h); }
+
+// The page table is not written while a kernel runs: scalar loads.
+__device__ inline uint32_t table_entry(const int32_t* p) {
+    return (uint32_t)*(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
+}
+
+// Rows that one workgroup handles and the positions that they see.
+struct RowTile {
+    int first;       // position of the sequence's row 0
+    int rows;        // the sequence's rows
+    int begin, end;  // positions that any of the tile's rows sees
+    int all_begin, all_end;   // positions that all of them see
+};
+
+__device__ inline RowTile row_tile(const Kv4Batch& b, const Kv4Cache& c, int seq, int tile, int per, int R, int window) {
+    RowTile t;
+    const int len = kv4_len(b, c, seq);
+    t.rows = b.starts[seq + 1] - b.starts[seq];
+    t.first = len - t.rows;
+    const int i0 = tile * per / R, i1 = min((tile * per + per - 1) / R, t.rows - 1);
+    t.end = max(0, t.first + i1 + 1);
+    t.all_end = max(0, t.first + i0 + 1);
+    const int seen = max(i0, -t.first);   // the first row with a position
+    t.begin = window ? max(0, t.first + seen + 1 - window) : 0;
+    t.all_begin = window ? max(0, t.first + i1 + 1 - window) : 0;
+    return t;
+}
+
+// Tokens of one split: the launch's stretch, or more where the splits would not reach the end.
+__device__ inline int split_tokens(const RowTile& t, int stretch, int nsplit) {
+    const int base = t.begin & ~(TB - 1);
+    const int need = (t.end - base + nsplit - 1) / nsplit;
+    return max(stretch, (need + TB * AW - 1) & ~(TB * AW - 1));
+}
+
+struct Split {
+    int n, stretch;   // splits, and tokens of each at the launch's max_len
+    int tiles;        // row tiles a sequence and kv head at the launch's max_q
+};
+
+// A step's cache data for one lane: lane (m = lane & 15, kg = lane >> 4) holds K's words of
+// tokens 8 (m / 4) + m % 4 (+ 4 for the second half of the block) and d = 32 i + 8 kg .., V's
+// words of tokens 8 kg .. 8 kg + 7 and quad m of each chunk, and the scales and lows of those
+// 8 tokens, in pairs.
 template <int D, int G>
-__global__ __launch_bounds__(AT) void attention_kv4_row_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b) {
-    using L = Kv4Layout<D, G>;
-    constexpr int PARTS = AT / D;   // parts of a step's tokens, each summed by D threads
-    __shared__ float qs[D], prob[AT], red[AT / WAVE], part[AT];
-    const int P = 1 << c.page_log2, tid = threadIdx.x;
-    const int row = blockIdx.x / a.q_heads, qh = blockIdx.x % a.q_heads;
-    const int head = qh / (a.q_heads / c.heads);
-    const int seq = kv4_seq(b, row), len = kv4_len(b, c, seq), pos = kv4_pos(b, seq, len, row);
-    const int end = pos >= len ? 0 : pos + 1;
-    const int begin = a.window && end > a.window ? end - a.window : 0;
+struct Block {
+    static constexpr int NG = D / G, NI = D / 32, NC = D / 64;
+    uint32_t k[2][NI];
+    u32x4 v[NC];
+    u32x4 ks[NG], kl[NG], vs[NG], vl[NG];
+};
 
-    if (tid < D)
-        qs[tid] = (float)a.q[row * a.q_stride + (int64_t)qh * D + tid];
-    __syncthreads();
-    float m = -INFINITY, sum = 0.0f, acc = 0.0f;
-    for (int j0 = begin; j0 < end; j0 += AT) {
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        if (j < end) {
-            const uint8_t* page = kv4_page(b, c, seq, j, head);
-            const int slot = j & (P - 1);
-            const uint32_t* kw = reinterpret_cast<const uint32_t*>(page + L::k_codes(slot));
-            float dot = 0.0f;
-            for (int g = 0; g < L::NG; ++g) {
-                float qc = 0.0f, q1 = 0.0f;
-                for (int d = g * G; d < g * G + G; d += 8) {
-                    const uint32_t w = kw[((d % 32) / 8) * (D / 32) + d / 32];
+template <int D, int G, bool BIG>
+struct Loader {
+    using L = Kv4Layout<D, G>;
+    using B = Block<D, G>;
+    const int32_t* table;
+    uint8_t* data;
+    int64_t head_bytes;
+    int64_t head_off;
+    int heads, pages, log2p, last;
+    int k_off, v_off, p_off;
+    bool k_hi, v_hi;
+
+    __device__ inline void init(const Kv4Batch& b, const Kv4Cache& c, int seq, int head, int end) {
+        table = b.table + (int64_t)seq * b.width;
+        data = c.data;
+        head_bytes = c.head_bytes;
+        head_off = head * c.head_bytes;
+        heads = c.heads;
+        pages = c.pages;
+        log2p = c.page_log2;
+        last = end - 1;
+        const int lane = threadIdx.x & (WAVE - 1), m = lane & 15, kg = lane >> 4, P = 1 << log2p;
+        // with pages of 16 tokens the upper two groups of 8 lie in a second page
+        const int kx = BIG ? m >> 2 : (m >> 2) & 1, vx = BIG ? kg : kg & 1;
+        k_hi = !BIG && (m >> 3);
+        v_hi = !BIG && (kg >> 1);
+        k_off = (kx * 8 + (m & 3)) * (D / 2) + kg * (D / 8);
+        v_off = L::v_codes(P, 0) + vx * 4 * D + m * 16;
+        p_off = vx * 16;
+    }
+    __device__ inline const uint8_t* page(int pos) const {
+        uint32_t p = table_entry(table + (min(pos, last) >> log2p));
+        p = p < (uint32_t)pages ? p : (uint32_t)pages - 1;
+        return data + (int64_t)p * (heads * head_bytes) + head_off;
+    }
+    __device__ inline void load(B& x, int t0) const {
+        const int P = 1 << log2p, slot = t0 & (P - 1);
+        const uint8_t* pa = page(t0);
+        const uint8_t *pk = pa, *pv = pa;
+        if constexpr (!BIG) {
+            const uint8_t* pb = page(t0 + 16);
+            pk = k_hi ? pb : pa;
+            pv = v_hi ? pb : pa;
+        }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        qc = fmaf(qs[d + e], (float)((w >> (16 * (e & 1) + 4 * (e >> 1))) & 15), qc);
-                        q1 += qs[d + e];
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* p = pk + (slot * (D / 2) + k_off + h * 4 * (D / 2));
+            if constexpr (D == 64) {
+                *reinterpret_cast<u32x2*>(x.k[h]) = *reinterpret_cast<const u32x2*>(p);
+            } else {
+#pragma unroll
+                for (int i = 0; i < B::NI; i += 4)
+                    *reinterpret_cast<u32x4*>(x.k[h] + i) = *reinterpret_cast<const u32x4*>(p + 4 * i);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < B::NC; ++c)
+            x.v[c] = *reinterpret_cast<const u32x4*>(pv + (slot * (D / 2) + v_off + c * 256));
+        const uint8_t* pp = pv + (2 * slot + p_off);
+#pragma unroll
+        for (int g = 0; g < B::NG; ++g) {
+            x.ks[g] = *reinterpret_cast<const u32x4*>(pp + L::k_scale(P, g));
+            x.kl[g] = *reinterpret_cast<const u32x4*>(pp + L::k_low(P, g));
+            x.vs[g] = *reinterpret_cast<const u32x4*>(pp + L::v_scale(P, g));
+            x.vl[g] = *reinterpret_cast<const u32x4*>(pp + L::v_low(P, g));
+        }
+    }
+};
+
+// fp16 subnormals of 8 codes, slots in d order: (0, 1) c, (2, 3) 16 c, (4, 5) c, (6, 7) 16 c.
+__device__ inline f16x8 codes_raw(uint32_t w) {
+    const uint32_t h = w >> 8;
+    const u32x4 r = {w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
+    return __builtin_bit_cast(f16x8, r);
+}
+
+// Codes of nibble JJ of each half as fp16 integers: 1024 + c (or 1024 + 16 c) is exact.
+template <int JJ>
+__device__ inline f16x2 codes_int(uint32_t w) {
+    const uint32_t h = JJ & 2 ? w >> 8 : w;
+    if constexpr (JJ & 1)
+        return as_f16x2((h & 0x00F000F0u) | 0x64006400u) * (f16x2){(_Float16)0.0625f, (_Float16)0.0625f} -
+               (f16x2){(_Float16)64.0f, (_Float16)64.0f};
+    else
+        return as_f16x2((h & 0x000F000Fu) | 0x64006400u) - (f16x2){(_Float16)1024.0f, (_Float16)1024.0f};
+}
+
+// V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16.
+template <int JJ>
+__device__ inline f16x8 v_values(u32x4 w, u32x4 s, u32x4 l) {
+    u32x4 r;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        r[p] = as_u32(__builtin_elementwise_fma(codes_int<JJ>(w[p]), as_f16x2(s[p]), as_f16x2(l[p])));
+    return __builtin_bit_cast(f16x8, r);
+}
+
+__device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2])[i & 1]; }
+
+template <int D, int G, bool BIG, int NQ>
+__global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_decode_kernel(Kv4Attn a, Kv4Cache c,
+                                                                                           Kv4Batch b, Split sp) {
+    using B = Block<D, G>;
+    constexpr int NG = B::NG, NI = B::NI, NC = B::NC, PER = 16 * NQ;
+    __shared__ float part[AW][16][D + 4];
+    __shared__ float stats[AW][16][2];
+    const int R = a.q_heads / c.heads;
+    int id = blockIdx.x;
+    const int head = id % c.heads;
+    id /= c.heads;
+    const int seq = id % b.batch;
+    id /= b.batch;
+    const int split = id % sp.n;
+    const int tile0 = id / sp.n;
+    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, n = lane & 15, kg = lane >> 4;
+    const float kappa = fabsf(a.scale) * 1.44269504088896f * 16777216.0f;   // the codes' 2^-24 taken out
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+
+    for (int tile = tile0;; tile += sp.tiles) {
+        const RowTile t = row_tile(b, c, seq, tile, PER, R, a.window);
+        if (tile * PER >= t.rows * R)
+            return;
+        const int base = t.begin & ~(TB - 1);
+        const int stretch = split_tokens(t, sp.stretch, sp.n);
+        const int from = base + split * stretch, to = min(from + stretch, t.end);
+        if (split > 0 && from >= t.end)
+            continue;   // no tokens; split 0 always writes
+
+        // Q's operand: column n of each row tile, slots 2, 3, 6, 7 of every 8 divided by 16
+        f16x8 q[NQ][NI];
+        float qsum[NQ][NG];
+        int rbeg[NQ], rend[NQ];
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+            const int idx = tile * PER + u * 16 + n, i = idx / R, row = b.starts[seq] + i;
+            const bool ok = i < t.rows && row < a.rows;
+            rend[u] = ok ? max(0, t.first + i + 1) : 0;
+            rbeg[u] = a.window ? max(0, rend[u] - a.window) : 0;
+            const _Float16* src = a.q + (int64_t)(ok ? row : 0) * a.q_stride + (int64_t)(head * R + idx % R) * D + kg * 8;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                qsum[u][g] = 0.0f;
+#pragma unroll
+            for (int i8 = 0; i8 < NI; ++i8) {
+                f16x8 x = {};
+                if (ok)
+                    x = *reinterpret_cast<const f16x8*>(src + 32 * i8);
+                float s = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s += (float)x[e];
+                    x[e] *= (_Float16)(e & 2 ? sign * 0.0625f : sign);
+                }
+                q[u][i8] = x;
+                qsum[u][i8 / (G / 32)] += s;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                qsum[u][g] += __shfl_xor(qsum[u][g], 16, WAVE);
+                qsum[u][g] += __shfl_xor(qsum[u][g], 32, WAVE);
+                qsum[u][g] *= sign * 5.9604644775390625e-08f;   // 2^-24
+            }
+        }
+
+        f32x4 o[NQ][D / 16], l[NQ];
+        float m[NQ];
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                o[u][i] = f32x4{0, 0, 0, 0};
+            l[u] = f32x4{0, 0, 0, 0};
+            m[u] = M_NONE;
+        }
+        const _Float16 one = (_Float16)1.0f;
+        const f16x8 ones = {one, one, one, one, one, one, one, one};
+
+        auto step = [&](B& x, int t0) {
+            const bool edge = t0 < t.all_begin || t0 + TB > t.all_end;   // some row does not see all of it
+            if (t0 < t.begin || t0 + TB > t.end) {
+                // what lies at positions that no row sees may be anything: a weight of 0 must
+                // not meet an infinite or NaN value
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int j = t0 + kg * 8 + 2 * p;
+                    const uint32_t keep = (j >= t.begin && j < t.end ? 0xFFFFu : 0u) |
+                                          (j + 1 >= t.begin && j + 1 < t.end ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        x.vs[g][p] &= keep;
+                        x.vl[g][p] &= keep;
                     }
                 }
-                dot = fmaf((float)reinterpret_cast<const _Float16*>(page + L::k_scale(P, g))[slot], qc, dot);
-                dot = fmaf((float)reinterpret_cast<const _Float16*>(page + L::k_low(P, g))[slot], q1, dot);
             }
-            s = dot * a.scale;
+            f32x4 s[NQ][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    f32x4 acc[NQ];
+#pragma unroll
+                    for (int u = 0; u < NQ; ++u)
+                        acc[u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = g * (G / 32); i < (g + 1) * (G / 32); ++i) {
+                        const f16x8 kc = codes_raw(x.k[h][i]);
+#pragma unroll
+                        for (int u = 0; u < NQ; ++u)
+                            acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kc, q[u][i], acc[u], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int u = 0; u < NQ; ++u)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float low = half_of(x.kl[g], 4 * h + r), sc = half_of(x.ks[g], 4 * h + r);
+                            s[u][h][r] = fmaf(low, qsum[u][g], g ? s[u][h][r] : 0.0f);
+                            s[u][h][r] = fmaf(sc, acc[u][r], s[u][h][r]);
+                        }
+                }
+            f16x8 p[NQ];
+#pragma unroll
+            for (int u = 0; u < NQ; ++u) {
+                bool see[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = t0 + kg * 8 + 4 * h + r;
+                        see[h][r] = !edge || (j >= rbeg[u] && j < rend[u]);
+                        if (edge && !see[h][r])
+                            s[u][h][r] = -3.0e38f;
+                    }
+                float top = s[u][0][0];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        top = fmaxf(top, s[u][h][r]);
+                top *= kappa;
+                if (__any(top > m[u] + M_SLACK)) {
+                    top = fmaxf(top, __shfl_xor(top, 16, WAVE));
+                    top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+                    const float mn = fmaxf(m[u], top);
+                    const float f = __builtin_amdgcn_exp2f(m[u] - mn);
+                    m[u] = mn;
+                    l[u][0] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        o[u][i] *= f;
+                }
+                const float shift = P_SHIFT - m[u];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float w = __builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa, shift));
+                        if (edge)
+                            w = see[h][r] ? w : 0.0f;
+                        p[u][4 * h + r] = (_Float16)w;
+                    }
+                // the sum of the rounded weights, so that their rounding cancels in the quotient
+                l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u], l[u], 0, 0, 0);
+            }
+            auto add = [&](auto jj, int ch) {
+                constexpr int JJ = decltype(jj)::value;
+                const int g = (64 * ch + 32 * (JJ / 2)) / G;
+                const f16x8 vv = v_values<JJ>(x.v[ch], x.vs[g], x.vl[g]);
+#pragma unroll
+                for (int u = 0; u < NQ; ++u)
+                    o[u][4 * ch + JJ] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[u], o[u][4 * ch + JJ], 0, 0, 0);
+            };
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) {
+                add(std::integral_constant<int, 0>{}, ch);
+                add(std::integral_constant<int, 1>{}, ch);
+                add(std::integral_constant<int, 2>{}, ch);
+                add(std::integral_constant<int, 3>{}, ch);
+            }
+        };
+
+        Loader<D, G, BIG> ld;
+        ld.init(b, c, seq, head, t.end);
+        int t0 = from + wave * TB;
+        if (t0 < to) {
+            B x, y;
+            ld.load(x, t0);
+            while (true) {
+                const bool more = t0 + AW * TB < to;
+                if (more)
+                    ld.load(y, t0 + AW * TB);
+                step(x, t0);
+                t0 += AW * TB;
+                if (!more)
+                    break;
+                x = y;
+            }
         }
-        float top = s;
-        for (int o = WAVE / 2; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor(top, o, WAVE));
-        __syncthreads();
-        if ((tid & (WAVE - 1)) == 0)
-            red[tid / WAVE] = top;
-        __syncthreads();
-        float mn = m;
-        for (int i = 0; i < AT / WAVE; ++i)
-            mn = fmaxf(mn, red[i]);
-        const float keep = __expf(m - mn);   // 0 at the first step (m = -inf, mn finite)
-        prob[tid] = __expf(s - mn);
-        m = mn;
-        __syncthreads();
-        sum *= keep;
-        acc *= keep;
-        const int d = tid % D, n = min(AT, end - j0);
-        const int g = d / G, quad = (d / 64) * 16 + (d % 32) / 2;
-        for (int i = 0; i < n; ++i)
-            sum += prob[i];
-        for (int i = tid / D; i < n; i += PARTS) {
-            const uint8_t* page = kv4_page(b, c, seq, j0 + i, head);
-            const int slot = (j0 + i) & (P - 1);
-            const uint32_t byte = page[L::v_codes(P, slot / 8) + quad * 16 + (slot % 8) * 2 + (d % 64) / 32];
-            const float vs = (float)reinterpret_cast<const _Float16*>(page + L::v_scale(P, g))[slot];
-            const float vl = (float)reinterpret_cast<const _Float16*>(page + L::v_low(P, g))[slot];
-            acc = fmaf(prob[i], fmaf(vs, (float)((byte >> (4 * (d & 1))) & 15), vl), acc);
+
+        // join the waves: each brings its O to the largest maximum
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+            __syncthreads();
+            if (kg == 0) {
+                stats[wave][n][0] = m[u];
+                stats[wave][n][1] = l[u][0];
+            }
+            __syncthreads();
+            float top = stats[0][n][0];
+#pragma unroll
+            for (int w = 1; w < AW; ++w)
+                top = fmaxf(top, stats[w][n][0]);
+            const float f = __builtin_amdgcn_exp2f(m[u] - top);
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        part[wave][n][ch * 64 + (jj >> 1) * 32 + kg * 8 + 2 * r + (jj & 1)] = o[u][4 * ch + jj][r] * f;
+            __syncthreads();
+            constexpr int E = D / 16;   // values of one thread: row tid / 16, E neighbouring d
+            const int rr = threadIdx.x / 16, d0 = (threadIdx.x % 16) * E;
+            const int idx = tile * PER + u * 16 + rr, i = idx / R, row = b.starts[seq] + i;
+            if (i < t.rows && row < a.rows) {
+                float mx = stats[0][rr][0], sum = 0.0f, v[E];
+#pragma unroll
+                for (int w = 1; w < AW; ++w)
+                    mx = fmaxf(mx, stats[w][rr][0]);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    v[e] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < AW; ++w) {
+                    sum += stats[w][rr][1] * __builtin_amdgcn_exp2f(stats[w][rr][0] - mx);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        v[e] += part[w][rr][d0 + e];
+                }
+                const int64_t at = (int64_t)row * a.q_heads + head * R + idx % R;
+                if (sp.n == 1) {
+                    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        a.out[at * D + d0 + e] = (_Float16)(v[e] * inv);
+                } else {
+                    float* ws = a.ws + ((int64_t)split * a.rows * a.q_heads + at) * D + d0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        ws[e] = v[e];
+                    if (threadIdx.x % 16 == 0) {
+                        float* st = a.ws + (int64_t)sp.n * a.rows * a.q_heads * D +
+                                    ((int64_t)split * a.rows * a.q_heads + at) * 2;
+                        st[0] = mx;
+                        st[1] = sum;
+                    }
+                }
+            }
         }
     }
-    part[tid] = acc;
+}
+
+// Joins the splits of one (row, head): their maxima and sums first, then D values by 256 / (D / 4)
+// parts of the splits.
+template <int D>
+__global__ __launch_bounds__(AT) void attention_kv4_join_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b, Split sp, int per) {
+    constexpr int LANES = D / 4, PARTS = AT / LANES;
+    __shared__ f32x4 part[PARTS][LANES];
+    const int R = a.q_heads / c.heads;
+    const int64_t at = blockIdx.x, all = (int64_t)a.rows * a.q_heads;
+    const int row = (int)(at / a.q_heads), h = (int)(at % a.q_heads);
+    const int seq = kv4_seq(b, row), i = row - b.starts[seq];
+    const RowTile t = row_tile(b, c, seq, (i * R + h % R) / per, per, R, a.window);
+    const int used = max(1, min(sp.n, (t.end - (t.begin & ~(TB - 1)) + split_tokens(t, sp.stretch, sp.n) - 1) /
+                                          split_tokens(t, sp.stretch, sp.n)));
+    const float* st = a.ws + sp.n * all * D + at * 2;
+    float top = M_NONE, sum = 0.0f;
+    for (int s = 0; s < used; ++s)
+        top = fmaxf(top, st[s * all * 2]);
+    const int d4 = threadIdx.x % LANES, p = threadIdx.x / LANES;
+    f32x4 v = {0, 0, 0, 0};
+    for (int s = 0; s < used; ++s)
+        sum += st[s * all * 2 + 1] * __builtin_amdgcn_exp2f(st[s * all * 2] - top);
+    for (int s = p; s < used; s += PARTS) {
+        const float f = __builtin_amdgcn_exp2f(st[s * all * 2] - top);
+        v += *reinterpret_cast<const f32x4*>(a.ws + (s * all + at) * D + 4 * d4) * f;
+    }
+    part[p][d4] = v;
     __syncthreads();
-    if (tid < D) {
-        for (int i = 1; i < PARTS; ++i)
-            acc += part[i * D + tid];
-        a.out[(int64_t)blockIdx.x * D + tid] = (_Float16)(end > begin ? acc / sum : 0.0f);
+    if (p == 0) {
+        for (int k = 1; k < PARTS; ++k)
+            v += part[k][d4];
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            a.out[at * D + 4 * d4 + e] = (_Float16)(v[e] * inv);
     }
+}
+
+// Rows of a tile: 16 columns, or 32 where a sequence has more.
+inline int rows_per_tile(int64_t pairs) { return pairs <= 16 ? 16 : 32; }
+
+// Splits: enough workgroups for every CU several times over, each with at least 512 tokens.
+Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len) {
+    const int64_t pairs = (int64_t)max_q * (q_heads / kv_heads);
+    Split s;
+    s.tiles = (int)((pairs + rows_per_tile(pairs) - 1) / rows_per_tile(pairs));
+    const int64_t base = (int64_t)batch * kv_heads * s.tiles;
+    const int64_t want = base > 0 ? (2048 + base - 1) / base : 1;
+    int64_t stretch = (max_len + want - 1) / want;
+    stretch = stretch < 512 ? 512 : (stretch + TB * AW - 1) / (TB * AW) * (TB * AW);
+    s.stretch = (int)stretch;
+    s.n = (int)((max_len + stretch - 1) / stretch);
+    return s;
 }
 
 }  // namespace
 
-int64_t attention_kv4_workspace(int64_t, int, int, int, int, int, int) { return 0; }
+int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len) {
+    const Split s = plan(q_heads, kv_heads, batch, max_q, max_len);
+    return s.n == 1 ? 0 : s.n * rows * q_heads * (D + 2);
+}
 
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream) {
+    const int per = rows_per_tile((int64_t)a.max_q * (a.q_heads / c.heads));
+    const Split sp = plan(a.q_heads, c.heads, b.batch, a.max_q, a.max_len);
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
-        attention_kv4_row_kernel<DD, GG><<<dim3((uint32_t)(a.rows * a.q_heads)), AT, 0, stream>>>(a, c, b);
+        const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * sp.n * sp.tiles));
+        auto go = [&](auto kernel) { kernel<<<grid, AT, 0, stream>>>(a, c, b, sp); };
+        if (per == 16) {
+            if (c.page_log2 >= 5)
+                go(attention_kv4_decode_kernel<DD, GG, true, 1>);
+            else
+                go(attention_kv4_decode_kernel<DD, GG, false, 1>);
+        } else {
+            if (c.page_log2 >= 5)
+                go(attention_kv4_decode_kernel<DD, GG, true, 2>);
+            else
+                go(attention_kv4_decode_kernel<DD, GG, false, 2>);
+        }
+        if (sp.n > 1)
+            attention_kv4_join_kernel<DD><<<dim3((uint32_t)(a.rows * a.q_heads)), AT, 0, stream>>>(a, c, b, sp, per);
         return launch_status();
     });
 }
