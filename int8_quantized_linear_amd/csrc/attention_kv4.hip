@@ -450,34 +450,62 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
     }
 }
 
-// Joins the splits of one (row, head): their maxima and sums first, then D values by 256 / (D / 4)
-// parts of the splits.
+// Joins the splits of one (row, head): their largest maximum and weights by all threads, then D
+// values by 256 / (D / 4) parts of the splits.
+constexpr int MAX_SPLITS = 256;
+
 template <int D>
 __global__ __launch_bounds__(AT) void attention_kv4_join_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b, Split sp, int per) {
     constexpr int LANES = D / 4, PARTS = AT / LANES;
     __shared__ f32x4 part[PARTS][LANES];
-    const int R = a.q_heads / c.heads;
+    __shared__ float weight[MAX_SPLITS], red[AW][2];
+    static_assert(MAX_SPLITS == AT, "one split a thread");
+    const int R = a.q_heads / c.heads, tid = threadIdx.x;
     const int64_t at = blockIdx.x, all = (int64_t)a.rows * a.q_heads;
     const int row = (int)(at / a.q_heads), h = (int)(at % a.q_heads);
     const int seq = kv4_seq(b, row), i = row - b.starts[seq];
     const RowTile t = row_tile(b, c, seq, (i * R + h % R) / per, per, R, a.window);
-    const int used = max(1, min(sp.n, (t.end - (t.begin & ~(TB - 1)) + split_tokens(t, sp.stretch, sp.n) - 1) /
-                                          split_tokens(t, sp.stretch, sp.n)));
+    const int stretch = split_tokens(t, sp.stretch, sp.n);
+    const int used = max(1, min(sp.n, (t.end - (t.begin & ~(TB - 1)) + stretch - 1) / stretch));
     const float* st = a.ws + sp.n * all * D + at * 2;
-    float top = M_NONE, sum = 0.0f;
-    for (int s = 0; s < used; ++s)
-        top = fmaxf(top, st[s * all * 2]);
-    const int d4 = threadIdx.x % LANES, p = threadIdx.x / LANES;
-    f32x4 v = {0, 0, 0, 0};
-    for (int s = 0; s < used; ++s)
-        sum += st[s * all * 2 + 1] * __builtin_amdgcn_exp2f(st[s * all * 2] - top);
-    for (int s = p; s < used; s += PARTS) {
-        const float f = __builtin_amdgcn_exp2f(st[s * all * 2] - top);
-        v += *reinterpret_cast<const f32x4*>(a.ws + (s * all + at) * D + 4 * d4) * f;
+    float m = M_NONE, l = 0.0f;
+    if (tid < used) {
+        m = st[tid * all * 2];
+        l = st[tid * all * 2 + 1];
     }
+    float top = m;
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor(top, o, WAVE));
+    if ((tid & (WAVE - 1)) == 0)
+        red[tid / WAVE][0] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < AW; ++w)
+        top = fmaxf(top, red[w][0]);
+    const float f = __builtin_amdgcn_exp2f(m - top);
+    weight[tid] = f;
+    float sum = l * f;
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o >>= 1)
+        sum += __shfl_xor(sum, o, WAVE);
+    if ((tid & (WAVE - 1)) == 0)
+        red[tid / WAVE][1] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < AW; ++w)
+        sum += red[w][1];
+    const int d4 = tid % LANES, p = tid / LANES;
+    const float* src = a.ws + at * D + 4 * d4;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = p; s < used; s += PARTS)
+        v += *reinterpret_cast<const f32x4*>(src + s * all * D) * weight[s];
     part[p][d4] = v;
     __syncthreads();
     if (p == 0) {
+#pragma unroll
         for (int k = 1; k < PARTS; ++k)
             v += part[k][d4];
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -488,17 +516,22 @@ __global__ __launch_bounds__(AT) void attention_kv4_join_kernel(Kv4Attn a, Kv4Ca
 }
 
 // Rows of a tile: 16 columns, or 32 where a sequence has more.
+constexpr int64_t FILL = 512;   // workgroups that the chip holds at once
+
 inline int rows_per_tile(int64_t pairs) { return pairs <= 16 ? 16 : 32; }
 
-// Splits: enough workgroups for every CU several times over, each with at least 512 tokens.
+// Splits: two workgroups of four waves a CU fill the chip, so that many in all, each with at
+// least 256 tokens, and at most what the second kernel joins.
 Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len) {
     const int64_t pairs = (int64_t)max_q * (q_heads / kv_heads);
+    constexpr int64_t unit = TB * AW;
     Split s;
     s.tiles = (int)((pairs + rows_per_tile(pairs) - 1) / rows_per_tile(pairs));
     const int64_t base = (int64_t)batch * kv_heads * s.tiles;
-    const int64_t want = base > 0 ? (2048 + base - 1) / base : 1;
+    int64_t want = base > 0 ? (FILL + base - 1) / base : 1;
+    want = want < MAX_SPLITS ? want : MAX_SPLITS;
     int64_t stretch = (max_len + want - 1) / want;
-    stretch = stretch < 512 ? 512 : (stretch + TB * AW - 1) / (TB * AW) * (TB * AW);
+    stretch = stretch < 2 * unit ? 2 * unit : (stretch + unit - 1) / unit * unit;
     s.stretch = (int)stretch;
     s.n = (int)((max_len + stretch - 1) / stretch);
     return s;

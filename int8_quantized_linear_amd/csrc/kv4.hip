@@ -11,14 +11,22 @@
 namespace ql {
 namespace {
 
-constexpr int KT = 256;   // threads per workgroup
+constexpr int KT = 256, KW = KT / WAVE;   // threads and waves per workgroup
 
+// 8 neighbouring values as fp32.
 template <bool F16>
-__device__ inline float load1(const void* p, int64_t i) {
-    if constexpr (F16)
-        return (float)reinterpret_cast<const _Float16*>(p)[i];
-    else
-        return reinterpret_cast<const float*>(p)[i];
+__device__ inline void load8(float (&v)[8], const void* p, int64_t i) {
+    if constexpr (F16) {
+        const f16x8 h = *reinterpret_cast<const f16x8*>(reinterpret_cast<const _Float16*>(p) + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = (float)h[e];
+    } else {
+        const f32x4* f = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = f[e / 4][e % 4];
+    }
 }
 
 // fp16 of a float, kept within fp16's finite range.
@@ -26,116 +34,194 @@ __device__ inline _Float16 to_f16_sat(float v) {
     return (_Float16)__builtin_amdgcn_fmed3f(v, -65504.0f, 65504.0f);
 }
 
-__device__ inline void group_params(float lo, float hi, _Float16& s16, _Float16& lo16) {
-    lo16 = to_f16_sat(lo);
-    s16 = to_f16_sat(fmaxf((hi - (float)lo16) / 15.0f, 0.0f));
-    const _Float16 least = (_Float16)5.9604644775390625e-08f;   // 2^-24
-    s16 = s16 > least ? s16 : least;
+// clamp(round(a / s), 0, 15) with y = 1 / s correctly rounded: a / s as RN(q0 + (a - q0 s) y),
+// q0 = RN(a y), the correctly rounded quotient (Markstein) where nothing underflows; where
+// something does, a / s is below 2^-80 and the code 0 on either path.
+__device__ inline uint32_t code4(float a, float s, float y) {
+    const float q0 = __fmul_rn(a, y);
+    const float q = fmaf(fmaf(-q0, s, a), y, q0);
+    return (uint32_t)__builtin_amdgcn_fmed3f(rintf(q), 0.0f, 15.0f);
 }
 
-__device__ inline uint32_t code4(float x, float s, float lo) {
-    return (uint32_t)__builtin_amdgcn_fmed3f(rintf((x - lo) / s), 0.0f, 15.0f);
-}
-
-// One thread per (row, head, group): min and max, then the codes of its G values.
+// A wave takes the runs of up to 8 rows that start among its `per` rows: rows of one sequence
+// whose positions lie in one aligned group of 8 (a unit of V's layout, inside one page). Lanes of
+// D / 8 take a token, 8 values each, so that a lane's K codes are one word, and G / 8 lanes share
+// a scale. V's codes of a full run are gathered through LDS into the 16-byte units of 8 tokens;
+// a part of a run writes its tokens' 16 bits, so that its neighbours keep theirs.
+//
+// per = 8 for prompts (one run a wave), 1 where most sequences bring one row. Bound by the rows'
+// read: prompts of 7108 rows, 32 heads of 128, 280 MB with the cache, see the table of cases.
 template <int D, int G, bool F16>
 __global__ __launch_bounds__(KT) void kv4_append_kernel(const void* __restrict__ k, const void* __restrict__ v,
-                                                        int64_t k_stride, int64_t v_stride, int rows, Kv4Cache c,
-                                                        Kv4Batch b) {
+                                                        int64_t k_stride, int64_t v_stride, int rows, int per,
+                                                        Kv4Cache c, Kv4Batch b) {
     using L = Kv4Layout<D, G>;
-    const int P = 1 << c.page_log2;
-    const int64_t id = (int64_t)blockIdx.x * KT + threadIdx.x;
-    const int g = (int)(id % L::NG);
-    const int64_t rh = id / L::NG;
-    const int head = (int)(rh % c.heads);
-    if (rh / c.heads >= rows)
-        return;
-    const int row = (int)(rh / c.heads);
-    const int seq = kv4_seq(b, row);
-    const int len = kv4_len(b, c, seq), pos = kv4_pos(b, seq, len, row);
-    if (pos < 0 || pos >= len)
-        return;
-    uint8_t* page = kv4_page(b, c, seq, pos, head);
-    const int slot = pos & (P - 1);
+    constexpr int LPT = D / 8, TPP = WAVE / LPT, PASSES = 8 / TPP;
+    __shared__ __attribute__((aligned(16))) uint16_t units[KW][D / 4][8];
+    const int P = 1 << c.page_log2, lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
+    const int head = blockIdx.x % c.heads;
+    const int r0 = (int)(blockIdx.x / c.heads * KW + wave) * per;
+
+    // lane i < per looks at row r0 + i: does a run start there?
+    int seq = 0, pos = -1, n = 0;
+    if (lane < per && r0 + lane < rows) {
+        const int row = r0 + lane;
+        seq = kv4_seq(b, row);
+        const int len = kv4_len(b, c, seq), end = b.starts[seq + 1];
+        pos = kv4_pos(b, seq, len, row);
+        if (pos >= 0 && pos < len && ((pos & 7) == 0 || row == b.starts[seq]))
+            n = min(min(8 - (pos & 7), end - row), rows - row);
+    }
+    uint64_t runs = __ballot(n > 0);
+    while (runs) {
+        const int i = __builtin_ctzll(runs);
+        runs &= runs - 1;
+        const int rseq = __builtin_amdgcn_readlane(seq, i), rpos = __builtin_amdgcn_readlane(pos, i);
+        const int rn = __builtin_amdgcn_readlane(n, i);
+        uint8_t* page = kv4_page(b, c, rseq, rpos, head);
+        const int slot0 = rpos & (P - 1) & ~7, t0 = rpos & 7;   // the run is tokens t0 .. t0 + rn - 1 of 8
+        const int d0 = (lane % LPT) * 8, g = d0 / G;
+        float x[2][PASSES][8];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const void* x = which ? v : k;
-        const int64_t base = row * (which ? v_stride : k_stride) + (int64_t)head * D + g * G;
-        float lo = INFINITY, hi = -INFINITY;
-        for (int i = 0; i < G; ++i) {
-            const float t = load1<F16>(x, base + i);
-            lo = fminf(lo, t);
-            hi = fmaxf(hi, t);
+        for (int p = 0; p < PASSES; ++p) {
+            const int t = p * TPP + lane / LPT - t0;
+            if (t >= 0 && t < rn) {
+                const int64_t row = r0 + i + t;
+                load8<F16>(x[0][p], k, row * k_stride + head * D + d0);
+                load8<F16>(x[1][p], v, row * v_stride + head * D + d0);
+            }
         }
-        _Float16 s16, lo16;
-        group_params(lo, hi, s16, lo16);
-        const float s = (float)s16, l = (float)lo16;
-        reinterpret_cast<_Float16*>(page + (which ? L::v_scale(P, g) : L::k_scale(P, g)))[slot] = s16;
-        reinterpret_cast<_Float16*>(page + (which ? L::v_low(P, g) : L::k_low(P, g)))[slot] = lo16;
-        if (which == 0) {
-            uint32_t* to = reinterpret_cast<uint32_t*>(page + L::k_codes(slot));
-            for (int w = 0; w < G / 8; ++w) {
-                const int d = g * G + 8 * w;
-                uint32_t word = 0;
-                for (int e = 0; e < 8; ++e)
-                    word |= code4(load1<F16>(x, base + 8 * w + e), s, l) << (16 * (e & 1) + 4 * (e >> 1));
-                to[((d % 32) / 8) * (D / 32) + d / 32] = word;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int tok = p * TPP + lane / LPT, slot = slot0 + tok;
+            const bool on = tok >= t0 && tok < t0 + rn;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const float(&xs)[8] = x[which][p];
+                float lo = xs[0], hi = xs[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) {
+                    lo = fminf(lo, xs[e]);
+                    hi = fmaxf(hi, xs[e]);
+                }
+#pragma unroll
+                for (int o = G / 16; o > 0; o >>= 1) {
+                    lo = fminf(lo, __shfl_xor(lo, o, WAVE));
+                    hi = fmaxf(hi, __shfl_xor(hi, o, WAVE));
+                }
+                const _Float16 lo16 = to_f16_sat(lo);
+                const float lf = (float)lo16;
+                const _Float16 least = (_Float16)5.9604644775390625e-08f;   // 2^-24
+                _Float16 s16 = to_f16_sat(fmaxf((hi - lf) / 15.0f, 0.0f));
+                s16 = s16 > least ? s16 : least;
+                const float s = (float)s16, y = 1.0f / s;
+                if (on && lane % (G / 8) == 0) {
+                    reinterpret_cast<_Float16*>(page + (which ? L::v_scale(P, g) : L::k_scale(P, g)))[slot] = s16;
+                    reinterpret_cast<_Float16*>(page + (which ? L::v_low(P, g) : L::k_low(P, g)))[slot] = lo16;
+                }
+                if (which == 0) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w |= code4(xs[e] - lf, s, y) << (16 * (e & 1) + 4 * (e >> 1));
+                    if (on)
+                        reinterpret_cast<uint32_t*>(page + L::k_codes(slot))[((d0 % 32) / 8) * (D / 32) + d0 / 32] = w;
+                } else {
+                    // bytes of d pairs, of 4 quads; the other half of each is 32 values away, in
+                    // lane ^ 4: either lane completes two quads
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w |= code4(xs[e] - lf, s, y) << (4 * e);
+                    const uint32_t z = __shfl_xor(w, 4, WAVE);
+                    const bool up = lane & 4;
+                    const uint32_t a = up ? z >> 16 : w, h = up ? w >> 16 : z;
+                    const uint32_t two = (a & 0xFF) | (h & 0xFF) << 8 | (a & 0xFF00) << 8 | (h & 0xFF00) << 16;
+                    const int quad = d0 / 64 * 16 + d0 % 32 / 2 + (up ? 2 : 0);
+                    if (rn == 8) {
+                        units[wave][quad][tok] = (uint16_t)two;
+                        units[wave][quad + 1][tok] = (uint16_t)(two >> 16);
+                    } else if (on) {
+                        uint16_t* to = reinterpret_cast<uint16_t*>(page + L::v_codes(P, slot / 8)) + slot % 8;
+                        to[quad * 8] = (uint16_t)two;
+                        to[quad * 8 + 8] = (uint16_t)(two >> 16);
+                    }
+                }
             }
-        } else {
-            // quads with their low half in this group; a group of 32 holds half of each quad
-            // of its 64-wide chunk, one byte (d, d + 1)
-            uint8_t* to = page + L::v_codes(P, slot / 8);
-            for (int w = 0; w < G / 2; ++w) {
-                const int d = g * G + 2 * w;
-                const uint32_t byte = code4(load1<F16>(x, base + 2 * w), s, l) |
-                                      code4(load1<F16>(x, base + 2 * w + 1), s, l) << 4;
-                const int quad = (d / 64) * 16 + (d % 32) / 2;
-                to[quad * 16 + (slot % 8) * 2 + (d % 64) / 32] = (uint8_t)byte;
-            }
+        }
+        if (rn == 8) {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if (lane < D / 4)
+                *reinterpret_cast<u32x4*>(page + L::v_codes(P, slot0 / 8) + lane * 16) =
+                    *reinterpret_cast<const u32x4*>(units[wave][lane]);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
     }
 }
 
-// One thread per (row, head, 8 values) of K and of V.
+template <bool F16>
+__device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
+    if constexpr (F16) {
+        f16x8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[e] = (_Float16)v[e];
+        *reinterpret_cast<f16x8*>(reinterpret_cast<_Float16*>(p) + i) = h;
+    } else {
+        f32x4* f = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i);
+        f[0] = f32x4{v[0], v[1], v[2], v[3]};
+        f[1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+}
+
+// One thread per (row, head) and 16 values of K and of V: d = 64 c + 8 kg + 0 .. 7 and 32 more,
+// which are two neighbouring words of K and the 4 quads 4 kg .. 4 kg + 3 of V's chunk c.
 template <int D, int G, bool F16>
 __global__ __launch_bounds__(KT) void kv4_read_kernel(Kv4Cache c, Kv4Batch b, int rows, void* __restrict__ k_out,
                                                       void* __restrict__ v_out) {
     using L = Kv4Layout<D, G>;
     const int P = 1 << c.page_log2;
     const int64_t id = (int64_t)blockIdx.x * KT + threadIdx.x;
-    const int d0 = (int)(id % (D / 8)) * 8;
-    const int64_t rh = id / (D / 8);
+    const int part = (int)(id % (D / 16)), ch = part / 4, kg = part % 4;
+    const int64_t rh = id / (D / 16);
     const int head = (int)(rh % c.heads);
     if (rh / c.heads >= rows)
         return;
     const int row = (int)(rh / c.heads);
     const int seq = kv4_seq(b, row);
     const int len = kv4_len(b, c, seq), pos = kv4_pos(b, seq, len, row);
-    float kx[8] = {}, vx[8] = {};
+    const int d0 = ch * 64 + kg * 8;
+    float kx[2][8] = {}, vx[2][8] = {};
     if (pos >= 0 && pos < len) {
         const uint8_t* page = kv4_page(b, c, seq, pos, head);
-        const int slot = pos & (P - 1), g = d0 / G;
-        const uint32_t kw = reinterpret_cast<const uint32_t*>(page + L::k_codes(slot))[((d0 % 32) / 8) * (D / 32) + d0 / 32];
-        const float ks = (float)reinterpret_cast<const _Float16*>(page + L::k_scale(P, g))[slot];
-        const float kl = (float)reinterpret_cast<const _Float16*>(page + L::k_low(P, g))[slot];
-        const float vs = (float)reinterpret_cast<const _Float16*>(page + L::v_scale(P, g))[slot];
-        const float vl = (float)reinterpret_cast<const _Float16*>(page + L::v_low(P, g))[slot];
-        const uint8_t* vb = page + L::v_codes(P, slot / 8);
-        for (int e = 0; e < 8; ++e) {
-            const int d = d0 + e, quad = (d / 64) * 16 + (d % 32) / 2;
-            kx[e] = fmaf(ks, (float)((kw >> (16 * (e & 1) + 4 * (e >> 1))) & 15), kl);
-            vx[e] = fmaf(vs, (float)((vb[quad * 16 + (slot % 8) * 2 + (d % 64) / 32] >> (4 * (d & 1))) & 15), vl);
+        const int slot = pos & (P - 1);
+        const u32x2 kw = *reinterpret_cast<const u32x2*>(page + L::k_codes(slot) + (kg * (D / 32) + 2 * ch) * 4);
+        const uint16_t* vq = reinterpret_cast<const uint16_t*>(page + L::v_codes(P, slot / 8)) + (ch * 16 + kg * 4) * 8 +
+                             slot % 8;
+        const uint32_t q[4] = {vq[0], vq[8], vq[16], vq[24]};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int g = (d0 + 32 * h) / G;
+            const float ks = (float)reinterpret_cast<const _Float16*>(page + L::k_scale(P, g))[slot];
+            const float kl = (float)reinterpret_cast<const _Float16*>(page + L::k_low(P, g))[slot];
+            const float vs = (float)reinterpret_cast<const _Float16*>(page + L::v_scale(P, g))[slot];
+            const float vl = (float)reinterpret_cast<const _Float16*>(page + L::v_low(P, g))[slot];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                kx[h][e] = fmaf(ks, (float)((kw[h] >> (16 * (e & 1) + 4 * (e >> 1))) & 15), kl);
+                vx[h][e] = fmaf(vs, (float)((q[e / 2] >> (8 * h + 4 * (e & 1))) & 15), vl);
+            }
         }
     }
-    const int64_t at = rh * D + d0;
-    for (int e = 0; e < 8; ++e)
-        if constexpr (F16) {
-            reinterpret_cast<_Float16*>(k_out)[at + e] = (_Float16)kx[e];
-            reinterpret_cast<_Float16*>(v_out)[at + e] = (_Float16)vx[e];
-        } else {
-            reinterpret_cast<float*>(k_out)[at + e] = kx[e];
-            reinterpret_cast<float*>(v_out)[at + e] = vx[e];
-        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        store8<F16>(k_out, rh * D + d0 + 32 * h, kx[h]);
+        store8<F16>(v_out, rh * D + d0 + 32 * h, vx[h]);
+    }
 }
 
 }  // namespace
@@ -144,12 +230,12 @@ ql_status launch_kv4_append(const void* k, const void* v, bool f16, int64_t k_st
                             const Kv4Cache& c, int D, int G, const Kv4Batch& b, hipStream_t stream) {
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
-        const int64_t n = rows * c.heads * (DD / GG);
-        const dim3 grid((uint32_t)((n + KT - 1) / KT));
+        const int per = rows > 4 * (int64_t)b.batch ? 8 : 1;
+        const dim3 grid((uint32_t)((rows + per * KW - 1) / (per * KW) * c.heads));
         if (f16)
-            kv4_append_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, c, b);
+            kv4_append_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, per, c, b);
         else
-            kv4_append_kernel<DD, GG, false><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, c, b);
+            kv4_append_kernel<DD, GG, false><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, per, c, b);
         return launch_status();
     });
 }
@@ -158,7 +244,7 @@ ql_status launch_kv4_read(const Kv4Cache& c, int D, int G, const Kv4Batch& b, in
                           bool f16, hipStream_t stream) {
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
-        const int64_t n = rows * c.heads * (DD / 8);
+        const int64_t n = rows * c.heads * (DD / 16);
         const dim3 grid((uint32_t)((n + KT - 1) / KT));
         if (f16)
             kv4_read_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(c, b, (int)rows, k_out, v_out);
