@@ -77,83 +77,168 @@ struct Split {
     int tiles;        // row tiles a sequence and kv head at the launch's max_q
 };
 
-// A step's cache data for one lane: lane (m = lane & 15, kg = lane >> 4) holds K's words of
-// tokens 8 (m / 4) + m % 4 (+ 4 for the second half of the block) and d = 32 i + 8 kg .., V's
-// words of tokens 8 kg .. 8 kg + 7 and quad m of each chunk, and the scales and lows of those
-// 8 tokens, in pairs.
-template <int D, int G>
-struct Block {
-    static constexpr int NG = D / G, NI = D / 32, NC = D / 64;
-    uint32_t k[2][NI];
-    u32x4 v[NC];
-    u32x4 ks[NG], kl[NG], vs[NG], vl[NG];
-};
+typedef __attribute__((address_space(3))) void* lds_ptr;
 
+// s_waitcnt immediate: at most n vector-memory operations pending (gfx9 encoding: vmcnt in
+// bits 3:0 and 15:14, the other counters not waited for)
+constexpr int vmcnt_le(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | (((n >> 4) & 3) << 14); }
+
+// 16 bytes per lane from memory straight into LDS: lane l's land at l * 16 past the wave-uniform
+// LDS address. Device pass only (in the host pass the builtin makes clang drop the kernel's
+// launch stub).
+__device__ inline void lds_copy16(const void* g, void* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_global_load_lds(g, (lds_ptr)lds, 16, 0, 0);
+#endif
+}
+
+// Reads from LDS that the compiler does not see as such: it would make each wait for every copy in
+// flight (the copies write LDS too). The reads and their wait are one block; what orders them
+// behind the copies of their slot is the caller's wait for those, and what orders a later copy
+// into the slot behind them is the wait in the block.
+__device__ inline uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)(lds_ptr)p; }
+
+template <int O0, int O1>
+__device__ inline void lds_read(uint32_t at, u32x2& a, u32x2& b) {
+    asm volatile("ds_read_b64 %0, %2 offset:%3\n\tds_read_b64 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b)
+                 : "v"(at), "n"(O0), "n"(O1));
+}
+template <int O0, int O1>
+__device__ inline void lds_read(uint32_t at, u32x4& a, u32x4& b) {
+    asm volatile("ds_read_b128 %0, %2 offset:%3\n\tds_read_b128 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b)
+                 : "v"(at), "n"(O0), "n"(O1));
+}
+template <int O0, int O1, int O2, int O3>
+__device__ inline void lds_read(uint32_t at, u32x4& a, u32x4& b, u32x4& c, u32x4& d) {
+    asm volatile(
+        "ds_read_b128 %0, %4 offset:%5\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b128 %2, %4 offset:%7\n\t"
+        "ds_read_b128 %3, %4 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+        : "v"(at), "n"(O0), "n"(O1), "n"(O2), "n"(O3));
+}
+
+// A block's cache data in LDS, copied straight from memory (16 bytes a lane, lane l's at 16 l of
+// each 1024-byte copy). K's codes, V's codes and each array of scales or lows of 32 tokens are
+// contiguous in a page, so all copies are linear; with pages of 16 tokens their upper halves come
+// from a second page. K's 16-byte chunks of token T are rotated by T / 8 places within the
+// token's row, so that the operands' reads (tokens 8 x + 0 .. 3 at once) meet no bank twice.
 template <int D, int G, bool BIG>
-struct Loader {
+struct Ring {
     using L = Kv4Layout<D, G>;
-    using B = Block<D, G>;
+    static constexpr int NG = D / G, KC = D / 64, PC = (NG + 3) / 4, COPIES = 2 * KC + PC;
+    static constexpr int K_AT = 0, V_AT = 16 * D, P_AT = 32 * D, BYTES = 32 * D + 256 * NG;
     const int32_t* table;
-    uint8_t* data;
-    int64_t head_bytes;
-    int64_t head_off;
-    int heads, pages, log2p, last;
-    int k_off, v_off, p_off;
-    bool k_hi, v_hi;
+    const uint8_t* data;   // the head's part of page 0
+    int64_t page_bytes;
+    int pages, log2p, last;
+    int k_src[KC], v_src, p_src[PC];   // this lane's byte offsets in a page, without the slot's part
+    bool k_hi, p_hi;                   // the lane's bytes come from the second page
 
-    __device__ inline void init(const Kv4Batch& b, const Kv4Cache& c, int seq, int head, int end) {
+    __device__ inline Ring(const Kv4Batch& b, const Kv4Cache& c, int seq, int head, int end) {
         table = b.table + (int64_t)seq * b.width;
-        data = c.data;
-        head_bytes = c.head_bytes;
-        head_off = head * c.head_bytes;
-        heads = c.heads;
+        data = c.data + head * c.head_bytes;
+        page_bytes = c.heads * c.head_bytes;
         pages = c.pages;
         log2p = c.page_log2;
         last = end - 1;
-        const int lane = threadIdx.x & (WAVE - 1), m = lane & 15, kg = lane >> 4, P = 1 << log2p;
-        // with pages of 16 tokens the upper two groups of 8 lie in a second page
-        const int kx = BIG ? m >> 2 : (m >> 2) & 1, vx = BIG ? kg : kg & 1;
-        k_hi = !BIG && (m >> 3);
-        v_hi = !BIG && (kg >> 1);
-        k_off = (kx * 8 + (m & 3)) * (D / 2) + kg * (D / 8);
-        v_off = L::v_codes(P, 0) + vx * 4 * D + m * 16;
-        p_off = vx * 16;
+        const int lane = threadIdx.x & (WAVE - 1), P = 1 << log2p;
+        constexpr int CPT = D / 32;   // 16-byte chunks of a token's K row
+        for (int i = 0; i < KC; ++i) {
+            const int at = i * 64 + lane, tok = at / CPT, part = at % CPT;
+            const int src = CPT == 4 || CPT == 8 ? (part & ~3) | ((part - tok / 8) & 3) : part;
+            k_src[i] = (BIG ? tok : tok & 15) * (D / 2) + src * 16;
+        }
+        // which page: D = 64 has both in one copy, larger rows a page in half the copies
+        k_hi = !BIG && D == 64 && lane >= 32;
+        v_src = L::v_codes(P, 0) + lane * 16 - (k_hi ? 512 : 0);
+        const int part = lane & 3;
+        p_hi = !BIG && part >= 2;
+        for (int i = 0; i < PC; ++i) {
+            const int seg = min(i * 16 + lane / 4, 4 * NG - 1);   // ks, kl of each group, then vs, vl
+            p_src[i] = (seg < 2 * NG ? L::k_scale(P, 0) : L::v_scale(P, 0)) + (seg % (2 * NG)) * 2 * P + (BIG ? part : part & 1) * 16;
+        }
     }
-    __device__ inline const uint8_t* page(int pos) const {
-        uint32_t p = table_entry(table + (min(pos, last) >> log2p));
-        p = p < (uint32_t)pages ? p : (uint32_t)pages - 1;
-        return data + (int64_t)p * (heads * head_bytes) + head_off;
+    __device__ inline uint32_t page_of(int pos) const {
+        const uint32_t p = table_entry(table + (min(pos, last) >> log2p));
+        return p < (uint32_t)pages ? p : (uint32_t)pages - 1;
     }
-    __device__ inline void load(B& x, int t0) const {
-        const int P = 1 << log2p, slot = t0 & (P - 1);
-        const uint8_t* pa = page(t0);
-        const uint8_t *pk = pa, *pv = pa;
-        if constexpr (!BIG) {
-            const uint8_t* pb = page(t0 + 16);
-            pk = k_hi ? pb : pa;
-            pv = v_hi ? pb : pa;
+    // Starts the copies of the block at t0, whose pages are a (and b, of its second 16 tokens).
+    __device__ inline void copy(uint8_t* slot, int t0, uint32_t a, uint32_t b) const {
+        const int in = t0 & ((1 << log2p) - 1);   // first token's place in the page
+        const uint8_t* pa = data + (int64_t)a * page_bytes;
+        const uint8_t* pb = BIG ? pa : data + (int64_t)b * page_bytes;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+            const uint8_t* base = BIG ? pa : D == 64 ? (k_hi ? pb : pa) : i < KC / 2 ? pa : pb;
+            lds_copy16(base + (in * (D / 2) + k_src[i]), slot + K_AT + 1024 * i);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint8_t* p = pk + (slot * (D / 2) + k_off + h * 4 * (D / 2));
-            if constexpr (D == 64) {
-                *reinterpret_cast<u32x2*>(x.k[h]) = *reinterpret_cast<const u32x2*>(p);
-            } else {
+        for (int i = 0; i < KC; ++i) {
+            const uint8_t* base = BIG ? pa : D == 64 ? (k_hi ? pb : pa) : i < KC / 2 ? pa : pb;
+            const int i0 = BIG || D == 64 || i < KC / 2 ? i : i - KC / 2;
+            lds_copy16(base + (in * (D / 2) + v_src + 1024 * i0), slot + V_AT + 1024 * i);
+        }
+        const uint8_t* pp = p_hi ? pb : pa;
 #pragma unroll
-                for (int i = 0; i < B::NI; i += 4)
-                    *reinterpret_cast<u32x4*>(x.k[h] + i) = *reinterpret_cast<const u32x4*>(p + 4 * i);
+        for (int i = 0; i < PC; ++i)
+            if (NG % 4 == 0 || (int)(threadIdx.x & (WAVE - 1)) < 16 * NG)
+                lds_copy16(pp + (2 * in + p_src[i]), slot + P_AT + 1024 * i);
+    }
+    // LDS addresses, past the slot's, of lane (m, kg)'s operand words: K's of token 8 (m / 4) + m % 4
+    // (+ 4) and d = 32 i + 8 kg .., V's of tokens 8 kg .. 8 kg + 7 and quad m, and those 8 tokens'
+    // scales and lows.
+    static __device__ inline uint32_t k_at() {
+        const int lane = threadIdx.x & (WAVE - 1), m = lane & 15, kg = lane >> 4, x = m >> 2;
+        const int chunk = D == 64 ? 0 : ((D / 128) * kg & ~3) | (((D / 128) * kg + x) & 3);   // D = 256: see k_words
+        return K_AT + (x * 8 + (m & 3)) * (D / 2) + (D == 64 ? kg * 8 : chunk * 16);
+    }
+    static __device__ inline uint32_t v_at() {
+        const int lane = threadIdx.x & (WAVE - 1), m = lane & 15, kg = lane >> 4;
+        return V_AT + kg * 4 * D + m * 16;
+    }
+    static __device__ inline uint32_t p_at() { return P_AT + ((threadIdx.x & (WAVE - 1)) >> 4) * 16; }
+    // K's words of both halves of the block.
+    static __device__ inline void k_words(uint32_t (&w)[2][D / 32], uint32_t at) {
+        if constexpr (D == 64) {
+            u32x2 x, y;
+            lds_read<0, 4 * (D / 2)>(at, x, y);
+            w[0][0] = x[0], w[0][1] = x[1], w[1][0] = y[0], w[1][1] = y[1];
+        } else {
+            // D = 256: the lane's second chunk is one place on, in the same 64 bytes, so the
+            // places wrap where x + 2 kg is odd and 3
+#pragma unroll
+            for (int c = 0; c < D / 128; ++c) {
+                const int lane = threadIdx.x & (WAVE - 1), kg = lane >> 4, q = (lane & 15) >> 2;
+                const int place = ((D / 128) * kg + q) & 3;
+                const uint32_t to = at + (c ? (place == 3 ? -48 : 16) : 0);
+                u32x4 x, y;
+                lds_read<0, 4 * (D / 2)>(to, x, y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[0][4 * c + j] = x[j], w[1][4 * c + j] = y[j];
             }
         }
-#pragma unroll
-        for (int c = 0; c < B::NC; ++c)
-            x.v[c] = *reinterpret_cast<const u32x4*>(pv + (slot * (D / 2) + v_off + c * 256));
-        const uint8_t* pp = pv + (2 * slot + p_off);
-#pragma unroll
-        for (int g = 0; g < B::NG; ++g) {
-            x.ks[g] = *reinterpret_cast<const u32x4*>(pp + L::k_scale(P, g));
-            x.kl[g] = *reinterpret_cast<const u32x4*>(pp + L::k_low(P, g));
-            x.vs[g] = *reinterpret_cast<const u32x4*>(pp + L::v_scale(P, g));
-            x.vl[g] = *reinterpret_cast<const u32x4*>(pp + L::v_low(P, g));
+    }
+    static __device__ inline void v_words(u32x4 (&w)[D / 64], uint32_t at) {
+        if constexpr (D == 64)
+            lds_read<0, 0>(at, w[0], w[0]);
+        else if constexpr (D == 128)
+            lds_read<0, 256>(at, w[0], w[1]);
+        else
+            lds_read<0, 256, 512, 768>(at, w[0], w[1], w[2], w[3]);
+    }
+    // Scales and lows of all groups, K's (0) or V's (1).
+    template <int WHICH, int GI = 0>
+    static __device__ inline void params(u32x4 (&sc)[NG], u32x4 (&low)[NG], uint32_t at) {
+        constexpr int O = (WHICH * NG + GI) * 128;
+        if constexpr (GI + 1 < NG) {
+            lds_read<O, O + 64, O + 128, O + 192>(at, sc[GI], low[GI], sc[GI + 1], low[GI + 1]);
+            if constexpr (GI + 2 < NG)
+                params<WHICH, GI + 2>(sc, low, at);
+        } else {
+            lds_read<O, O + 64>(at, sc[GI], low[GI]);
         }
     }
 };
@@ -165,36 +250,54 @@ __device__ inline f16x8 codes_raw(uint32_t w) {
     return __builtin_bit_cast(f16x8, r);
 }
 
+// Constants of the masks in registers: (w & mask) | 1024 is then one v_and_or_b32 (an instruction
+// with three operands takes no literal).
+struct Masks {
+    uint32_t even, odd, k1024;
+    __device__ inline Masks() {
+        asm("s_mov_b32 %0, 0x000F000F" : "=s"(even));
+        asm("s_mov_b32 %0, 0x00F000F0" : "=s"(odd));
+        asm("v_mov_b32 %0, 0x64006400" : "=v"(k1024));
+    }
+};
+
 // Codes of nibble JJ of each half as fp16 integers: 1024 + c (or 1024 + 16 c) is exact.
 template <int JJ>
-__device__ inline f16x2 codes_int(uint32_t w) {
+__device__ inline f16x2 codes_int(uint32_t w, const Masks& mk) {
     const uint32_t h = JJ & 2 ? w >> 8 : w;
     if constexpr (JJ & 1)
-        return as_f16x2((h & 0x00F000F0u) | 0x64006400u) * (f16x2){(_Float16)0.0625f, (_Float16)0.0625f} -
+        return as_f16x2((h & mk.odd) | mk.k1024) * (f16x2){(_Float16)0.0625f, (_Float16)0.0625f} -
                (f16x2){(_Float16)64.0f, (_Float16)64.0f};
     else
-        return as_f16x2((h & 0x000F000Fu) | 0x64006400u) - (f16x2){(_Float16)1024.0f, (_Float16)1024.0f};
+        return as_f16x2((h & mk.even) | mk.k1024) - (f16x2){(_Float16)1024.0f, (_Float16)1024.0f};
 }
 
 // V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16.
 template <int JJ>
-__device__ inline f16x8 v_values(u32x4 w, u32x4 s, u32x4 l) {
+__device__ inline f16x8 v_values(u32x4 w, u32x4 s, u32x4 l, const Masks& mk) {
     u32x4 r;
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-        r[p] = as_u32(__builtin_elementwise_fma(codes_int<JJ>(w[p]), as_f16x2(s[p]), as_f16x2(l[p])));
+        r[p] = as_u32(__builtin_elementwise_fma(codes_int<JJ>(w[p], mk), as_f16x2(s[p]), as_f16x2(l[p])));
     return __builtin_bit_cast(f16x8, r);
 }
 
 __device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2])[i & 1]; }
 
+// Ring slots of a wave: one in use, the other filling. Two let four workgroups of a CU (two of
+// D = 256) share its 160 KB of LDS.
+constexpr int SLOTS = 2;
+
 template <int D, int G, bool BIG, int NQ>
-__global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_decode_kernel(Kv4Attn a, Kv4Cache c,
-                                                                                           Kv4Batch b, Split sp) {
-    using B = Block<D, G>;
-    constexpr int NG = B::NG, NI = B::NI, NC = B::NC, PER = 16 * NQ;
-    __shared__ float part[AW][16][D + 4];
+__global__ __launch_bounds__(AT, D == 256 ? (NQ == 1 ? 2 : 1) : NQ == 1 ? 4 : 2) void attention_kv4_decode_kernel(
+    Kv4Attn a, Kv4Cache c, Kv4Batch b, Split sp) {
+    using RG = Ring<D, G, BIG>;
+    constexpr int NG = D / G, NI = D / 32, NC = D / 64, PER = 16 * NQ;
+    // the ring, and after the loop the waves' partial results in its place
+    constexpr int RING = AW * SLOTS * RG::BYTES, PART = AW * 16 * (D + 4) * 4;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[RING > PART ? RING : PART];
     __shared__ float stats[AW][16][2];
+    float(*part)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(lds);
     const int R = a.q_heads / c.heads;
     int id = blockIdx.x;
     const int head = id % c.heads;
@@ -203,9 +306,12 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
     id /= b.batch;
     const int split = id % sp.n;
     const int tile0 = id / sp.n;
-    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, n = lane & 15, kg = lane >> 4;
-    const float kappa = fabsf(a.scale) * 1.44269504088896f * 16777216.0f;   // the codes' 2^-24 taken out
-    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+    const int lane = threadIdx.x & (WAVE - 1), n = lane & 15, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const Masks mk;
+    // the codes' 2^-24 taken out; not 0, so that a masked score stays the smallest
+    const float kappa = fmaxf(fabsf(a.scale) * 1.44269504088896f * 16777216.0f, 1e-30f);
+    const float sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
 
     for (int tile = tile0;; tile += sp.tiles) {
         const RowTile t = row_tile(b, c, seq, tile, PER, R, a.window);
@@ -216,6 +322,27 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
         const int from = base + split * stretch, to = min(from + stretch, t.end);
         if (split > 0 && from >= t.end)
             continue;   // no tokens; split 0 always writes
+
+        const RG ring(b, c, seq, head, t.end);
+        uint8_t* slots = lds + wave * (SLOTS * RG::BYTES);
+        const uint32_t k_at = lds_addr(slots) + RG::k_at(), v_at = lds_addr(slots) + RG::v_at(),
+                       p_at = lds_addr(slots) + RG::p_at();
+        int t0 = from + wave * TB;   // the block in use
+        uint32_t pa = 0, pb = 0;     // pages of the block to be copied next
+        auto pages = [&](int pos) {
+            if (pos < to) {
+                pa = ring.page_of(pos);
+                pb = BIG ? pa : ring.page_of(pos + 16);
+            }
+        };
+        __syncthreads();   // the last tile's partial results have been read
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            pages(t0 + i * AW * TB);
+            if (t0 + i * AW * TB < to)
+                ring.copy(slots + i * RG::BYTES, t0 + i * AW * TB, pa, pb);
+        }
+        pages(t0 + SLOTS * AW * TB);
 
         // Q's operand: column n of each row tile, slots 2, 3, 6, 7 of every 8 divided by 16
         f16x8 q[NQ][NI];
@@ -266,26 +393,15 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
         const _Float16 one = (_Float16)1.0f;
         const f16x8 ones = {one, one, one, one, one, one, one, one};
 
-        auto step = [&](B& x, int t0) {
+        auto step = [&](uint32_t at) {
             const bool edge = t0 < t.all_begin || t0 + TB > t.all_end;   // some row does not see all of it
-            if (t0 < t.begin || t0 + TB > t.end) {
-                // what lies at positions that no row sees may be anything: a weight of 0 must
-                // not meet an infinite or NaN value
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int j = t0 + kg * 8 + 2 * p;
-                    const uint32_t keep = (j >= t.begin && j < t.end ? 0xFFFFu : 0u) |
-                                          (j + 1 >= t.begin && j + 1 < t.end ? 0xFFFF0000u : 0u);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        x.vs[g][p] &= keep;
-                        x.vl[g][p] &= keep;
-                    }
-                }
-            }
             f32x4 s[NQ][2];
+            uint32_t kw[2][NI];
+            u32x4 sc[NG], low[NG];
+            RG::k_words(kw, k_at + at);
+            RG::template params<0>(sc, low, p_at + at);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     f32x4 acc[NQ];
@@ -294,7 +410,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
                         acc[u] = f32x4{0, 0, 0, 0};
 #pragma unroll
                     for (int i = g * (G / 32); i < (g + 1) * (G / 32); ++i) {
-                        const f16x8 kc = codes_raw(x.k[h][i]);
+                        const f16x8 kc = codes_raw(kw[h][i]);
 #pragma unroll
                         for (int u = 0; u < NQ; ++u)
                             acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kc, q[u][i], acc[u], 0, 0, 0);
@@ -303,24 +419,28 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
                     for (int u = 0; u < NQ; ++u)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float low = half_of(x.kl[g], 4 * h + r), sc = half_of(x.ks[g], 4 * h + r);
-                            s[u][h][r] = fmaf(low, qsum[u][g], g ? s[u][h][r] : 0.0f);
-                            s[u][h][r] = fmaf(sc, acc[u][r], s[u][h][r]);
+                            s[u][h][r] = fmaf(half_of(low[g], 4 * h + r), qsum[u][g], g ? s[u][h][r] : 0.0f);
+                            s[u][h][r] = fmaf(half_of(sc[g], 4 * h + r), acc[u][r], s[u][h][r]);
                         }
                 }
+            }
+            if (edge) {
+                // a score far below all others: its weight is exactly 0
+                int tb = t0;
+                asm volatile("" : "+s"(tb));   // a branch, not selects in every step
+#pragma unroll
+                for (int u = 0; u < NQ; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int j = tb + kg * 8 + 4 * h + r;
+                            s[u][h][r] = j >= rbeg[u] && j < rend[u] ? s[u][h][r] : -3.0e38f;
+                        }
+            }
             f16x8 p[NQ];
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
-                bool see[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = t0 + kg * 8 + 4 * h + r;
-                        see[h][r] = !edge || (j >= rbeg[u] && j < rend[u]);
-                        if (edge && !see[h][r])
-                            s[u][h][r] = -3.0e38f;
-                    }
                 float top = s[u][0][0];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -339,52 +459,66 @@ __global__ __launch_bounds__(AT, NQ == 1 && D < 256 ? 2 : 1) void attention_kv4_
                     for (int i = 0; i < D / 16; ++i)
                         o[u][i] *= f;
                 }
-                const float shift = P_SHIFT - m[u];
+                // before a row's first score, 0 in place of the maximum: masked weights stay 0
+                const float shift = m[u] > M_NONE ? P_SHIFT - m[u] : 0.0f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float w = __builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa, shift));
-                        if (edge)
-                            w = see[h][r] ? w : 0.0f;
-                        p[u][4 * h + r] = (_Float16)w;
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        p[u][4 * h + r] = (_Float16)__builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa, shift));
                 // the sum of the rounded weights, so that their rounding cancels in the quotient
                 l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u], l[u], 0, 0, 0);
             }
-            auto add = [&](auto jj, int ch) {
-                constexpr int JJ = decltype(jj)::value;
-                const int g = (64 * ch + 32 * (JJ / 2)) / G;
-                const f16x8 vv = v_values<JJ>(x.v[ch], x.vs[g], x.vl[g]);
+            u32x4 vs[NG], vl[NG], vw[NC];
+            RG::v_words(vw, v_at + at);
+            RG::template params<1>(vs, vl, p_at + at);
+            if (edge && (t0 < t.begin || t0 + TB > t.end)) {
+                // what lies at positions that no row sees may be anything: a weight of 0 must
+                // not meet an infinite or NaN value
+                int tb = t0;
+                asm volatile("" : "+s"(tb));
 #pragma unroll
-                for (int u = 0; u < NQ; ++u)
-                    o[u][4 * ch + JJ] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[u], o[u][4 * ch + JJ], 0, 0, 0);
-            };
+                for (int w = 0; w < 4; ++w) {
+                    const int j = tb + kg * 8 + 2 * w;
+                    const uint32_t keep = (j >= t.begin && j < t.end ? 0xFFFFu : 0u) |
+                                          (j + 1 >= t.begin && j + 1 < t.end ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        vs[g][w] &= keep;
+                        vl[g][w] &= keep;
+                    }
+                }
+            }
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) {
-                add(std::integral_constant<int, 0>{}, ch);
-                add(std::integral_constant<int, 1>{}, ch);
-                add(std::integral_constant<int, 2>{}, ch);
-                add(std::integral_constant<int, 3>{}, ch);
+                auto add = [&](auto jj) {
+                    constexpr int JJ = decltype(jj)::value;
+                    const int g = (64 * ch + 32 * (JJ / 2)) / G;
+                    const f16x8 vv = v_values<JJ>(vw[ch], vs[g], vl[g], mk);
+#pragma unroll
+                    for (int u = 0; u < NQ; ++u)
+                        o[u][4 * ch + JJ] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[u], o[u][4 * ch + JJ], 0, 0, 0);
+                };
+                add(std::integral_constant<int, 0>{});
+                add(std::integral_constant<int, 1>{});
+                add(std::integral_constant<int, 2>{});
+                add(std::integral_constant<int, 3>{});
             }
         };
 
-        Loader<D, G, BIG> ld;
-        ld.init(b, c, seq, head, t.end);
-        int t0 = from + wave * TB;
-        if (t0 < to) {
-            B x, y;
-            ld.load(x, t0);
-            while (true) {
-                const bool more = t0 + AW * TB < to;
-                if (more)
-                    ld.load(y, t0 + AW * TB);
-                step(x, t0);
-                t0 += AW * TB;
-                if (!more)
-                    break;
-                x = y;
-            }
+        for (uint32_t at = 0; t0 < to; t0 += AW * TB) {
+            // the block's copies have landed when only the younger slots' are pending
+            if (t0 + (SLOTS - 1) * AW * TB < to)
+                __builtin_amdgcn_s_waitcnt(vmcnt_le((SLOTS - 1) * RG::COPIES));
+            else
+                __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
+            __builtin_amdgcn_sched_barrier(0);
+            step(at);
+            __builtin_amdgcn_sched_barrier(0);
+            if (t0 + SLOTS * AW * TB < to)
+                ring.copy(slots + at, t0 + SLOTS * AW * TB, pa, pb);
+            pages(t0 + (SLOTS + 1) * AW * TB);
+            at = at + RG::BYTES == SLOTS * RG::BYTES ? 0 : at + RG::BYTES;
         }
 
         // join the waves: each brings its O to the largest maximum
