@@ -452,7 +452,8 @@ ql_status attention_kv4(const void* q, int64_t q_stride, void* out, int64_t rows
                         int64_t max_len, float scale, int64_t window, void* workspace,
                         int64_t workspace_bytes, void* stream);
 ql_status attention_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t D,
-                                        int64_t batch, int64_t max_q, int64_t max_len, int64_t* bytes);
+                                        int64_t batch, int64_t max_q, int64_t max_len, int64_t window,
+                                        int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@ the import fails with an ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -73,7 +74,7 @@ _SIGS = {
     "kv4_read": [_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _P],
     "attention_kv4": [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64,
                       _I64, _F, _I64, _P, _I64, _P],
-    "attention_kv4_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
+    "attention_kv4_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
@@ -261,26 +262,54 @@ def rms_norm_quantize_e4m3(x, gamma, residual=None, eps: float = 1e-6, res_out=N
 
 
 _FLOATS = (torch.float16, torch.float32)
+# The stream's handle without a Stream object around it: a decode step makes these calls once a
+# layer, and building the object is a sixth of a call's host time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _same(t, name, dtype, shape, index):
+    """_check for one dtype, an exact shape and a device index, quick where all is as it should be."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous()):
+        _check(t, name, (dtype,), shape, torch.device("cuda", index))
+    return t.data_ptr()
+
+
+def _float_matrix(t, name):
+    """fp16 or fp32, contiguous, on the GPU: its dtype code and pointer."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _FLOATS and t.is_contiguous()):
+        _check(t, name, _FLOATS)
+    return QL_F16 if t.dtype is torch.float16 else QL_F32, t.data_ptr()
+
+
+def _status(fn, st):
+    if st != 0:
+        raise QLError(fn, st)
 
 
 def _rms_norm(x, gamma, residual, eps, res_out, fn, code_dtype):
-    _check(x, "x", _FLOATS)
-    if x.dim() != 2:
+    xdt, xp = _float_matrix(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be 2-D [M, K]")
-    M, K = x.shape
-    dev = x.device
-    _check(gamma, "gamma", (torch.float32,), (K,), dev)
-    rdt = QL_F32
+    M, K = shape
+    index = x.get_device()
+    gp = _same(gamma, "gamma", torch.float32, (K,), index)
+    rdt, rp, op = QL_F32, None, None
     if residual is not None:
-        _check(residual, "residual", _FLOATS, (M, K), dev)
-        rdt = QL_F16 if residual.dtype == torch.float16 else QL_F32
-        res_out = _out(res_out, "res_out", (M, K), residual.dtype, dev)
+        rdt, rp = _float_matrix(residual, "residual")
+        rt = residual.dtype
+        _same(residual, "residual", rt, shape, index)
+        if res_out is None:
+            res_out = torch.empty_like(residual)
+        op = rp if res_out is residual else _same(res_out, "res_out", rt, shape, index)
     elif res_out is not None:
         raise ValueError("res_out needs a residual")
-    xq = torch.empty((M, K), dtype=code_dtype, device=dev)
-    xs = torch.empty((M,), dtype=torch.float32, device=dev)
-    _call(fn, _ptr(x), QL_F16 if x.dtype == torch.float16 else QL_F32, _ptr(residual), rdt, _ptr(gamma), eps, M, K,
-          _ptr(res_out), _ptr(xq), _ptr(xs), _stream(x))
+    xq = torch.empty_like(x, dtype=code_dtype)
+    xs = gamma.new_empty((M,))
+    _status(fn, getattr(lib, fn)(xp, xdt, rp, rdt, gp, eps, M, K,
+                                 op, xq.data_ptr(), xs.data_ptr(), _raw_stream(index)))
     return (xq, xs) if residual is None else (xq, xs, res_out)
 
 
@@ -291,36 +320,39 @@ def kv4_page_bytes(page_size: int, head_dim: int, group: int) -> int:
 
 
 def _check_kv4(cache, block_table, seq_lens, starts, head_dim, page_size, group):
+    """Device index, batch and the pointers of the cache and of the batch's arrays."""
     _check(cache, "cache", (torch.uint8,))
     if group <= 0 or head_dim % group:
         raise ValueError("group must divide the head size")
     if cache.dim() != 3 or cache.shape[2] != kv4_page_bytes(page_size, head_dim, group):
         raise ValueError("cache has shape %s, expected [num_pages, kv_heads, %d]"
                          % (tuple(cache.shape), kv4_page_bytes(page_size, head_dim, group)))
-    dev = cache.device
-    _check(block_table, "block_table", (torch.int32,), None, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be 2-D [batch, pages of a sequence]")
-    batch = block_table.shape[0]
-    _check(seq_lens, "seq_lens", (torch.int32,), (batch,), dev)
-    _check(starts, "starts", (torch.int32,), (batch + 1,), dev)
-    return dev, batch
+    index = cache.get_device()
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a 2-D tensor [batch, pages of a sequence]")
+    shape = block_table.shape
+    batch = shape[0]
+    return (index, batch, cache.data_ptr(), _same(block_table, "block_table", torch.int32, shape, index),
+            _same(seq_lens, "seq_lens", torch.int32, (batch,), index),
+            _same(starts, "starts", torch.int32, (batch + 1,), index))
 
 
-def _rows3(t, name, dtypes, heads, head_dim, device):
-    """A [rows, heads, head_dim] tensor whose rows may lie apart (a slice of a wider projection)."""
+def _rows3(t, name, dtypes, heads, head_dim, index):
+    """The row stride of a [rows, heads, head_dim] tensor, whose rows may lie apart (a slice of a
+    wider projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
     if t.dtype not in dtypes:
         raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
-    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads):
         raise ValueError("%s has shape %s, expected [rows, %s, %d]"
-                         % (name, tuple(t.shape), "heads" if heads is None else heads, head_dim))
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim)):
+                         % (name, tuple(shape), "heads" if heads is None else heads, head_dim))
+    if (stride[2] != 1 or (shape[1] > 1 and stride[1] != head_dim)) and t.numel():
         raise ValueError("%s must have contiguous rows" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim
+    return stride[0] if shape[0] > 1 else shape[1] * head_dim
 
 
 def kv4_append(k, v, cache, block_table, seq_lens, starts, page_size: int, group: int = 64):
@@ -331,29 +363,36 @@ def kv4_append(k, v, cache, block_table, seq_lens, starts, page_size: int, group
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be 3-D [rows, kv_heads, head_dim]")
     T, H, D = k.shape
-    dev, batch = _check_kv4(cache, block_table, seq_lens, starts, D, page_size, group)
-    ks = _rows3(k, "k", _FLOATS, cache.shape[1], D, dev)
-    vs = _rows3(v, "v", (k.dtype,), H, D, dev)
+    index, batch, cp, tp, lp, sp = _check_kv4(cache, block_table, seq_lens, starts, D, page_size, group)
+    ks = _rows3(k, "k", _FLOATS, cache.shape[1], D, index)
+    vs = _rows3(v, "v", (k.dtype,), H, D, index)
     if v.shape[0] != T:
         raise ValueError("k and v have different numbers of rows")
-    _call("kv4_append", _ptr(k), _ptr(v), QL_F16 if k.dtype == torch.float16 else QL_F32, ks, vs, T, _ptr(cache),
-          cache.shape[0], page_size, H, D, group, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-          _ptr(starts), batch, _stream(cache))
+    _status("kv4_append", lib.kv4_append(
+        k.data_ptr(), v.data_ptr(), QL_F16 if k.dtype is torch.float16 else QL_F32, ks, vs, T, cp, cache.shape[0],
+        page_size, H, D, group, tp, block_table.shape[1], lp, sp, batch, _raw_stream(index)))
 
 
 def kv4_read(cache, block_table, seq_lens, starts, rows: int, head_dim: int, page_size: int, group: int = 64,
              dtype=torch.float16):
     """The last starts[b + 1] - starts[b] positions of each sequence, `rows` in all, as k and v
     [rows, kv_heads, head_dim] in dtype (fp16 or fp32)."""
-    dev, batch = _check_kv4(cache, block_table, seq_lens, starts, head_dim, page_size, group)
+    index, batch, cp, tp, lp, sp = _check_kv4(cache, block_table, seq_lens, starts, head_dim, page_size, group)
     if dtype not in _FLOATS:
         raise TypeError("dtype must be float16 or float32")
-    k = torch.empty((rows, cache.shape[1], head_dim), dtype=dtype, device=dev)
+    k = cache.new_empty((rows, cache.shape[1], head_dim), dtype=dtype)
     v = torch.empty_like(k)
-    _call("kv4_read", _ptr(cache), cache.shape[0], page_size, cache.shape[1], head_dim, group, _ptr(block_table),
-          block_table.shape[1], _ptr(seq_lens), _ptr(starts), batch, rows,
-          QL_F16 if dtype == torch.float16 else QL_F32, _ptr(k), _ptr(v), _stream(cache))
+    _status("kv4_read", lib.kv4_read(
+        cp, cache.shape[0], page_size, cache.shape[1], head_dim, group, tp, block_table.shape[1], lp, sp, batch, rows,
+        QL_F16 if dtype is torch.float16 else QL_F32, k.data_ptr(), v.data_ptr(), _raw_stream(index)))
     return k, v
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(*sizes):
+    need = _I64(0)
+    _call("attention_kv4_workspace_bytes", *sizes, ctypes.byref(need))
+    return need.value
 
 
 def attention_kv4(q, cache, block_table, seq_lens, starts, page_size: int, group: int = 64,
@@ -368,24 +407,28 @@ def attention_kv4(q, cache, block_table, seq_lens, starts, page_size: int, group
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be 3-D [rows, q_heads, head_dim]")
     T, HQ, D = q.shape
-    dev, batch = _check_kv4(cache, block_table, seq_lens, starts, D, page_size, group)
-    H = cache.shape[1]
-    qs = _rows3(q, "q", (torch.float16,), None, D, dev)
+    index, batch, cp, tp, lp, sp = _check_kv4(cache, block_table, seq_lens, starts, D, page_size, group)
+    pages, H, _ = cache.shape
+    qs = _rows3(q, "q", (torch.float16,), None, D, index)
     if H == 0 or HQ == 0 or HQ % H:
         raise ValueError("q has %d heads, not a multiple of the cache's %d" % (HQ, H))
+    width = block_table.shape[1]
     if max_q is None:
         max_q = max(1, T - batch + 1)
     if max_len is None:
-        max_len = max(1, block_table.shape[1] * page_size)
+        max_len = max(1, width * page_size)
     if scale is None:
         scale = D ** -0.5
-    out = _out(out, "out", (T, HQ, D), torch.float16, dev)
-    need = _I64(0)
-    _call("attention_kv4_workspace_bytes", T, HQ, H, D, batch, max_q, max_len, ctypes.byref(need))
-    ws = torch.empty((need.value,), dtype=torch.uint8, device=dev) if need.value else None
-    _call("attention_kv4", _ptr(q), qs, _ptr(out), T, HQ, _ptr(cache), cache.shape[0], page_size, H, D, group,
-          _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(starts), batch, max_q, max_len, scale,
-          window, _ptr(ws), need.value, _stream(cache))
+    if out is None:
+        out = q.new_empty((T, HQ, D))
+        op = out.data_ptr()
+    else:
+        op = _same(out, "out", torch.float16, (T, HQ, D), index)
+    need = _attention_workspace(T, HQ, H, D, batch, max_q, max_len, window)
+    ws = cache.new_empty((need,)) if need else None   # of the current stream, as the kernels are
+    _status("attention_kv4", lib.attention_kv4(
+        q.data_ptr(), qs, op, T, HQ, cp, pages, page_size, H, D, group, tp, width, lp, sp, batch, max_q, max_len,
+        scale, window, None if ws is None else ws.data_ptr(), need, _raw_stream(index)))
     return out
 
 

@@ -22,6 +22,8 @@
 //                 range to V's magnitude.
 // The running maximum is raised only when a score exceeds it by 2^8 (weights up to 2^14, sums
 // in fp32), so most steps have neither a reduction across lanes nor a rescaling of O.
+#include <algorithm>
+
 #include "kv4.h"
 
 namespace ql {
@@ -88,7 +90,7 @@ constexpr int vmcnt_le(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | (((
 // launch stub).
 __device__ inline void lds_copy16(const void* g, void* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_global_load_lds(g, (lds_ptr)lds, 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(g, (lds_ptr)lds, 16, 0, 2);   // nt: read once
 #endif
 }
 
@@ -320,8 +322,21 @@ __global__ __launch_bounds__(AT, D == 256 ? (NQ == 1 ? 2 : 1) : NQ == 1 ? 4 : 2)
         const int base = t.begin & ~(TB - 1);
         const int stretch = split_tokens(t, sp.stretch, sp.n);
         const int from = base + split * stretch, to = min(from + stretch, t.end);
-        if (split > 0 && from >= t.end)
-            continue;   // no tokens; split 0 always writes
+        // a split's maximum and sum for one (row, head), behind all splits' sums of values
+        auto split_stats = [&](int64_t at) {
+            return a.ws + ((int64_t)sp.n * a.rows * a.q_heads * D + (at * sp.n + split) * 2);
+        };
+        if (split > 0 && from >= t.end) {
+            // no tokens: a sum of 0, whose values nobody reads
+            for (int idx = tile * PER + threadIdx.x; idx < min(tile * PER + PER, t.rows * R); idx += AT) {
+                const int row = b.starts[seq] + idx / R;
+                if (row < a.rows) {
+                    float* st = split_stats((int64_t)row * a.q_heads + head * R + idx % R);
+                    st[0] = M_NONE, st[1] = 0.0f;
+                }
+            }
+            continue;
+        }
 
         const RG ring(b, c, seq, head, t.end);
         uint8_t* slots = lds + wave * (SLOTS * RG::BYTES);
@@ -572,80 +587,80 @@ __global__ __launch_bounds__(AT, D == 256 ? (NQ == 1 ? 2 : 1) : NQ == 1 ? 4 : 2)
 #pragma unroll
                     for (int e = 0; e < E; ++e)
                         ws[e] = v[e];
-                    if (threadIdx.x % 16 == 0) {
-                        float* st = a.ws + (int64_t)sp.n * a.rows * a.q_heads * D +
-                                    ((int64_t)split * a.rows * a.q_heads + at) * 2;
-                        st[0] = mx;
-                        st[1] = sum;
-                    }
+                    if (threadIdx.x % 16 == 0)
+                        split_stats(at)[0] = mx, split_stats(at)[1] = sum;
                 }
             }
         }
     }
 }
 
-// Joins the splits of one (row, head): their largest maximum and weights by all threads, then D
-// values by 256 / (D / 4) parts of the splits.
+// Joins the splits of one (row, head): v = sum_s 2^(m_s - max) v_s over l = sum_s 2^(m_s - max) l_s.
+// Two launches' latencies (a split's statistics, then its values) are most of it, so nothing
+// else is looked up: splits without tokens have left l = 0. One workgroup for many splits of few
+// rows, one wave for a few splits of many.
 constexpr int MAX_SPLITS = 256;
 
-template <int D>
-__global__ __launch_bounds__(AT) void attention_kv4_join_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b, Split sp, int per) {
-    constexpr int LANES = D / 4, PARTS = AT / LANES;
-    __shared__ f32x4 part[PARTS][LANES];
-    __shared__ float weight[MAX_SPLITS], red[AW][2];
-    static_assert(MAX_SPLITS == AT, "one split a thread");
-    const int R = a.q_heads / c.heads, tid = threadIdx.x;
-    const int64_t at = blockIdx.x, all = (int64_t)a.rows * a.q_heads;
-    const int row = (int)(at / a.q_heads), h = (int)(at % a.q_heads);
-    const int seq = kv4_seq(b, row), i = row - b.starts[seq];
-    const RowTile t = row_tile(b, c, seq, (i * R + h % R) / per, per, R, a.window);
-    const int stretch = split_tokens(t, sp.stretch, sp.n);
-    const int used = max(1, min(sp.n, (t.end - (t.begin & ~(TB - 1)) + stretch - 1) / stretch));
-    const float* st = a.ws + sp.n * all * D + at * 2;
+template <int D, int WAVES>
+__global__ __launch_bounds__(AT) void attention_kv4_join_kernel(const float* __restrict__ ws, _Float16* __restrict__ out,
+                                                                int64_t all, int n) {
+    constexpr int LANES = D / 4, PARTS = WAVES * WAVE / LANES, ROWS = AW / WAVES;
+    static_assert(PARTS >= 1, "a row's waves hold its values");
+    __shared__ float weight[ROWS][WAVES * WAVE], red[AW][2];
+    __shared__ f32x4 part[ROWS][PARTS][LANES];
+    const int group = threadIdx.x / (WAVES * WAVE), tid = threadIdx.x % (WAVES * WAVE);
+    const int64_t at = (int64_t)blockIdx.x * ROWS + group;
+    const float* st = ws + (int64_t)n * all * D + at * n * 2;
     float m = M_NONE, l = 0.0f;
-    if (tid < used) {
-        m = st[tid * all * 2];
-        l = st[tid * all * 2 + 1];
+    if (at < all && tid < n) {
+        m = st[2 * tid];
+        l = st[2 * tid + 1];
     }
     float top = m;
 #pragma unroll
     for (int o = WAVE / 2; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor(top, o, WAVE));
     if ((tid & (WAVE - 1)) == 0)
-        red[tid / WAVE][0] = top;
+        red[threadIdx.x / WAVE][0] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < AW; ++w)
-        top = fmaxf(top, red[w][0]);
-    const float f = __builtin_amdgcn_exp2f(m - top);
-    weight[tid] = f;
+    for (int w = 0; w < WAVES; ++w)
+        top = fmaxf(top, red[group * WAVES + w][0]);
+    const float f = l > 0.0f ? __builtin_amdgcn_exp2f(m - top) : 0.0f;
+    weight[group][tid] = f;
     float sum = l * f;
 #pragma unroll
     for (int o = WAVE / 2; o > 0; o >>= 1)
         sum += __shfl_xor(sum, o, WAVE);
     if ((tid & (WAVE - 1)) == 0)
-        red[tid / WAVE][1] = sum;
+        red[threadIdx.x / WAVE][1] = sum;
     __syncthreads();
     sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < AW; ++w)
-        sum += red[w][1];
+    for (int w = 0; w < WAVES; ++w)
+        sum += red[group * WAVES + w][1];
     const int d4 = tid % LANES, p = tid / LANES;
-    const float* src = a.ws + at * D + 4 * d4;
     f32x4 v = {0, 0, 0, 0};
+    if (at < all) {
+        const float* src = ws + at * D + 4 * d4;
 #pragma unroll 4
-    for (int s = p; s < used; s += PARTS)
-        v += *reinterpret_cast<const f32x4*>(src + s * all * D) * weight[s];
-    part[p][d4] = v;
+        for (int s = p; s < n; s += PARTS) {
+            const float w = weight[group][s];
+            if (w != 0.0f)   // a split without tokens wrote no values
+                v += *reinterpret_cast<const f32x4*>(src + s * all * D) * w;
+        }
+    }
+    part[group][p][d4] = v;
     __syncthreads();
-    if (p == 0) {
+    if (p == 0 && at < all) {
 #pragma unroll
         for (int k = 1; k < PARTS; ++k)
-            v += part[k][d4];
+            v += part[group][k][d4];
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        _Float16* to = out + at * D + 4 * d4;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            a.out[at * D + 4 * d4 + e] = (_Float16)(v[e] * inv);
+            to[e] = (_Float16)(v[e] * inv);
     }
 }
 
@@ -655,16 +670,20 @@ constexpr int64_t FILL = 512;   // workgroups that the chip holds at once
 inline int rows_per_tile(int64_t pairs) { return pairs <= 16 ? 16 : 32; }
 
 // Splits: two workgroups of four waves a CU fill the chip, so that many in all, each with at
-// least 256 tokens, and at most what the second kernel joins.
-Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len) {
+// least 256 tokens, and at most what the second kernel joins. Up to 640 tokens stay whole: the
+// join costs what 256 tokens do (32 heads of 128, 512 tokens 8.7 us whole, 9.5 us in halves;
+// 1024 tokens 12.8 us whole, 9.9 us in quarters).
+Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len, int window) {
     const int64_t pairs = (int64_t)max_q * (q_heads / kv_heads);
     constexpr int64_t unit = TB * AW;
+    if (window > 0)   // the positions that a sequence's rows see together
+        max_len = (int)std::min<int64_t>(max_len, (int64_t)window + max_q);
     Split s;
     s.tiles = (int)((pairs + rows_per_tile(pairs) - 1) / rows_per_tile(pairs));
     const int64_t base = (int64_t)batch * kv_heads * s.tiles;
     int64_t want = base > 0 ? (FILL + base - 1) / base : 1;
     want = want < MAX_SPLITS ? want : MAX_SPLITS;
-    int64_t stretch = (max_len + want - 1) / want;
+    int64_t stretch = max_len <= 5 * unit ? max_len : (max_len + want - 1) / want;
     stretch = stretch < 2 * unit ? 2 * unit : (stretch + unit - 1) / unit * unit;
     s.stretch = (int)stretch;
     s.n = (int)((max_len + stretch - 1) / stretch);
@@ -673,15 +692,16 @@ Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len) {
 
 }  // namespace
 
-int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len) {
-    const Split s = plan(q_heads, kv_heads, batch, max_q, max_len);
+int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
+                                int window) {
+    const Split s = plan(q_heads, kv_heads, batch, max_q, max_len, window);
     return s.n == 1 ? 0 : s.n * rows * q_heads * (D + 2);
 }
 
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream) {
     const int per = rows_per_tile((int64_t)a.max_q * (a.q_heads / c.heads));
-    const Split sp = plan(a.q_heads, c.heads, b.batch, a.max_q, a.max_len);
+    const Split sp = plan(a.q_heads, c.heads, b.batch, a.max_q, a.max_len, a.window);
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
         const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * sp.n * sp.tiles));
@@ -697,8 +717,14 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
             else
                 go(attention_kv4_decode_kernel<DD, GG, false, 2>);
         }
-        if (sp.n > 1)
-            attention_kv4_join_kernel<DD><<<dim3((uint32_t)(a.rows * a.q_heads)), AT, 0, stream>>>(a, c, b, sp, per);
+        if (sp.n > 1) {
+            const int64_t all = (int64_t)a.rows * a.q_heads;
+            if (sp.n > 16)
+                attention_kv4_join_kernel<DD, AW><<<dim3((uint32_t)all), AT, 0, stream>>>(a.ws, a.out, all, sp.n);
+            else
+                attention_kv4_join_kernel<DD, 1>
+                    <<<dim3((uint32_t)((all + AW - 1) / AW)), AT, 0, stream>>>(a.ws, a.out, all, sp.n);
+        }
         return launch_status();
     });
 }

@@ -477,21 +477,22 @@ ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, i
                                dtype == QL_F16, as_stream(stream));
 }
 
-static bool bad_kv4_attention(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t max_q, int64_t max_len) {
+static bool bad_kv4_attention(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t max_q, int64_t max_len,
+                              int64_t window) {
     return q_heads < 1 || q_heads > 4096 || kv_heads < 1 || q_heads % kv_heads != 0 || rows < 0 ||
            rows > (1 << 24) || rows * q_heads > ((int64_t)1 << 30) || max_q < 1 || max_q >= kMaxDim || max_len < 1 ||
-           max_len >= kMaxDim;
+           max_len >= kMaxDim || window < 0 || window >= kMaxDim;
 }
 
 ql_status attention_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t batch,
-                                        int64_t max_q, int64_t max_len, int64_t* bytes) {
-    if (bad_kv4_attention(rows, q_heads, kv_heads, max_q, max_len) || (D != 64 && D != 128 && D != 256) || batch < 0 ||
+                                        int64_t max_q, int64_t max_len, int64_t window, int64_t* bytes) {
+    if (bad_kv4_attention(rows, q_heads, kv_heads, max_q, max_len, window) || (D != 64 && D != 128 && D != 256) || batch < 0 ||
         batch > (1 << 20))
         return QL_ERR_SHAPE;
     if (!bytes)
         return QL_ERR_NULL;
     *bytes = 4 * ql::attention_kv4_workspace(rows, (int)q_heads, (int)kv_heads, (int)D, (int)batch, (int)max_q,
-                                             (int)max_len);
+                                             (int)max_len, (int)window);
     return QL_OK;
 }
 
@@ -502,13 +503,13 @@ ql_status attention_kv4(const void* q, int64_t q_stride, void* out, int64_t rows
                         int64_t max_len, float scale, int64_t window, void* workspace,
                         int64_t workspace_bytes, void* stream) {
     if (bad_kv4(rows, num_pages, page_size, kv_heads, D, group, table_width, batch) ||
-        bad_kv4_attention(rows, q_heads, kv_heads, max_q, max_len) || q_stride < q_heads * D || q_stride >= kMaxDim ||
-        !std::isfinite(scale) || window < 0 || window >= kMaxDim || workspace_bytes < 0)
+        bad_kv4_attention(rows, q_heads, kv_heads, max_q, max_len, window) || q_stride < q_heads * D ||
+        q_stride >= kMaxDim || !std::isfinite(scale) || workspace_bytes < 0)
         return QL_ERR_SHAPE;
     if (rows == 0)
         return QL_OK;
     if (workspace_bytes < 4 * ql::attention_kv4_workspace(rows, (int)q_heads, (int)kv_heads, (int)D, (int)batch,
-                                                          (int)max_q, (int)max_len))
+                                                          (int)max_q, (int)max_len, (int)window))
         return QL_ERR_SHAPE;
     if (!q || !out || (workspace_bytes > 0 && !workspace))
         return QL_ERR_NULL;

@@ -123,7 +123,8 @@ struct Kv4Attn {
     int64_t ws_floats;
 };
 // Floats of workspace that launch_attention_kv4 uses for these sizes.
-int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len);
+int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
+                                int window);
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream);
 

@@ -24,7 +24,7 @@ def lib():
     L.kv4_read.argtypes = [P, I64, I64, I64, I64, I64, P, I64, P, P, I64, I64, I, P, P, P]
     L.attention_kv4.argtypes = [P, I64, P, I64, I64, P, I64, I64, I64, I64, I64, P, I64, P, P, I64, I64, I64, F, I64,
                                 P, I64, P]
-    L.attention_kv4_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64, I64, ctypes.POINTER(I64)]
+    L.attention_kv4_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64, I64, I64, ctypes.POINTER(I64)]
     return L
 
 
@@ -86,10 +86,10 @@ def test_read(lib):
 def test_attention(lib):
     def need(**kw):
         n = ctypes.c_int64(-1)
-        a = dict(rows=4, HQ=4, H=2, D=128, batch=2, max_q=3, max_len=40)
+        a = dict(rows=4, HQ=4, H=2, D=128, batch=2, max_q=3, max_len=40, window=0)
         a.update({k: v for k, v in kw.items() if k in a})
         st = lib.attention_kv4_workspace_bytes(a["rows"], a["HQ"], a["H"], a["D"], a["batch"], a["max_q"], a["max_len"],
-                                               ctypes.byref(n))
+                                               a["window"], ctypes.byref(n))
         return st, n.value
 
     def f(q=A, qs=None, out=A, rows=4, HQ=4, cache=A, pages=9, P=16, H=2, D=128, G=64, table=A, width=3, lens=A,
@@ -109,5 +109,5 @@ def test_attention(lib):
     assert st == OK and n >= 0 and n % 4 == 0
     if n:
         assert f(rows=1, batch=1, max_q=1, max_len=1 << 17, wb=n - 4) == SHAPE
-    assert need(D=100)[0] == SHAPE and need(HQ=3)[0] == SHAPE and need(max_q=0)[0] == SHAPE
-    assert lib.attention_kv4_workspace_bytes(4, 4, 2, 128, 2, 3, 40, None) == NULL
+    assert need(D=100)[0] == SHAPE and need(HQ=3)[0] == SHAPE and need(max_q=0)[0] == SHAPE and need(window=-1)[0] == SHAPE
+    assert lib.attention_kv4_workspace_bytes(4, 4, 2, 128, 2, 3, 40, 0, None) == NULL
