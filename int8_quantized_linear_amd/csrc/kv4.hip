@@ -13,21 +13,29 @@ namespace {
 
 constexpr int KT = 256, KW = KT / WAVE;   // threads and waves per workgroup
 
-// 8 neighbouring values as fp32.
+// 8 neighbouring values as they lie in memory (fp16 or fp32), and as fp32.
 template <bool F16>
-__device__ inline void load8(float (&v)[8], const void* p, int64_t i) {
-    if constexpr (F16) {
-        const f16x8 h = *reinterpret_cast<const f16x8*>(reinterpret_cast<const _Float16*>(p) + i);
+struct Eight {
+    u32x4 w[F16 ? 1 : 2];
+    __device__ inline void load(const void* p, int64_t i) {
+        const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(p) + i * (F16 ? 2 : 4));
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = (float)h[e];
-    } else {
-        const f32x4* f = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = f[e / 4][e % 4];
+        for (int j = 0; j < (F16 ? 1 : 2); ++j)
+            w[j] = s[j];
     }
-}
+    __device__ inline void get(float (&v)[8]) const {
+        if constexpr (F16) {
+            const f16x8 h = __builtin_bit_cast(f16x8, w[0]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = (float)h[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __uint_as_float(w[e / 4][e % 4]);
+        }
+    }
+};
 
 // fp16 of a float, kept within fp16's finite range.
 __device__ inline _Float16 to_f16_sat(float v) {
@@ -36,31 +44,51 @@ __device__ inline _Float16 to_f16_sat(float v) {
 
 // clamp(round(a / s), 0, 15) with y = 1 / s correctly rounded: a / s as RN(q0 + (a - q0 s) y),
 // q0 = RN(a y), the correctly rounded quotient (Markstein) where nothing underflows; where
-// something does, a / s is below 2^-80 and the code 0 on either path.
+// something does, a / s is below 2^-80 and the code 0 on either path. Clamping first changes no
+// code (the bounds are integers), and adding 1.5 2^23 rounds half to even into the low bits:
+// the result is the code + ROUNDED.
+constexpr float ROUND = 12582912.0f;
+constexpr uint32_t ROUNDED = 0x4B400000u;
 __device__ inline uint32_t code4(float a, float s, float y) {
     const float q0 = __fmul_rn(a, y);
     const float q = fmaf(fmaf(-q0, s, a), y, q0);
-    return (uint32_t)__builtin_amdgcn_fmed3f(rintf(q), 0.0f, 15.0f);
+    return __float_as_uint(__fadd_rn(__builtin_amdgcn_fmed3f(q, 0.0f, 15.0f), ROUND));
+}
+
+// Place of code e in a word: K's pairs of neighbours meet in the halves, V's bytes hold pairs.
+constexpr int k_shift(int e) { return 16 * (e & 1) + 4 * (e >> 1); }
+constexpr int v_shift(int e) { return 4 * e; }
+
+// Eight codes in one word; the sum of the shifted ROUNDED wraps to a constant, taken off first.
+template <bool K>
+__device__ inline uint32_t codes8(const float (&x)[8], float low, float s, float y) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w -= ROUNDED << (K ? k_shift(e) : v_shift(e));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w += code4(x[e] - low, s, y) << (K ? k_shift(e) : v_shift(e));
+    return w;
 }
 
 // A wave takes the runs of up to 8 rows that start among its `per` rows: rows of one sequence
-// whose positions lie in one aligned group of 8 (a unit of V's layout, inside one page). Lanes of
-// D / 8 take a token, 8 values each, so that a lane's K codes are one word, and G / 8 lanes share
-// a scale. V's codes of a full run are gathered through LDS into the 16-byte units of 8 tokens;
-// a part of a run writes its tokens' 16 bits, so that its neighbours keep theirs.
-//
-// per = 8 for prompts (one run a wave), 1 where most sequences bring one row. Bound by the rows'
-// read: prompts of 7108 rows, 32 heads of 128, 280 MB with the cache, see the table of cases.
+// whose positions lie in one aligned group of 8 (a unit of V's layout, inside one page), for the
+// heads of its group, the next head's rows in flight while one is written. Lanes of D / 8 take a
+// token, 8 values each, so that a lane's K codes are one word, and G / 8 lanes share a scale.
+// V's codes of a full run are gathered through LDS into the 16-byte units of 8 tokens; a part of
+// a run writes its tokens' 16 bits, so that its neighbours keep theirs.
 template <int D, int G, bool F16>
 __global__ __launch_bounds__(KT) void kv4_append_kernel(const void* __restrict__ k, const void* __restrict__ v,
                                                         int64_t k_stride, int64_t v_stride, int rows, int per,
-                                                        Kv4Cache c, Kv4Batch b) {
+                                                        int head_groups, Kv4Cache c, Kv4Batch b) {
     using L = Kv4Layout<D, G>;
     constexpr int LPT = D / 8, TPP = WAVE / LPT, PASSES = 8 / TPP;
     __shared__ __attribute__((aligned(16))) uint16_t units[KW][D / 4][8];
-    const int P = 1 << c.page_log2, lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
-    const int head = blockIdx.x % c.heads;
-    const int r0 = (int)(blockIdx.x / c.heads * KW + wave) * per;
+    const int P = 1 << c.page_log2, lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int head0 = blockIdx.x % head_groups;
+    const int r0 = (int)(blockIdx.x / head_groups * KW + wave) * per;
 
     // lane i < per looks at row r0 + i: does a run start there?
     int seq = 0, pos = -1, n = 0;
@@ -78,87 +106,94 @@ __global__ __launch_bounds__(KT) void kv4_append_kernel(const void* __restrict__
         runs &= runs - 1;
         const int rseq = __builtin_amdgcn_readlane(seq, i), rpos = __builtin_amdgcn_readlane(pos, i);
         const int rn = __builtin_amdgcn_readlane(n, i);
-        uint8_t* page = kv4_page(b, c, rseq, rpos, head);
         const int slot0 = rpos & (P - 1) & ~7, t0 = rpos & 7;   // the run is tokens t0 .. t0 + rn - 1 of 8
         const int d0 = (lane % LPT) * 8, g = d0 / G;
-        float x[2][PASSES][8];
+        Eight<F16> next[2][PASSES];
+        auto load = [&](int head) {
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int t = p * TPP + lane / LPT - t0;
-            if (t >= 0 && t < rn) {
-                const int64_t row = r0 + i + t;
-                load8<F16>(x[0][p], k, row * k_stride + head * D + d0);
-                load8<F16>(x[1][p], v, row * v_stride + head * D + d0);
+            for (int p = 0; p < PASSES; ++p) {
+                const int t = p * TPP + lane / LPT - t0;
+                if (t >= 0 && t < rn) {
+                    const int64_t row = r0 + i + t;
+                    next[0][p].load(k, row * k_stride + head * D + d0);
+                    next[1][p].load(v, row * v_stride + head * D + d0);
+                }
             }
-        }
+        };
+        load(head0);
+        uint8_t* page = kv4_page(b, c, rseq, rpos, head0);
+        for (int head = head0; head < c.heads; head += head_groups) {
+            Eight<F16> raw[2][PASSES];
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int tok = p * TPP + lane / LPT, slot = slot0 + tok;
-            const bool on = tok >= t0 && tok < t0 + rn;
+            for (int p = 0; p < PASSES; ++p)
+                raw[0][p] = next[0][p], raw[1][p] = next[1][p];
+            if (head + head_groups < c.heads)
+                load(head + head_groups);
 #pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const float(&xs)[8] = x[which][p];
-                float lo = xs[0], hi = xs[0];
+            for (int p = 0; p < PASSES; ++p) {
+                const int tok = p * TPP + lane / LPT, slot = slot0 + tok;
+                const bool on = tok >= t0 && tok < t0 + rn;
 #pragma unroll
-                for (int e = 1; e < 8; ++e) {
-                    lo = fminf(lo, xs[e]);
-                    hi = fmaxf(hi, xs[e]);
-                }
+                for (int which = 0; which < 2; ++which) {
+                    float x[8];
+                    raw[which][p].get(x);
+                    float lo = x[0], hi = x[0];
 #pragma unroll
-                for (int o = G / 16; o > 0; o >>= 1) {
-                    lo = fminf(lo, __shfl_xor(lo, o, WAVE));
-                    hi = fmaxf(hi, __shfl_xor(hi, o, WAVE));
-                }
-                const _Float16 lo16 = to_f16_sat(lo);
-                const float lf = (float)lo16;
-                const _Float16 least = (_Float16)5.9604644775390625e-08f;   // 2^-24
-                _Float16 s16 = to_f16_sat(fmaxf((hi - lf) / 15.0f, 0.0f));
-                s16 = s16 > least ? s16 : least;
-                const float s = (float)s16, y = 1.0f / s;
-                if (on && lane % (G / 8) == 0) {
-                    reinterpret_cast<_Float16*>(page + (which ? L::v_scale(P, g) : L::k_scale(P, g)))[slot] = s16;
-                    reinterpret_cast<_Float16*>(page + (which ? L::v_low(P, g) : L::k_low(P, g)))[slot] = lo16;
-                }
-                if (which == 0) {
-                    uint32_t w = 0;
+                    for (int e = 1; e < 8; ++e) {
+                        lo = fminf(lo, x[e]);
+                        hi = fmaxf(hi, x[e]);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w |= code4(xs[e] - lf, s, y) << (16 * (e & 1) + 4 * (e >> 1));
-                    if (on)
-                        reinterpret_cast<uint32_t*>(page + L::k_codes(slot))[((d0 % 32) / 8) * (D / 32) + d0 / 32] = w;
-                } else {
-                    // bytes of d pairs, of 4 quads; the other half of each is 32 values away, in
-                    // lane ^ 4: either lane completes two quads
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w |= code4(xs[e] - lf, s, y) << (4 * e);
-                    const uint32_t z = __shfl_xor(w, 4, WAVE);
-                    const bool up = lane & 4;
-                    const uint32_t a = up ? z >> 16 : w, h = up ? w >> 16 : z;
-                    const uint32_t two = (a & 0xFF) | (h & 0xFF) << 8 | (a & 0xFF00) << 8 | (h & 0xFF00) << 16;
-                    const int quad = d0 / 64 * 16 + d0 % 32 / 2 + (up ? 2 : 0);
-                    if (rn == 8) {
-                        units[wave][quad][tok] = (uint16_t)two;
-                        units[wave][quad + 1][tok] = (uint16_t)(two >> 16);
-                    } else if (on) {
-                        uint16_t* to = reinterpret_cast<uint16_t*>(page + L::v_codes(P, slot / 8)) + slot % 8;
-                        to[quad * 8] = (uint16_t)two;
-                        to[quad * 8 + 8] = (uint16_t)(two >> 16);
+                    for (int o = G / 16; o > 0; o >>= 1) {
+                        lo = fminf(lo, __shfl_xor(lo, o, WAVE));
+                        hi = fmaxf(hi, __shfl_xor(hi, o, WAVE));
+                    }
+                    const _Float16 lo16 = to_f16_sat(lo);
+                    const float lf = (float)lo16;
+                    const _Float16 least = (_Float16)5.9604644775390625e-08f;   // 2^-24
+                    _Float16 s16 = to_f16_sat(fmaxf((hi - lf) / 15.0f, 0.0f));
+                    s16 = s16 > least ? s16 : least;
+                    const float s = (float)s16, y = 1.0f / s;
+                    if (on && lane % (G / 8) == 0) {
+                        reinterpret_cast<_Float16*>(page + (which ? L::v_scale(P, g) : L::k_scale(P, g)))[slot] = s16;
+                        reinterpret_cast<_Float16*>(page + (which ? L::v_low(P, g) : L::k_low(P, g)))[slot] = lo16;
+                    }
+                    if (which == 0) {
+                        const uint32_t w = codes8<true>(x, lf, s, y);
+                        if (on)
+                            reinterpret_cast<uint32_t*>(page + L::k_codes(slot))[((d0 % 32) / 8) * (D / 32) + d0 / 32] = w;
+                    } else {
+                        // bytes of d pairs, of 4 quads; the other half of each is 32 values away,
+                        // in lane ^ 4: either lane completes two quads
+                        const uint32_t w = codes8<false>(x, lf, s, y);
+                        const uint32_t z = __shfl_xor(w, 4, WAVE);
+                        const bool up = lane & 4;
+                        const uint32_t a = up ? z >> 16 : w, h = up ? w >> 16 : z;
+                        const uint32_t two = (a & 0xFF) | (h & 0xFF) << 8 | (a & 0xFF00) << 8 | (h & 0xFF00) << 16;
+                        const int quad = d0 / 64 * 16 + d0 % 32 / 2 + (up ? 2 : 0);
+                        if (rn == 8) {
+                            units[wave][quad][tok] = (uint16_t)two;
+                            units[wave][quad + 1][tok] = (uint16_t)(two >> 16);
+                        } else if (on) {
+                            uint16_t* to = reinterpret_cast<uint16_t*>(page + L::v_codes(P, slot / 8)) + slot % 8;
+                            to[quad * 8] = (uint16_t)two;
+                            to[quad * 8 + 8] = (uint16_t)(two >> 16);
+                        }
                     }
                 }
             }
-        }
-        if (rn == 8) {
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            if (lane < D / 4)
-                *reinterpret_cast<u32x4*>(page + L::v_codes(P, slot0 / 8) + lane * 16) =
-                    *reinterpret_cast<const u32x4*>(units[wave][lane]);
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if (rn == 8) {
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                if (lane < D / 4)
+                    *reinterpret_cast<u32x4*>(page + L::v_codes(P, slot0 / 8) + lane * 16) =
+                        *reinterpret_cast<const u32x4*>(units[wave][lane]);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            }
+            page += head_groups * c.head_bytes;
         }
     }
 }
@@ -178,50 +213,66 @@ __device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
     }
 }
 
-// One thread per (row, head) and 16 values of K and of V: d = 64 c + 8 kg + 0 .. 7 and 32 more,
-// which are two neighbouring words of K and the 4 quads 4 kg .. 4 kg + 3 of V's chunk c.
+// Lanes of D / 16 take a row, 16 values of K and of V each: d = 64 c + 8 kg + 0 .. 7 and 32 more,
+// which are two neighbouring words of K and the 4 quads 4 kg .. 4 kg + 3 of V's chunk c. A wave
+// has 1024 / D neighbouring rows, so that V's units of 8 tokens are read whole, and goes through
+// the heads of its group.
 template <int D, int G, bool F16>
-__global__ __launch_bounds__(KT) void kv4_read_kernel(Kv4Cache c, Kv4Batch b, int rows, void* __restrict__ k_out,
-                                                      void* __restrict__ v_out) {
+__global__ __launch_bounds__(KT) void kv4_read_kernel(Kv4Cache c, Kv4Batch b, int rows, int head_groups,
+                                                      void* __restrict__ k_out, void* __restrict__ v_out) {
     using L = Kv4Layout<D, G>;
-    const int P = 1 << c.page_log2;
-    const int64_t id = (int64_t)blockIdx.x * KT + threadIdx.x;
-    const int part = (int)(id % (D / 16)), ch = part / 4, kg = part % 4;
-    const int64_t rh = id / (D / 16);
-    const int head = (int)(rh % c.heads);
-    if (rh / c.heads >= rows)
+    constexpr int LPR = D / 16, RPW = WAVE / LPR;
+    const int P = 1 << c.page_log2, lane = threadIdx.x & (WAVE - 1);
+    const int row = (int)(blockIdx.x / head_groups * KW + threadIdx.x / WAVE) * RPW + lane / LPR;
+    if (row >= rows)
         return;
-    const int row = (int)(rh / c.heads);
+    const int head0 = blockIdx.x % head_groups, ch = lane % LPR / 4, kg = lane % 4, d0 = ch * 64 + kg * 8;
     const int seq = kv4_seq(b, row);
     const int len = kv4_len(b, c, seq), pos = kv4_pos(b, seq, len, row);
-    const int d0 = ch * 64 + kg * 8;
-    float kx[2][8] = {}, vx[2][8] = {};
-    if (pos >= 0 && pos < len) {
-        const uint8_t* page = kv4_page(b, c, seq, pos, head);
-        const int slot = pos & (P - 1);
-        const u32x2 kw = *reinterpret_cast<const u32x2*>(page + L::k_codes(slot) + (kg * (D / 32) + 2 * ch) * 4);
-        const uint16_t* vq = reinterpret_cast<const uint16_t*>(page + L::v_codes(P, slot / 8)) + (ch * 16 + kg * 4) * 8 +
-                             slot % 8;
-        const uint32_t q[4] = {vq[0], vq[8], vq[16], vq[24]};
+    const bool on = pos >= 0 && pos < len;
+    const uint8_t* page = on ? kv4_page(b, c, seq, pos, head0) : nullptr;
+    const int slot = pos & (P - 1);
+    const int k_at = L::k_codes(slot) + (kg * (D / 32) + 2 * ch) * 4;
+    const int v_at = L::v_codes(P, slot / 8) + (ch * 16 + kg * 4) * 16 + slot % 8 * 2;
+#pragma unroll 2
+    for (int head = head0; head < c.heads; head += head_groups) {
+        float kx[2][8] = {}, vx[2][8] = {};
+        if (on) {
+            const u32x2 kw = *reinterpret_cast<const u32x2*>(page + k_at);
+            const uint16_t* vq = reinterpret_cast<const uint16_t*>(page + v_at);
+            const uint32_t q[4] = {vq[0], vq[8], vq[16], vq[24]};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int g = (d0 + 32 * h) / G;
-            const float ks = (float)reinterpret_cast<const _Float16*>(page + L::k_scale(P, g))[slot];
-            const float kl = (float)reinterpret_cast<const _Float16*>(page + L::k_low(P, g))[slot];
-            const float vs = (float)reinterpret_cast<const _Float16*>(page + L::v_scale(P, g))[slot];
-            const float vl = (float)reinterpret_cast<const _Float16*>(page + L::v_low(P, g))[slot];
+            for (int h = 0; h < 2; ++h) {
+                const int g = (d0 + 32 * h) / G;
+                const float ks = (float)reinterpret_cast<const _Float16*>(page + L::k_scale(P, g))[slot];
+                const float kl = (float)reinterpret_cast<const _Float16*>(page + L::k_low(P, g))[slot];
+                const float vs = (float)reinterpret_cast<const _Float16*>(page + L::v_scale(P, g))[slot];
+                const float vl = (float)reinterpret_cast<const _Float16*>(page + L::v_low(P, g))[slot];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                kx[h][e] = fmaf(ks, (float)((kw[h] >> (16 * (e & 1) + 4 * (e >> 1))) & 15), kl);
-                vx[h][e] = fmaf(vs, (float)((q[e / 2] >> (8 * h + 4 * (e & 1))) & 15), vl);
+                for (int e = 0; e < 8; ++e) {
+                    kx[h][e] = fmaf(ks, (float)((kw[h] >> k_shift(e)) & 15), kl);
+                    vx[h][e] = fmaf(vs, (float)((q[e / 2] >> (8 * h + 4 * (e & 1))) & 15), vl);
+                }
             }
         }
-    }
+        const int64_t at = ((int64_t)row * c.heads + head) * D + d0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        store8<F16>(k_out, rh * D + d0 + 32 * h, kx[h]);
-        store8<F16>(v_out, rh * D + d0 + 32 * h, vx[h]);
+        for (int h = 0; h < 2; ++h) {
+            store8<F16>(k_out, at + 32 * h, kx[h]);
+            store8<F16>(v_out, at + 32 * h, vx[h]);
+        }
+        page += head_groups * c.head_bytes;
     }
+}
+
+// Groups of heads, each a workgroup's loop: one head each until that makes FILL workgroups.
+constexpr int64_t FILL = 2048;   // workgroups that keep every CU busy
+
+inline int groups_of_heads(int64_t blocks, int heads) {
+    int n = heads;
+    while (n > 1 && n % 2 == 0 && blocks * n / 2 >= FILL)
+        n /= 2;
+    return n;
 }
 
 }  // namespace
@@ -230,12 +281,15 @@ ql_status launch_kv4_append(const void* k, const void* v, bool f16, int64_t k_st
                             const Kv4Cache& c, int D, int G, const Kv4Batch& b, hipStream_t stream) {
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
+        // runs of 8 rows a wave for prompts, single rows where most sequences bring one
         const int per = rows > 4 * (int64_t)b.batch ? 8 : 1;
-        const dim3 grid((uint32_t)((rows + per * KW - 1) / (per * KW) * c.heads));
+        const int64_t blocks = (rows + per * KW - 1) / (per * KW);
+        const int hg = groups_of_heads(blocks, c.heads);
+        const dim3 grid((uint32_t)(blocks * hg));
         if (f16)
-            kv4_append_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, per, c, b);
+            kv4_append_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, per, hg, c, b);
         else
-            kv4_append_kernel<DD, GG, false><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, per, c, b);
+            kv4_append_kernel<DD, GG, false><<<grid, KT, 0, stream>>>(k, v, k_stride, v_stride, (int)rows, per, hg, c, b);
         return launch_status();
     });
 }
@@ -244,12 +298,14 @@ ql_status launch_kv4_read(const Kv4Cache& c, int D, int G, const Kv4Batch& b, in
                           bool f16, hipStream_t stream) {
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
-        const int64_t n = rows * c.heads * (DD / 16);
-        const dim3 grid((uint32_t)((n + KT - 1) / KT));
+        constexpr int per = KW * (1024 / DD);
+        const int64_t blocks = (rows + per - 1) / per;
+        const int hg = groups_of_heads(blocks, c.heads);
+        const dim3 grid((uint32_t)(blocks * hg));
         if (f16)
-            kv4_read_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(c, b, (int)rows, k_out, v_out);
+            kv4_read_kernel<DD, GG, true><<<grid, KT, 0, stream>>>(c, b, (int)rows, hg, k_out, v_out);
         else
-            kv4_read_kernel<DD, GG, false><<<grid, KT, 0, stream>>>(c, b, (int)rows, k_out, v_out);
+            kv4_read_kernel<DD, GG, false><<<grid, KT, 0, stream>>>(c, b, (int)rows, hg, k_out, v_out);
         return launch_status();
     });
 }
