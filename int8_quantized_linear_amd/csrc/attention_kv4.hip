@@ -666,19 +666,32 @@ __global__ __launch_bounds__(AT) void attention_kv4_join_kernel(const float* __r
 
 // Prompt kernel (many rows of a sequence): bound by the matrix cores and the softmax beside them.
 // A workgroup of eight waves takes 128 NQ (row, head) pairs, 16 NQ a wave, and steps through the
-// tokens in blocks of 64 that all its waves share: each thread turns its part of the block's
+// tokens in blocks of PB that all its waves share: each thread turns its part of the block's
 // codes into operands once, in LDS, in 16-byte units (8 d of a token for K, 8 tokens of one d for
-// V, neighbouring lanes' units side by side). Two buffers, one barrier a block; a block's codes
-// are read from memory two blocks ahead, into registers. As in the decode kernel K's operand is
-// its codes and V's its values. A score is
+// V, neighbouring lanes' units side by side). As in the decode kernel K's operand is its codes
+// and V's its values. A score is
 //   sum_g s_tg (sum_{d in g} c q_d) + sum_g low_tg (sum_{d in g} q_d):
 // the second sum is a product over groups, taken on the matrix cores too and exactly, with low in
 // two bf16 terms (11 bits) and the sums of q in three (24 bits): 6 of the 8 slots of a group, so
 // that one product serves 4 groups. A score then costs one fused multiply-add a group.
-constexpr int PT = 512, PB = 64;   // threads, tokens of a block
+//
+// A block has two phases, products (P V of the block before, then S) and vector work (softmax,
+// the operands of the block after next, loads of the one after that). Each SIMD holds a wave of
+// either half of the workgroup, and the halves run one phase apart, with a barrier at each
+// phase's end: one wave's products run beside the other's vector work. What block j's operands
+// overwrite has then been read: K's of block j - 3 (three buffers), V's of j - 4 (four).
+constexpr int PT = 512;   // threads
+constexpr int prompt_block(int D) { return D == 256 ? 32 : 64; }   // tokens of a block: 126 KB of LDS
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Workgroup barrier for LDS alone: loads into registers stay in flight across it.
+__device__ inline void phase_end() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 // The leading 8 bits of v, a bf16 value.
 __device__ inline float bf16_part(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
@@ -691,11 +704,12 @@ __device__ inline bf16x8 bf16_terms(float a, float b, float c, float d, float e,
 template <int D, int G, bool BIG, int NQ>
 __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b, int tiles) {
     using L = Kv4Layout<D, G>;
-    constexpr int NI = D / 32, NC = D / 64, PER = 128 * NQ, NP = (D * PB / 16 + PT - 1) / PT;
-    constexpr int NG = D / G, NL = (NG + 3) / 4;
-    __shared__ __attribute__((aligned(16))) f16x8 kt[2][D / 8][PB], vt[2][PB / 8][D];
-    __shared__ __attribute__((aligned(16))) u32x4 lowt[2][4 * NL][PB];   // low's terms
-    __shared__ __attribute__((aligned(16))) _Float16 sct[2][NG][PB];
+    constexpr int PB = prompt_block(D), XT = PB / 16, NI = D / 32, NG = D / G, NL = (NG + 3) / 4, PER = 128 * NQ;
+    constexpr int PARTS = D * PB / 16;   // threads' parts of a block
+    static_assert(PARTS <= PT, "one part a thread");
+    __shared__ __attribute__((aligned(16))) f16x8 kt[3][D / 8][PB], vt[4][PB / 8][D];
+    __shared__ __attribute__((aligned(16))) u32x4 lowt[3][NG][PB];   // low's terms
+    __shared__ __attribute__((aligned(16))) _Float16 sct[3][NG][PB];
     const int R = a.q_heads / c.heads, P = 1 << c.page_log2;
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), n = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -709,11 +723,18 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
     const float kappa = fmaxf(fabsf(a.scale) * 1.44269504088896f * 16777216.0f, 1e-30f);   // as in the decode kernel
     const float sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
 
+    // The thread's part of a block: of K two words, d = 32 (2 j + z) + 8 kgk .., of one token; of V
+    // two d, 64 (quad / 16) + 32 half + 2 (quad % 16) + 0, 1, of 8 tokens.
+    const int tok = tid % PB, kgk = tid / PB & 3, j = tid / PB >> 2;
+    const int place = (tok & ~31) | (tok & 4) << 2 | (tok & 24) >> 1 | (tok & 3);   // its row of the products
+    const int quad = tid % (D / 4), half = tid / (D / 4) & 1, t8 = tid / (D / 2);
+    const bool mine = PARTS == PT || tid < PARTS;
+
     for (int tile = tile0;; tile += tiles) {
         const RowTile t = row_tile(b, c, seq, tile, PER, R, a.window);
         if (tile * PER >= t.rows * R)
             return;
-        const int from = t.begin & ~(PB - 1), to = t.end;
+        const int from = t.begin & ~(PB - 1), nb = t.end > from ? (t.end - from + PB - 1) / PB : 0;
 
         f16x8 q[NQ][NI];
         bf16x8 ql[NQ][NL];   // lane (n, kg): the terms of the sum of q over group kg (+ 4)
@@ -745,27 +766,25 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
             }
 #pragma unroll
             for (int y = 0; y < NL; ++y) {
-                float mine = 0.0f;
+                float own = 0.0f;
 #pragma unroll
                 for (int g = 4 * y; g < NG && g < 4 * y + 4; ++g) {
                     qsum[g] += __shfl_xor(qsum[g], 16, WAVE);
                     qsum[g] += __shfl_xor(qsum[g], 32, WAVE);
-                    mine = kg == g - 4 * y ? qsum[g] : mine;
+                    own = kg == g - 4 * y ? qsum[g] : own;
                 }
-                mine *= sign * 5.9604644775390625e-08f;   // 2^-24
-                const float q1 = bf16_part(mine), q2 = bf16_part(mine - q1), q3 = mine - q1 - q2;
+                own *= sign * 5.9604644775390625e-08f;   // 2^-24
+                const float q1 = bf16_part(own), q2 = bf16_part(own - q1), q3 = own - q1 - q2;
                 ql[u][y] = bf16_terms(q1, q2, q3, q1, q2, q3);
             }
         }
-        // positions that the wave's rows see: some row, and every row
+        // positions that all of the wave's rows see
         const int w0 = tile * PER + wave * 16 * NQ, wl = min(w0 + 16 * NQ - 1, t.rows * R - 1);
-        const bool rows_here = w0 < t.rows * R;
-        const int w_end = rows_here ? max(0, t.first + wl / R + 1) : 0;
-        const int w_begin = a.window ? max(0, t.first + w0 / R + 1 - a.window) : 0;
-        const int w_all_end = rows_here ? max(0, t.first + w0 / R + 1) : 0;
+        const int w_all_end = max(0, t.first + w0 / R + 1);
         const int w_all_begin = a.window ? max(0, t.first + wl / R + 1 - a.window) : 0;
 
         f32x4 o[NQ][D / 16], l[NQ];
+        f16x8 p[NQ][XT / 2];
         float m[NQ];
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
@@ -778,139 +797,148 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
         const _Float16 one = (_Float16)1.0f;
         const f16x8 ones = {one, one, one, one, one, one, one, one};
 
-        // a thread's parts of a block: part p of K is (token, kg, i pair), of V (t8, quad, half)
-        u32x2 kw[NP];
-        _Float16 ks[NP][2], kl[NP][2];
-        u32x4 vw[NP], vs[NP], vl[NP];
+        u32x2 kw;
+        _Float16 ks[2], kl[2];
+        u32x4 vw, vs, vl;
         const int32_t* table = b.table + (int64_t)seq * b.width;
-        auto page = [&](int pos) {
-            uint32_t p = (uint32_t)table[min(pos, t.end - 1) >> c.page_log2];
-            p = p < (uint32_t)c.pages ? p : (uint32_t)c.pages - 1;
-            return c.data + ((int64_t)p * c.heads + head) * c.head_bytes;
+        auto page = [&](int pos, auto uniform) {
+            const int32_t* e = table + (min(pos, t.end - 1) >> c.page_log2);
+            uint32_t pg = decltype(uniform)::value ? table_entry(e) : (uint32_t)*e;
+            pg = pg < (uint32_t)c.pages ? pg : (uint32_t)c.pages - 1;
+            return c.data + ((int64_t)pg * c.heads + head) * c.head_bytes;
         };
-        auto load = [&](int t0) {
+        // BIG: the block lies in one page
+        auto load = [&](int i) {
+            const int t0 = from + i * PB, in = t0 & (P - 1);
+            if (mine) {
+                const uint8_t* pk = BIG ? page(t0, std::true_type{}) : page(t0 + tok, std::false_type{});
+                const int slot = BIG ? in + tok : (t0 + tok) & (P - 1);
+                kw = *reinterpret_cast<const u32x2*>(pk + (L::k_codes(slot) + (kgk * NI + 2 * j) * 4));
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const int at = p * PT + tid;
-                if (NP * PT == D * PB / 16 || at < D * PB / 16) {
-                    const int tok = at % PB, part = at / PB, kgk = part & 3, j = part >> 2;
-                    const uint8_t* pk = page(BIG ? t0 + (tok & ~31) : t0 + tok);
-                    const int slot = (t0 + tok) & (P - 1);
-                    kw[p] = *reinterpret_cast<const u32x2*>(pk + L::k_codes(slot) + (kgk * NI + 2 * j) * 4);
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int g = (2 * j + z) * 32 / G;
-                        ks[p][z] = reinterpret_cast<const _Float16*>(pk + L::k_scale(P, g))[slot];
-                        kl[p][z] = reinterpret_cast<const _Float16*>(pk + L::k_low(P, g))[slot];
-                    }
-                    // quads fastest, then halves, then t8
-                    const int quad = at % (D / 4), half = at / (D / 4) & 1, t8 = at / (D / 2);
-                    const uint8_t* pv = page(t0 + 8 * t8);
-                    const int vslot = (t0 + 8 * t8) & (P - 1);
-                    vw[p] = *reinterpret_cast<const u32x4*>(pv + L::v_codes(P, vslot / 8) + quad * 16);
-                    const int g = (quad / 16 * 64 + half * 32) / G;
-                    vs[p] = *reinterpret_cast<const u32x4*>(pv + L::v_scale(P, g) + 2 * vslot);
-                    vl[p] = *reinterpret_cast<const u32x4*>(pv + L::v_low(P, g) + 2 * vslot);
+                for (int z = 0; z < 2; ++z) {
+                    const int g = (2 * j + z) * 32 / G;
+                    ks[z] = *reinterpret_cast<const _Float16*>(pk + (L::k_scale(P, g) + 2 * slot));
+                    kl[z] = *reinterpret_cast<const _Float16*>(pk + (L::k_low(P, g) + 2 * slot));
                 }
+                const uint8_t* pv = BIG ? pk : page(t0 + 8 * t8, std::false_type{});
+                const int vslot = BIG ? in + 8 * t8 : (t0 + 8 * t8) & (P - 1);
+                vw = *reinterpret_cast<const u32x4*>(pv + (L::v_codes(P, vslot / 8) + quad * 16));
+                const int g = (quad / 16 * 64 + half * 32) / G;
+                vs = *reinterpret_cast<const u32x4*>(pv + (L::v_scale(P, g) + 2 * vslot));
+                vl = *reinterpret_cast<const u32x4*>(pv + (L::v_low(P, g) + 2 * vslot));
             }
         };
-        auto put = [&](int buf, int t0) {
-            const bool cut = t0 < t.begin || t0 + PB > t.end;   // holds positions that no row sees
+        auto put = [&](int i, int kb, int vb) {
+            const int t0 = from + i * PB;
+            if (mine) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const int at = p * PT + tid;
-                if (NP * PT == D * PB / 16 || at < D * PB / 16) {
-                    const int tok = at % PB, part = at / PB, kgk = part & 3, j = part >> 2;
-                    // a token's place: the products' rows, 8 x + 4 h + y at 16 h + 4 x + y of 32
-                    const int place = (tok & ~31) | (tok & 4) << 2 | (tok & 24) >> 1 | (tok & 3);
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        kt[buf][(2 * j + z) * 4 + kgk][place] = codes_raw(kw[p][z]);
-                        const int g = (2 * j + z) * 32 / G;
-                        if (kgk == 0 && (2 * j + z) * 32 % G == 0) {   // one thread a token and group
-                            sct[buf][g][tok] = ks[p][z];
-                            const float low = (float)kl[p][z], l1 = bf16_part(low), l2 = low - l1;
-                            lowt[buf][g][place] = __builtin_bit_cast(u32x4, bf16_terms(l1, l1, l1, l2, l2, l2));
-                        }
+                for (int z = 0; z < 2; ++z) {
+                    kt[kb][(2 * j + z) * 4 + kgk][place] = codes_raw(kw[z]);
+                    const int g = (2 * j + z) * 32 / G;
+                    if (kgk == 0 && (2 * j + z) * 32 % G == 0) {   // one thread a token and group
+                        sct[kb][g][tok] = ks[z];
+                        const float low = (float)kl[z], l1 = bf16_part(low), l2 = low - l1;
+                        lowt[kb][g][place] = __builtin_bit_cast(u32x4, bf16_terms(l1, l1, l1, l2, l2, l2));
                     }
-                    const int quad = at % (D / 4), half = at / (D / 4) & 1, t8 = at / (D / 2);
-                    if (cut) {
-                        int tb = t0 + 8 * t8;
-                        asm volatile("" : "+v"(tb));   // a branch, not selects in every block
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int x = tb + 2 * w;
-                            const uint32_t keep = (x >= t.begin && x < t.end ? 0xFFFFu : 0u) |
-                                                  (x + 1 >= t.begin && x + 1 < t.end ? 0xFFFF0000u : 0u);
-                            vs[p][w] &= keep;
-                            vl[p][w] &= keep;
-                        }
-                    }
-                    u32x4 w = vw[p];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] >>= 8 * half;
-                    f16x8* to = &vt[buf][t8][quad / 16 * 64 + half * 32 + quad % 16 * 2];
-                    to[0] = v_values<0>(w, vs[p], vl[p], mk);
-                    to[1] = v_values<1>(w, vs[p], vl[p], mk);
                 }
+                if (t0 < t.begin || t0 + PB > t.end) {
+                    // what lies at positions that no row sees may be anything
+                    int tb = t0 + 8 * t8;
+                    asm volatile("" : "+v"(tb));   // a branch, not selects in every block
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int x = tb + 2 * w;
+                        const uint32_t keep = (x >= t.begin && x < t.end ? 0xFFFFu : 0u) |
+                                              (x + 1 >= t.begin && x + 1 < t.end ? 0xFFFF0000u : 0u);
+                        vs[w] &= keep;
+                        vl[w] &= keep;
+                    }
+                }
+                u32x4 w = vw;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    w[x] >>= 8 * half;
+                f16x8* to = &vt[vb][t8][quad / 16 * 64 + half * 32 + quad % 16 * 2];
+                to[0] = v_values<0>(w, vs, vl, mk);
+                to[1] = v_values<1>(w, vs, vl, mk);
             }
         };
-        auto step = [&](int buf, int t0) {
-            const bool edge = t0 < w_all_begin || t0 + PB > w_all_end;
-            f32x4 s[NQ][4];
+        // The operands of the next rows of products are read while the present ones run; the
+        // scheduling barriers keep more of them from piling up in registers.
+        struct Keys {
+            f16x8 k[NI];
+            bf16x8 low[NL];
+            f16x4 sc[NG];
+        };
+        auto keys = [&](int kb, int x) {
+            Keys f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int y = 0; y < NL; ++y)   // lanes past the last group meet q's zeros
+                f.low[y] = __builtin_bit_cast(bf16x8, lowt[kb][min(4 * y + kg, NG - 1)][16 * x + n]);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                f.k[i] = kt[kb][4 * i + kg][16 * x + n];
+#pragma unroll
+            for (int g = 0; g < NG; ++g)   // scales of tokens 32 (x / 2) + 8 kg + 4 (x % 2) + r
+                f.sc[g] = *reinterpret_cast<const f16x4*>(&sct[kb][g][(x >> 1) * 32 + kg * 8 + (x & 1) * 4]);
+            return f;
+        };
+        auto scores = [&](f32x4(&s)[NQ][XT], int kb) {
+            Keys f = keys(kb, 0);
+#pragma unroll
+            for (int x = 0; x < XT; ++x) {
+                __builtin_amdgcn_sched_barrier(0);
+                Keys next = f;
+                if (x + 1 < XT)
+                    next = keys(kb, x + 1);
+#pragma unroll
                 for (int u = 0; u < NQ; ++u)
                     s[u][x] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int y = 0; y < NL; ++y) {
-                    const bf16x8 lf = __builtin_bit_cast(bf16x8, lowt[buf][4 * y + kg][16 * x + n]);
+                for (int y = 0; y < NL; ++y)
 #pragma unroll
                     for (int u = 0; u < NQ; ++u)
-                        s[u][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lf, ql[u][y], s[u][x], 0, 0, 0);
-                }
+                        s[u][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.low[y], ql[u][y], s[u][x], 0, 0, 0);
+                f32x4 acc[NG][NQ];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    f32x4 acc[NQ];
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
-                    for (int u = 0; u < NQ; ++u)
-                        acc[u] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int i = g * (G / 32); i < (g + 1) * (G / 32); ++i) {
-                        const f16x8 kf = kt[buf][4 * i + kg][16 * x + n];
+                    for (int i = g * (G / 32); i < (g + 1) * (G / 32); ++i)
 #pragma unroll
                         for (int u = 0; u < NQ; ++u)
-                            acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[u][i], acc[u], 0, 0, 0);
-                    }
-                    // scales of tokens 32 (x / 2) + 8 kg + 4 (x % 2) + r
-                    const f16x4 sc = *reinterpret_cast<const f16x4*>(&sct[buf][g][(x >> 1) * 32 + kg * 8 + (x & 1) * 4]);
+                            acc[g][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                f.k[i], q[u][i], i == g * (G / 32) ? f32x4{0, 0, 0, 0} : acc[g][u], 0, 0, 0);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
                     for (int u = 0; u < NQ; ++u)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            s[u][x][r] = fmaf((float)sc[r], acc[u][r], s[u][x][r]);
-                }
+                            s[u][x][r] = fmaf((float)f.sc[g][r], acc[g][u][r], s[u][x][r]);
+                f = next;
             }
-            if (edge) {
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto softmax = [&](f32x4(&s)[NQ][XT], int i) {
+            const int t0 = from + i * PB;
+            if (t0 < w_all_begin || t0 + PB > w_all_end) {
                 int tb = t0;
                 asm volatile("" : "+s"(tb));
 #pragma unroll
                 for (int u = 0; u < NQ; ++u)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < XT; ++x)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const int j = tb + (x >> 1) * 32 + kg * 8 + (x & 1) * 4 + r;
-                            s[u][x][r] = j >= rbeg[u] && j < rend[u] ? s[u][x][r] : -3.0e38f;
+                            const int at = tb + (x >> 1) * 32 + kg * 8 + (x & 1) * 4 + r;
+                            s[u][x][r] = at >= rbeg[u] && at < rend[u] ? s[u][x][r] : -3.0e38f;
                         }
             }
-            f16x8 p[NQ][2];
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
                 float top = s[u][0][0];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < XT; ++x)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         top = fmaxf(top, s[u][x][r]);
@@ -923,53 +951,96 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                     m[u] = mn;
                     l[u][0] *= f;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-                        o[u][i] *= f;
+                    for (int x = 0; x < D / 16; ++x)
+                        o[u][x] *= f;
                 }
                 const float shift = m[u] > M_NONE ? P_SHIFT - m[u] : 0.0f;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < XT; ++x)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         p[u][x >> 1][(x & 1) * 4 + r] = (_Float16)__builtin_amdgcn_exp2f(fmaf(s[u][x][r], kappa, shift));
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u][y], l[u], 0, 0, 0);
             }
+            // the weights are done in this phase, not where they are used
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int u = 0; u < NQ; ++u)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const f16x8 vf = vt[buf][4 * y + kg][16 * i + n];
+                for (int y = 0; y < XT / 2; ++y)
+                    asm volatile("" : "+v"(p[u][y]));
+        };
+        auto values = [&](int vb) {
+            constexpr int STEP = 2;   // of D / 16
+            f16x8 f[STEP][XT / 2];
+            auto read = [&](f16x8(&to)[STEP][XT / 2], int x0) {
 #pragma unroll
-                    for (int u = 0; u < NQ; ++u)
-                        o[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[u][y], o[u][i], 0, 0, 0);
-                }
+                for (int x = 0; x < STEP; ++x)
+#pragma unroll
+                    for (int y = 0; y < XT / 2; ++y)
+                        to[x][y] = vt[vb][4 * y + kg][16 * (x0 + x) + n];
+            };
+            read(f, 0);
+#pragma unroll
+            for (int u = 0; u < NQ; ++u)
+#pragma unroll
+                for (int y = 0; y < XT / 2; ++y)
+                    l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u][y], l[u], 0, 0, 0);
+#pragma unroll
+            for (int x0 = 0; x0 < D / 16; x0 += STEP) {
+                __builtin_amdgcn_sched_barrier(0);
+                f16x8 next[STEP][XT / 2];
+                if (x0 + STEP < D / 16)
+                    read(next, x0 + STEP);
+#pragma unroll
+                for (int x = 0; x < STEP; ++x)
+#pragma unroll
+                    for (int y = 0; y < XT / 2; ++y)
+#pragma unroll
+                        for (int u = 0; u < NQ; ++u)
+                            o[u][x0 + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x][y], p[u][y], o[u][x0 + x], 0, 0, 0);
+#pragma unroll
+                for (int x = 0; x < STEP; ++x)
+#pragma unroll
+                    for (int y = 0; y < XT / 2; ++y)
+                        f[x][y] = next[x][y];
+            }
+            __builtin_amdgcn_sched_barrier(0);
         };
 
         __syncthreads();   // the last tile's blocks have been read
-        if constexpr (NG % 4 != 0) {   // slots of groups that are not there: q's terms are 0, low's have to be finite
-            for (int i = tid; i < 2 * (4 * NL - NG) * PB; i += PT)
-                lowt[i / ((4 * NL - NG) * PB)][NG + i / PB % (4 * NL - NG)][i % PB] = u32x4{0, 0, 0, 0};
-        }
-        if (from < to) {
-            load(from);
-            put(0, from);
-            if (from + PB < to)
-                load(from + PB);
-            __syncthreads();
-            int buf = 0;
-            for (int t0 = from; t0 < to; t0 += PB) {
-                if (t0 + PB < to) {
-                    put(buf ^ 1, t0 + PB);
-                    if (t0 + 2 * PB < to)
-                        load(t0 + 2 * PB);
-                }
-                if (t0 < w_end && t0 + PB > w_begin)
-                    step(buf, t0);
-                __syncthreads();
-                buf ^= 1;
+        if (nb > 0) {
+            load(0);
+            put(0, 0, 0);
+            if (nb > 1) {
+                load(1);
+                put(1, 1, 1);
             }
+            if (nb > 2)
+                load(2);
+            phase_end();
+            if (wave >= 4)
+                phase_end();   // the second half runs one phase behind
+            int kb = 0;        // i % 3
+#pragma clang loop unroll(disable)
+            for (int i = 0; i < nb; ++i) {
+                f32x4 s[NQ][XT];
+                __builtin_amdgcn_s_setprio(1);
+                if (i > 0)
+                    values((i - 1) & 3);
+                scores(s, kb);
+                __builtin_amdgcn_s_setprio(0);
+                phase_end();
+                softmax(s, i);
+                if (i + 2 < nb) {
+                    put(i + 2, kb == 0 ? 2 : kb - 1, (i + 2) & 3);
+                    if (i + 3 < nb)
+                        load(i + 3);
+                }
+                phase_end();
+                kb = kb == 2 ? 0 : kb + 1;
+            }
+            values((nb - 1) & 3);
+            if (wave < 4)
+                phase_end();
         }
 
 #pragma unroll
@@ -981,7 +1052,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                 // o's tile x, register r: d = 16 x + 4 kg + r
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                        f16x4 h;
+                    f16x4 h;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         h[r] = (_Float16)(o[u][x][r] * inv);
@@ -1037,9 +1108,9 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
     if (pairs > PROMPT_PAIRS)
         return kv4_dispatch(D, G, [&](auto d, auto g) {
             constexpr int DD = decltype(d)::value, GG = decltype(g)::value, NQ = DD == 256 ? 1 : 2;
-            const int tiles = (int)((pairs + 128 * NQ - 1) / (128 * NQ));
+            const int tiles = (int)((pairs + 128 * NQ - 1) / (128 * NQ)), P = 1 << c.page_log2;
             const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * tiles));
-            if (c.page_log2 >= 5)
+            if (P >= prompt_block(DD))
                 attention_kv4_prompt_kernel<DD, GG, true, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
             else
                 attention_kv4_prompt_kernel<DD, GG, false, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
