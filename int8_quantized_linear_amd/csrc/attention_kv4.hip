@@ -291,7 +291,7 @@ __device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2
 constexpr int SLOTS = 2;
 
 template <int D, int G, bool BIG, int NQ>
-__global__ __launch_bounds__(AT, D == 256 ? (NQ == 1 ? 2 : 1) : NQ == 1 ? 4 : 2) void attention_kv4_decode_kernel(
+__global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 4 : D == 256 && G == 32 ? 1 : 2) void attention_kv4_decode_kernel(
     Kv4Attn a, Kv4Cache c, Kv4Batch b, Split sp) {
     using RG = Ring<D, G, BIG>;
     constexpr int NG = D / G, NI = D / 32, NC = D / 64, PER = 16 * NQ;
@@ -1063,25 +1063,37 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
     }
 }
 
-// (Row, head) pairs of a sequence from which the prompt kernel takes over.
-constexpr int64_t PROMPT_PAIRS = 64;
+// Whether the prompt kernel takes a call: its workgroups each hold a CU and are not split over the
+// length, so it needs nearly a chip of them. Cycles a token of the length, as measured on 8 kv
+// heads with 4 query heads each: a round of prompt workgroups, and a decode tile of 32 rows as a
+// share of the whole chip. (One sequence, D = 128: 2048 rows after 2048 take 152 us against the
+// decode kernel's 195, 17 rows over 65536 tokens 2070 us against 84.)
+inline int prompt_rows(int D) { return D == 256 ? 128 : 256; }
+inline bool use_prompt(int64_t pairs, int64_t heads, int D) {
+    const double round = D == 64 ? 61.0 : D == 128 ? 86.0 : 100.0, tile = D == 64 ? 0.034 : D == 128 ? 0.07 : 0.15;
+    const int64_t workgroups = heads * ((pairs + prompt_rows(D) - 1) / prompt_rows(D));
+    return tile * (double)(heads * ((pairs + 31) / 32)) > round * (double)((workgroups + 255) / 256);
+}
 
-// Rows of a decode tile: 16 columns, or 32 where a sequence has more.
-constexpr int64_t FILL = 512;   // workgroups that the chip holds at once
+// Rows of a decode tile: 16, or 32 where a sequence has more and two tiles' O and Q fit in the
+// registers of two waves a SIMD (5 rows of 4 heads over 8192 tokens, 8 sequences of 8 kv heads:
+// D = 128 27.9 us in tiles of 32, 32.0 of 16; D = 256 64.8 and 51.7).
+inline int rows_per_tile(int64_t pairs, int D) { return pairs <= 16 || D == 256 ? 16 : 32; }
 
-inline int rows_per_tile(int64_t pairs) { return pairs <= 16 ? 16 : 32; }
+constexpr int64_t FILL = 512;   // workgroups that two on each CU make
 
 // Splits: two workgroups of four waves a CU fill the chip, so that many in all, each with at
 // least 256 tokens, and at most what the second kernel joins. Up to 640 tokens stay whole: the
 // join costs what 256 tokens do (32 heads of 128, 512 tokens 8.7 us whole, 9.5 us in halves;
 // 1024 tokens 12.8 us whole, 9.9 us in quarters).
-Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len, int window) {
+Split plan(int q_heads, int kv_heads, int D, int batch, int max_q, int max_len, int window) {
     const int64_t pairs = (int64_t)max_q * (q_heads / kv_heads);
     constexpr int64_t unit = TB * AW;
     if (window > 0)   // the positions that a sequence's rows see together
         max_len = (int)std::min<int64_t>(max_len, (int64_t)window + max_q);
     Split s;
-    s.tiles = (int)((pairs + rows_per_tile(pairs) - 1) / rows_per_tile(pairs));
+    const int per = rows_per_tile(pairs, D);
+    s.tiles = (int)((pairs + per - 1) / per);
     const int64_t base = (int64_t)batch * kv_heads * s.tiles;
     int64_t want = base > 0 ? (FILL + base - 1) / base : 1;
     want = want < MAX_SPLITS ? want : MAX_SPLITS;
@@ -1096,19 +1108,19 @@ Split plan(int q_heads, int kv_heads, int batch, int max_q, int max_len, int win
 
 int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
                                 int window) {
-    if ((int64_t)max_q * (q_heads / kv_heads) > PROMPT_PAIRS)
+    if (use_prompt((int64_t)max_q * (q_heads / kv_heads), (int64_t)batch * kv_heads, D))
         return 0;
-    const Split s = plan(q_heads, kv_heads, batch, max_q, max_len, window);
+    const Split s = plan(q_heads, kv_heads, D, batch, max_q, max_len, window);
     return s.n == 1 ? 0 : s.n * rows * q_heads * (D + 2);
 }
 
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream) {
     const int64_t pairs = (int64_t)a.max_q * (a.q_heads / c.heads);
-    if (pairs > PROMPT_PAIRS)
+    if (use_prompt(pairs, (int64_t)b.batch * c.heads, D))
         return kv4_dispatch(D, G, [&](auto d, auto g) {
             constexpr int DD = decltype(d)::value, GG = decltype(g)::value, NQ = DD == 256 ? 1 : 2;
-            const int tiles = (int)((pairs + 128 * NQ - 1) / (128 * NQ)), P = 1 << c.page_log2;
+            const int tiles = (int)((pairs + prompt_rows(DD) - 1) / prompt_rows(DD)), P = 1 << c.page_log2;
             const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * tiles));
             if (P >= prompt_block(DD))
                 attention_kv4_prompt_kernel<DD, GG, true, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
@@ -1116,8 +1128,8 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
                 attention_kv4_prompt_kernel<DD, GG, false, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
             return launch_status();
         });
-    const int per = rows_per_tile(pairs);
-    const Split sp = plan(a.q_heads, c.heads, b.batch, a.max_q, a.max_len, a.window);
+    const int per = rows_per_tile(pairs, D);
+    const Split sp = plan(a.q_heads, c.heads, D, b.batch, a.max_q, a.max_len, a.window);
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
         const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * sp.n * sp.tiles));
@@ -1127,7 +1139,7 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
                 go(attention_kv4_decode_kernel<DD, GG, true, 1>);
             else
                 go(attention_kv4_decode_kernel<DD, GG, false, 1>);
-        } else {
+        } else if constexpr (DD < 256) {
             if (c.page_log2 >= 5)
                 go(attention_kv4_decode_kernel<DD, GG, true, 2>);
             else
