@@ -19,7 +19,12 @@
 //                 one column, which is the layout of the next product's operand: P never
 //                 crosses lanes. V becomes fp16 values scale * code + low (one rounding), since
 //                 its scales lie along the summed axis; folding them into P would tie P's fp16
-//                 range to V's magnitude.
+//                 range to V's magnitude. P enters as two fp16 terms (22 bits): V's rounding and
+//                 the output's are the only ones to fp16. With one term the error against 64
+//                 bits is 1.6 times the output's own rounding, with two 1.4 times, and with V's
+//                 codes and scales kept apart as well 1.0 times, but for long sums, whose two parts
+//                 cancel (4 times at 131072 tokens). The second term costs the decode kernel 4 to
+//                 8% (64 x 8-16k tokens 171 -> 185 us).
 // The running maximum is raised only when a score exceeds it by 2^8 (weights up to 2^14, sums
 // in fp32), so most steps have neither a reduction across lanes nor a rescaling of O.
 #include <algorithm>
@@ -274,6 +279,16 @@ __device__ inline f16x2 codes_int(uint32_t w, const Masks& mk) {
         return as_f16x2((h & mk.even) | mk.k1024) - (f16x2){(_Float16)1024.0f, (_Float16)1024.0f};
 }
 
+// v as two fp16 terms.
+__device__ inline void two_terms(const float (&v)[8], f16x8& hi, f16x8& lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        hi[e] = (_Float16)v[e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        lo[e] = (_Float16)fmaf((float)hi[e], -1.0f, v[e]);
+}
+
 // V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16.
 template <int JJ>
 __device__ inline f16x8 v_values(u32x4 w, u32x4 s, u32x4 l, const Masks& mk) {
@@ -291,7 +306,7 @@ __device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2
 constexpr int SLOTS = 2;
 
 template <int D, int G, bool BIG, int NQ>
-__global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 4 : D == 256 && G == 32 ? 1 : 2) void attention_kv4_decode_kernel(
+__global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 256 && G == 32 ? 1 : 2) void attention_kv4_decode_kernel(
     Kv4Attn a, Kv4Cache c, Kv4Batch b, Split sp) {
     using RG = Ring<D, G, BIG>;
     constexpr int NG = D / G, NI = D / 32, NC = D / 64, PER = 16 * NQ;
@@ -453,7 +468,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 4 : D == 25
                             s[u][h][r] = j >= rbeg[u] && j < rend[u] ? s[u][h][r] : -3.0e38f;
                         }
             }
-            f16x8 p[NQ];
+            f16x8 p[NQ], pl[NQ];
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
                 float top = s[u][0][0];
@@ -476,13 +491,15 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 4 : D == 25
                 }
                 // before a row's first score, 0 in place of the maximum: masked weights stay 0
                 const float shift = m[u] > M_NONE ? P_SHIFT - m[u] : 0.0f;
+                float w[8];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        p[u][4 * h + r] = (_Float16)__builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa, shift));
-                // the sum of the rounded weights, so that their rounding cancels in the quotient
+                        w[4 * h + r] = __builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa, shift));
+                two_terms(w, p[u], pl[u]);
                 l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u], l[u], 0, 0, 0);
+                l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[u], l[u], 0, 0, 0);
             }
             u32x4 vs[NG], vl[NG], vw[NC];
             RG::v_words(vw, v_at + at);
@@ -506,18 +523,20 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 4 : D == 25
             }
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) {
-                auto add = [&](auto jj) {
-                    constexpr int JJ = decltype(jj)::value;
-                    const int g = (64 * ch + 32 * (JJ / 2)) / G;
-                    const f16x8 vv = v_values<JJ>(vw[ch], vs[g], vl[g], mk);
+                const int g0 = 64 * ch / G, g1 = (64 * ch + 32) / G;
+                const f16x8 vv[4] = {v_values<0>(vw[ch], vs[g0], vl[g0], mk), v_values<1>(vw[ch], vs[g0], vl[g0], mk),
+                                     v_values<2>(vw[ch], vs[g1], vl[g1], mk), v_values<3>(vw[ch], vs[g1], vl[g1], mk)};
+                // the second terms after all first ones: a product that waits for the one before
+                // it on the same sum would stall
+                auto add = [&](const f16x8(&w)[NQ]) {
 #pragma unroll
-                    for (int u = 0; u < NQ; ++u)
-                        o[u][4 * ch + JJ] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[u], o[u][4 * ch + JJ], 0, 0, 0);
+                    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                        for (int u = 0; u < NQ; ++u)
+                            o[u][4 * ch + jj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv[jj], w[u], o[u][4 * ch + jj], 0, 0, 0);
                 };
-                add(std::integral_constant<int, 0>{});
-                add(std::integral_constant<int, 1>{});
-                add(std::integral_constant<int, 2>{});
-                add(std::integral_constant<int, 3>{});
+                add(p);
+                add(pl);
             }
         };
 
@@ -784,7 +803,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
         const int w_all_begin = a.window ? max(0, t.first + wl / R + 1 - a.window) : 0;
 
         f32x4 o[NQ][D / 16], l[NQ];
-        f16x8 p[NQ][XT / 2];
+        f16x8 p[NQ][XT / 2], pl[NQ][XT / 2];
         float m[NQ];
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
@@ -956,17 +975,20 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                 }
                 const float shift = m[u] > M_NONE ? P_SHIFT - m[u] : 0.0f;
 #pragma unroll
-                for (int x = 0; x < XT; ++x)
+                for (int y = 0; y < XT / 2; ++y) {
+                    float w[8];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        p[u][x >> 1][(x & 1) * 4 + r] = (_Float16)__builtin_amdgcn_exp2f(fmaf(s[u][x][r], kappa, shift));
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = __builtin_amdgcn_exp2f(fmaf(s[u][2 * y + e / 4][e % 4], kappa, shift));
+                    two_terms(w, p[u][y], pl[u][y]);
+                }
             }
             // the weights are done in this phase, not where they are used
 #pragma unroll
             for (int u = 0; u < NQ; ++u)
 #pragma unroll
                 for (int y = 0; y < XT / 2; ++y)
-                    asm volatile("" : "+v"(p[u][y]));
+                    asm volatile("" : "+v"(p[u][y]), "+v"(pl[u][y]));
         };
         auto values = [&](int vb) {
             constexpr int STEP = 2;   // of D / 16
@@ -982,21 +1004,28 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
 #pragma unroll
             for (int u = 0; u < NQ; ++u)
 #pragma unroll
-                for (int y = 0; y < XT / 2; ++y)
+                for (int y = 0; y < XT / 2; ++y) {
                     l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u][y], l[u], 0, 0, 0);
+                    l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[u][y], l[u], 0, 0, 0);
+                }
 #pragma unroll
             for (int x0 = 0; x0 < D / 16; x0 += STEP) {
                 __builtin_amdgcn_sched_barrier(0);
                 f16x8 next[STEP][XT / 2];
                 if (x0 + STEP < D / 16)
                     read(next, x0 + STEP);
-#pragma unroll
-                for (int x = 0; x < STEP; ++x)
+                auto add = [&](const f16x8(&w)[NQ][XT / 2]) {
 #pragma unroll
                     for (int y = 0; y < XT / 2; ++y)
 #pragma unroll
-                        for (int u = 0; u < NQ; ++u)
-                            o[u][x0 + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x][y], p[u][y], o[u][x0 + x], 0, 0, 0);
+                        for (int x = 0; x < STEP; ++x)
+#pragma unroll
+                            for (int u = 0; u < NQ; ++u)
+                                o[u][x0 + x] =
+                                    __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x][y], w[u][y], o[u][x0 + x], 0, 0, 0);
+                };
+                add(p);
+                add(pl);
 #pragma unroll
                 for (int x = 0; x < STEP; ++x)
 #pragma unroll
@@ -1066,18 +1095,18 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
 // Whether the prompt kernel takes a call: its workgroups each hold a CU and are not split over the
 // length, so it needs nearly a chip of them. Cycles a token of the length, as measured on 8 kv
 // heads with 4 query heads each: a round of prompt workgroups, and a decode tile of 32 rows as a
-// share of the whole chip. (One sequence, D = 128: 2048 rows after 2048 take 152 us against the
-// decode kernel's 195, 17 rows over 65536 tokens 2070 us against 84.)
+// share of the whole chip. (D = 128: 4 sequences of 2048 rows take 265 us against the decode
+// kernel's 392, 17 rows over 65536 tokens 2680 us against 98.)
 inline int prompt_rows(int D) { return D == 256 ? 128 : 256; }
 inline bool use_prompt(int64_t pairs, int64_t heads, int D) {
-    const double round = D == 64 ? 61.0 : D == 128 ? 86.0 : 100.0, tile = D == 64 ? 0.034 : D == 128 ? 0.07 : 0.15;
+    const double round = D == 64 ? 80.0 : D == 128 ? 106.0 : 118.0, tile = D == 64 ? 0.043 : D == 128 ? 0.086 : 0.164;
     const int64_t workgroups = heads * ((pairs + prompt_rows(D) - 1) / prompt_rows(D));
     return tile * (double)(heads * ((pairs + 31) / 32)) > round * (double)((workgroups + 255) / 256);
 }
 
 // Rows of a decode tile: 16, or 32 where a sequence has more and two tiles' O and Q fit in the
-// registers of two waves a SIMD (5 rows of 4 heads over 8192 tokens, 8 sequences of 8 kv heads:
-// D = 128 27.9 us in tiles of 32, 32.0 of 16; D = 256 64.8 and 51.7).
+// registers of two waves a SIMD (5 rows of 4 heads over 8192 tokens, 8 sequences of 8 kv heads,
+// with one term for P: D = 128 27.9 us in tiles of 32, 32.0 of 16; D = 256 64.8 and 51.7).
 inline int rows_per_tile(int64_t pairs, int D) { return pairs <= 16 || D == 256 ? 16 : 32; }
 
 constexpr int64_t FILL = 512;   // workgroups that two on each CU make
