@@ -401,8 +401,9 @@ ql_status rms_norm_quantize_e4m3(const void* x, ql_dtype x_dtype, const void* re
  *             sequence is shorter than its rows, its first rows have no position.
  * No page may be shared by two sequences that a kv4_append call writes. Page numbers outside
  * [0, num_pages) are a caller's error that no call turns into an access outside the cache.
- * QL_ERR_SHAPE also for sizes outside what is stated, num_pages == 0 with rows, and
- * q_heads not a multiple of kv_heads.
+ * QL_ERR_SHAPE also for sizes outside what is stated, num_pages == 0 with rows, q_heads not a
+ * multiple of kv_heads, rows above 2^24, heads above 4096, rows * heads above 2^28, batch above
+ * 2^20, batch * kv_heads above 2^22, and table_width * page_size not below 2^31.
  */
 
 /*

@@ -61,7 +61,7 @@ struct RowTile {
 __device__ inline RowTile row_tile(const Kv4Batch& b, const Kv4Cache& c, int seq, int tile, int per, int R, int window) {
     RowTile t;
     const int len = kv4_len(b, c, seq);
-    t.rows = b.starts[seq + 1] - b.starts[seq];
+    t.rows = min(b.starts[seq + 1] - b.starts[seq], b.rows);
     t.first = len - t.rows;
     const int i0 = tile * per / R, i1 = min((tile * per + per - 1) / R, t.rows - 1);
     t.end = max(0, t.first + i1 + 1);
@@ -628,58 +628,61 @@ __global__ __launch_bounds__(AT) void attention_kv4_join_kernel(const float* __r
     __shared__ float weight[ROWS][WAVES * WAVE], red[AW][2];
     __shared__ f32x4 part[ROWS][PARTS][LANES];
     const int group = threadIdx.x / (WAVES * WAVE), tid = threadIdx.x % (WAVES * WAVE);
-    const int64_t at = (int64_t)blockIdx.x * ROWS + group;
-    const float* st = ws + (int64_t)n * all * D + at * n * 2;
-    float m = M_NONE, l = 0.0f;
-    if (at < all && tid < n) {
-        m = st[2 * tid];
-        l = st[2 * tid + 1];
-    }
-    float top = m;
-#pragma unroll
-    for (int o = WAVE / 2; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor(top, o, WAVE));
-    if ((tid & (WAVE - 1)) == 0)
-        red[threadIdx.x / WAVE][0] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-        top = fmaxf(top, red[group * WAVES + w][0]);
-    const float f = l > 0.0f ? __builtin_amdgcn_exp2f(m - top) : 0.0f;
-    weight[group][tid] = f;
-    float sum = l * f;
-#pragma unroll
-    for (int o = WAVE / 2; o > 0; o >>= 1)
-        sum += __shfl_xor(sum, o, WAVE);
-    if ((tid & (WAVE - 1)) == 0)
-        red[threadIdx.x / WAVE][1] = sum;
-    __syncthreads();
-    sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-        sum += red[group * WAVES + w][1];
-    const int d4 = tid % LANES, p = tid / LANES;
-    f32x4 v = {0, 0, 0, 0};
-    if (at < all) {
-        const float* src = ws + at * D + 4 * d4;
-#pragma unroll 4
-        for (int s = p; s < n; s += PARTS) {
-            const float w = weight[group][s];
-            if (w != 0.0f)   // a split without tokens wrote no values
-                v += *reinterpret_cast<const f32x4*>(src + s * all * D) * w;
+    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < all; first += (int64_t)gridDim.x * ROWS) {
+        const int64_t at = first + group;
+        const float* st = ws + (int64_t)n * all * D + at * n * 2;
+        float m = M_NONE, l = 0.0f;
+        if (at < all && tid < n) {
+            m = st[2 * tid];
+            l = st[2 * tid + 1];
         }
-    }
-    part[group][p][d4] = v;
-    __syncthreads();
-    if (p == 0 && at < all) {
+        float top = m;
 #pragma unroll
-        for (int k = 1; k < PARTS; ++k)
-            v += part[group][k][d4];
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        _Float16* to = out + at * D + 4 * d4;
+        for (int o = WAVE / 2; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor(top, o, WAVE));
+        if ((tid & (WAVE - 1)) == 0)
+            red[threadIdx.x / WAVE][0] = top;
+        __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            to[e] = (_Float16)(v[e] * inv);
+        for (int w = 0; w < WAVES; ++w)
+            top = fmaxf(top, red[group * WAVES + w][0]);
+        const float f = l > 0.0f ? __builtin_amdgcn_exp2f(m - top) : 0.0f;
+        weight[group][tid] = f;
+        float sum = l * f;
+#pragma unroll
+        for (int o = WAVE / 2; o > 0; o >>= 1)
+            sum += __shfl_xor(sum, o, WAVE);
+        if ((tid & (WAVE - 1)) == 0)
+            red[threadIdx.x / WAVE][1] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            sum += red[group * WAVES + w][1];
+        const int d4 = tid % LANES, p = tid / LANES;
+        f32x4 v = {0, 0, 0, 0};
+        if (at < all) {
+            const float* src = ws + at * D + 4 * d4;
+#pragma unroll 4
+            for (int s = p; s < n; s += PARTS) {
+                const float w = weight[group][s];
+                if (w != 0.0f)   // a split without tokens wrote no values
+                    v += *reinterpret_cast<const f32x4*>(src + s * all * D) * w;
+            }
+        }
+        part[group][p][d4] = v;
+        __syncthreads();
+        if (p == 0 && at < all) {
+#pragma unroll
+            for (int k = 1; k < PARTS; ++k)
+                v += part[group][k][d4];
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            _Float16* to = out + at * D + 4 * d4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                to[e] = (_Float16)(v[e] * inv);
+        }
+        __syncthreads();   // the shared arrays have been read
     }
 }
 
@@ -1092,6 +1095,9 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
     }
 }
 
+constexpr int64_t FILL = 512;                      // workgroups that two on each CU make
+constexpr int64_t MAX_GROUPS = (int64_t)1 << 22;   // of a launch (threads stay below 2^32); the kernels loop
+
 // Whether the prompt kernel takes a call: its workgroups each hold a CU and are not split over the
 // length, so it needs nearly a chip of them. Cycles a token of the length, as measured on 8 kv
 // heads with 4 query heads each: a round of prompt workgroups, and a decode tile of 32 rows as a
@@ -1109,8 +1115,6 @@ inline bool use_prompt(int64_t pairs, int64_t heads, int D) {
 // with one term for P: D = 128 27.9 us in tiles of 32, 32.0 of 16; D = 256 64.8 and 51.7).
 inline int rows_per_tile(int64_t pairs, int D) { return pairs <= 16 || D == 256 ? 16 : 32; }
 
-constexpr int64_t FILL = 512;   // workgroups that two on each CU make
-
 // Splits: two workgroups of four waves a CU fill the chip, so that many in all, each with at
 // least 256 tokens, and at most what the second kernel joins. Up to 640 tokens stay whole: the
 // join costs what 256 tokens do (32 heads of 128, 512 tokens 8.7 us whole, 9.5 us in halves;
@@ -1122,8 +1126,9 @@ Split plan(int q_heads, int kv_heads, int D, int batch, int max_q, int max_len, 
         max_len = (int)std::min<int64_t>(max_len, (int64_t)window + max_q);
     Split s;
     const int per = rows_per_tile(pairs, D);
-    s.tiles = (int)((pairs + per - 1) / per);
-    const int64_t base = (int64_t)batch * kv_heads * s.tiles;
+    const int64_t heads = (int64_t)batch * kv_heads;   // at most MAX_GROUPS
+    s.tiles = (int)std::min((pairs + per - 1) / per, std::max<int64_t>(1, MAX_GROUPS / std::max<int64_t>(1, heads)));
+    const int64_t base = heads * s.tiles;
     int64_t want = base > 0 ? (FILL + base - 1) / base : 1;
     want = want < MAX_SPLITS ? want : MAX_SPLITS;
     int64_t stretch = max_len <= 5 * unit ? max_len : (max_len + want - 1) / want;
@@ -1137,6 +1142,7 @@ Split plan(int q_heads, int kv_heads, int D, int batch, int max_q, int max_len, 
 
 int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
                                 int window) {
+    max_q = (int)std::min<int64_t>(max_q, std::max<int64_t>(rows, 1));
     if (use_prompt((int64_t)max_q * (q_heads / kv_heads), (int64_t)batch * kv_heads, D))
         return 0;
     const Split s = plan(q_heads, kv_heads, D, batch, max_q, max_len, window);
@@ -1145,12 +1151,15 @@ int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, 
 
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream) {
-    const int64_t pairs = (int64_t)a.max_q * (a.q_heads / c.heads);
+    const int max_q = std::min(a.max_q, a.rows);
+    const int64_t pairs = (int64_t)max_q * (a.q_heads / c.heads);
     if (use_prompt(pairs, (int64_t)b.batch * c.heads, D))
         return kv4_dispatch(D, G, [&](auto d, auto g) {
             constexpr int DD = decltype(d)::value, GG = decltype(g)::value, NQ = DD == 256 ? 1 : 2;
-            const int tiles = (int)((pairs + prompt_rows(DD) - 1) / prompt_rows(DD)), P = 1 << c.page_log2;
-            const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * tiles));
+            const int64_t heads = (int64_t)c.heads * b.batch;
+            const int tiles = (int)std::min((pairs + prompt_rows(DD) - 1) / prompt_rows(DD), std::max<int64_t>(1, MAX_GROUPS / heads));
+            const int P = 1 << c.page_log2;
+            const dim3 grid((uint32_t)(heads * tiles));
             if (P >= prompt_block(DD))
                 attention_kv4_prompt_kernel<DD, GG, true, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
             else
@@ -1158,7 +1167,7 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
             return launch_status();
         });
     const int per = rows_per_tile(pairs, D);
-    const Split sp = plan(a.q_heads, c.heads, D, b.batch, a.max_q, a.max_len, a.window);
+    const Split sp = plan(a.q_heads, c.heads, D, b.batch, max_q, a.max_len, a.window);
     return kv4_dispatch(D, G, [&](auto d, auto g) {
         constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
         const dim3 grid((uint32_t)((int64_t)c.heads * b.batch * sp.n * sp.tiles));
@@ -1175,12 +1184,13 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
                 go(attention_kv4_decode_kernel<DD, GG, false, 2>);
         }
         if (sp.n > 1) {
-            const int64_t all = (int64_t)a.rows * a.q_heads;
+            const int64_t all = (int64_t)a.rows * a.q_heads, most = MAX_GROUPS;
             if (sp.n > 16)
-                attention_kv4_join_kernel<DD, AW><<<dim3((uint32_t)all), AT, 0, stream>>>(a.ws, a.out, all, sp.n);
+                attention_kv4_join_kernel<DD, AW>
+                    <<<dim3((uint32_t)std::min(all, most)), AT, 0, stream>>>(a.ws, a.out, all, sp.n);
             else
                 attention_kv4_join_kernel<DD, 1>
-                    <<<dim3((uint32_t)((all + AW - 1) / AW)), AT, 0, stream>>>(a.ws, a.out, all, sp.n);
+                    <<<dim3((uint32_t)std::min((all + AW - 1) / AW, most)), AT, 0, stream>>>(a.ws, a.out, all, sp.n);
         }
         return launch_status();
     });

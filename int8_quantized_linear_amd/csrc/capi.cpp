@@ -401,14 +401,15 @@ ql_status rms_norm_quantize_e4m3(const void* x, ql_dtype x_dtype, const void* re
 }
 
 // Sizes that the three calls on the 4-bit cache share. Rows and heads are passed to kernels as
-// int, and rows * kv_heads (at most 2^30, as rows * q_heads) sizes grids.
+// int, rows * kv_heads and rows * q_heads (at most 2^28) index tiles, batch * kv_heads sizes grids.
 static bool bad_kv4(int64_t rows, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D, int64_t group,
                     int64_t table_width, int64_t batch) {
     return rows < 0 || rows > (1 << 24) || num_pages < 0 || num_pages >= kMaxDim || page_size < 16 ||
            page_size > 4096 || (page_size & (page_size - 1)) != 0 || kv_heads < 1 || kv_heads > 4096 ||
            (D != 64 && D != 128 && D != 256) || (group != 32 && group != 64 && group != 128) || group > D ||
            table_width < 0 || table_width >= kMaxDim || table_width * page_size >= kMaxDim || batch < 0 ||
-           batch > (1 << 20) || rows * kv_heads > ((int64_t)1 << 30) || (rows > 0 && (batch == 0 || num_pages == 0));
+           batch > (1 << 20) || batch * kv_heads > (1 << 22) || rows * kv_heads > ((int64_t)1 << 28) ||
+           (rows > 0 && (batch == 0 || num_pages == 0));
 }
 
 static ql::Kv4Cache kv4_cache(const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
@@ -418,8 +419,8 @@ static ql::Kv4Cache kv4_cache(const uint8_t* cache, int64_t num_pages, int64_t p
 }
 
 static ql::Kv4Batch kv4_batch(const int32_t* table, int64_t width, const int32_t* lens, const int32_t* starts,
-                              int64_t batch) {
-    return {table, lens, starts, (int)batch, (int)width};
+                              int64_t batch, int64_t rows) {
+    return {table, lens, starts, (int)batch, (int)width, (int)rows};
 }
 
 static ql_status check_kv4_arrays(const uint8_t* cache, const int32_t* table, int64_t width, const int32_t* lens,
@@ -452,7 +453,7 @@ ql_status kv4_append(const void* k, const void* v, ql_dtype dtype, int64_t k_str
         return QL_ERR_ALIGN;
     return ql::launch_kv4_append(k, v, dtype == QL_F16, k_stride, v_stride, rows,
                                  kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
-                                 kv4_batch(block_table, table_width, seq_lens, starts, batch), as_stream(stream));
+                                 kv4_batch(block_table, table_width, seq_lens, starts, batch, rows), as_stream(stream));
 }
 
 ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
@@ -473,14 +474,14 @@ ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, i
     if (!aligned(k_out, 16) || !aligned(v_out, 16))
         return QL_ERR_ALIGN;
     return ql::launch_kv4_read(kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
-                               kv4_batch(block_table, table_width, seq_lens, starts, batch), rows, k_out, v_out,
+                               kv4_batch(block_table, table_width, seq_lens, starts, batch, rows), rows, k_out, v_out,
                                dtype == QL_F16, as_stream(stream));
 }
 
 static bool bad_kv4_attention(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t max_q, int64_t max_len,
                               int64_t window) {
     return q_heads < 1 || q_heads > 4096 || kv_heads < 1 || q_heads % kv_heads != 0 || rows < 0 ||
-           rows > (1 << 24) || rows * q_heads > ((int64_t)1 << 30) || max_q < 1 || max_q >= kMaxDim || max_len < 1 ||
+           rows > (1 << 24) || rows * q_heads > ((int64_t)1 << 28) || max_q < 1 || max_q >= kMaxDim || max_len < 1 ||
            max_len >= kMaxDim || window < 0 || window >= kMaxDim;
 }
 
@@ -531,7 +532,7 @@ ql_status attention_kv4(const void* q, int64_t q_stride, void* out, int64_t rows
     a.ws = reinterpret_cast<float*>(workspace);
     a.ws_floats = workspace_bytes / 4;
     return ql::launch_attention_kv4(a, kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
-                                    kv4_batch(block_table, table_width, seq_lens, starts, batch), as_stream(stream));
+                                    kv4_batch(block_table, table_width, seq_lens, starts, batch, rows), as_stream(stream));
 }
 
 }  // extern "C"

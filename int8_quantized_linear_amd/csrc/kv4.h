@@ -18,12 +18,12 @@
 
 namespace ql {
 
-// The batch: sequence b has the rows starts[b] .. starts[b + 1], its last positions.
+// The batch: sequence b has the rows starts[b] .. starts[b + 1] of `rows`, its last positions.
 struct Kv4Batch {
     const int32_t* table;    // [batch][width] page numbers
     const int32_t* lens;     // [batch] lengths, the rows included
     const int32_t* starts;   // [batch + 1]
-    int batch, width;
+    int batch, width, rows;
 };
 
 struct Kv4Cache {

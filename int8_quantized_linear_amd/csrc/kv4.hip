@@ -265,14 +265,11 @@ __global__ __launch_bounds__(KT) void kv4_read_kernel(Kv4Cache c, Kv4Batch b, in
     }
 }
 
-// Groups of heads, each a workgroup's loop: one head each until that makes FILL workgroups.
-constexpr int64_t FILL = 2048;   // workgroups that keep every CU busy
-
+// Groups of heads, each a workgroup's loop: as many as make FILL workgroups.
+constexpr int64_t FILL = 2048;
 inline int groups_of_heads(int64_t blocks, int heads) {
-    int n = heads;
-    while (n > 1 && n % 2 == 0 && blocks * n / 2 >= FILL)
-        n /= 2;
-    return n;
+    const int64_t n = (FILL + blocks - 1) / blocks;
+    return n < heads ? (int)n : heads;
 }
 
 }  // namespace

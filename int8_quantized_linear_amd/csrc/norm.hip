@@ -144,8 +144,13 @@ template <bool XF16, int RES, bool E4M3>
 void launch_typed(const void* x, const void* residual, const float* gamma, float eps, int64_t M, int64_t K,
                   void* res_out, int8_t* q, float* scale, hipStream_t stream) {
     const int64_t nch = K / 8;
+    constexpr int64_t MOST = (int64_t)1 << 22;   // rows of a launch: its threads stay below 2^32
     auto go = [&](auto kernel) {
-        kernel<<<dim3((uint32_t)M), dim3(NT), 0, stream>>>(x, residual, gamma, eps, K, res_out, q, scale);
+        auto at = [&](auto* p, int64_t i) { return p ? reinterpret_cast<decltype(p)>((uintptr_t)p + i) : nullptr; };
+        for (int64_t m = 0; m < M; m += MOST)
+            kernel<<<dim3((uint32_t)(M - m < MOST ? M - m : MOST)), dim3(NT), 0, stream>>>(
+                at(x, m * K * (XF16 ? 2 : 4)), at(residual, m * K * (RES == R_F16 ? 2 : 4)), gamma, eps, K,
+                at(res_out, m * K * (RES == R_F16 ? 2 : 4)), q + m * K, scale + m);
     };
     if (nch <= NT)
         go(rms_norm_quant_kernel<XF16, RES, E4M3, 1>);

@@ -140,3 +140,18 @@ def test_refusals(ql):
         f(dev(np.zeros((2, 24), np.float16)), dev(np.zeros(24, np.float32)))
     xq, xs = f(x[:0], gamma)
     assert xq.shape == (0, 64) and xs.shape == (0,)
+
+
+def test_more_rows_than_a_launch(ql):
+    """2^22 rows make one launch; the rows of the second are its own."""
+    M, K = (1 << 22) + 3, 16
+    x = torch.randn((M, K), device="cuda:0", dtype=torch.float16)
+    res = torch.randn((M, K), device="cuda:0", dtype=torch.float32)
+    gamma = torch.ones(K, device="cuda:0")
+    xq, xs, h = ql.rms_norm_quantize_int8(x, gamma, res)
+    pick = [0, 1, (1 << 22) - 1, 1 << 22, M - 1]
+    hw, t, s = ref.norm_codes(host(x[pick]), host(res[pick]), host(gamma), 127)
+    assert np.array_equal(host(xq[pick]), np.clip(np.rint(t), -127, 127).astype(np.int8))
+    assert np.array_equal(host(h[pick]), hw)
+    want = ref.norm_scale64(hw, s, 1e-6)
+    assert np.abs(host(xs[pick]).astype(np.float64) / want - 1).max() <= ((K / 256 + 10) / 2 + 5) * 2.0 ** -24
