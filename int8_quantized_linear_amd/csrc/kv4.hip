@@ -243,6 +243,23 @@ __device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
     }
 }
 
+// Values d .. of two chunks c and c + 1, held as halves (0, 32) of c in the even lanes and of c + 1
+// in the odd ones (4 lanes on): the even chunk's halves from both lanes, then the odd chunk's.
+__device__ inline void trade_store(_Float16* to, const float (&v)[2][8], bool odd) {
+    f16x8 h[2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        h[0][e] = (_Float16)v[0][e], h[1][e] = (_Float16)v[1][e];
+    const u32x4 give = __builtin_bit_cast(u32x4, odd ? h[0] : h[1]);
+    u32x4 got;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        got[e] = (uint32_t)__shfl_xor((int)give[e], 4, WAVE);
+    const u32x4 own = __builtin_bit_cast(u32x4, odd ? h[1] : h[0]);
+    __builtin_nontemporal_store(odd ? got : own, reinterpret_cast<u32x4*>(to));
+    __builtin_nontemporal_store(odd ? own : got, reinterpret_cast<u32x4*>(to + 64));
+}
+
 // Lanes of D / 16 take a row, 16 values of K and of V each: d = 64 c + 8 kg + 0 .. 7 and 32 more,
 // which are two neighbouring words of K and the 4 quads 4 kg .. 4 kg + 3 of V's chunk c. A wave
 // has 1024 / D neighbouring rows, so that V's units of 8 tokens are read whole, and goes through
@@ -265,7 +282,6 @@ __global__ __launch_bounds__(KT) void kv4_read_kernel(Kv4Cache c, Kv4Batch b, in
     const int slot = pos & (P - 1);
     const int k_at = L::k_codes(slot) + (kg * (D / 32) + 2 * ch) * 4;
     const int v_at = L::v_codes(P, slot / 8) + (ch * 16 + kg * 4) * 16 + slot % 8 * 2;
-#pragma unroll 2
     for (int head = h0; head < h1; ++head) {
         float kx[2][8] = {}, vx[2][8] = {};
         if (on) {
@@ -286,11 +302,22 @@ __global__ __launch_bounds__(KT) void kv4_read_kernel(Kv4Cache c, Kv4Batch b, in
                 }
             }
         }
-        const int64_t at = ((int64_t)row * c.heads + head) * D + d0;
+        const int64_t at = ((int64_t)row * c.heads + head) * D;
+        if constexpr (F16 && D >= 128) {
+            // 32 values (64 bytes) of a row in each half and 4 lanes: lanes of neighbouring chunks
+            // trade halves, so that 8 lanes write 128 bytes together, past the caches. (Left dirty
+            // in them, the 100 MB of 24600 rows of 8 heads hold up the next kernel: 49 us a write
+            // and a read of these sizes, 36 like this.)
+            const bool odd = ch & 1;
+            const int64_t even_at = at + (ch & ~1) * 64 + kg * 8 + (odd ? 32 : 0);
+            trade_store(reinterpret_cast<_Float16*>(k_out) + even_at, kx, odd);
+            trade_store(reinterpret_cast<_Float16*>(v_out) + even_at, vx, odd);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            store8<F16>(k_out, at + 32 * h, kx[h]);
-            store8<F16>(v_out, at + 32 * h, vx[h]);
+            for (int h = 0; h < 2; ++h) {
+                store8<F16>(k_out, at + d0 + 32 * h, kx[h]);
+                store8<F16>(v_out, at + d0 + 32 * h, vx[h]);
+            }
         }
         page += c.head_bytes;
     }
