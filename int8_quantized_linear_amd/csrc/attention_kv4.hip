@@ -279,14 +279,24 @@ __device__ inline f16x2 codes_int(uint32_t w, const Masks& mk) {
         return as_f16x2((h & mk.even) | mk.k1024) - (f16x2){(_Float16)1024.0f, (_Float16)1024.0f};
 }
 
-// v as two fp16 terms.
+// v as two fp16 terms: hi rounded to nearest, lo = fp16(v - hi). The factor -1 is kept from the
+// compiler's sight so that each difference and its rounding stay one mixed-precision instruction on
+// the packed hi; written as a subtraction, hi is converted twice and back once.
 __device__ inline void two_terms(const float (&v)[8], f16x8& hi, f16x8& lo) {
+    u32x4 h, l;
+    float minus = -1.f;
+    asm("" : "+s"(minus));
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        hi[e] = (_Float16)v[e];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        lo[e] = (_Float16)fmaf((float)hi[e], -1.0f, v[e]);
+    for (int e = 0; e < 4; ++e) {
+        f16x2 a{(_Float16)v[2 * e], (_Float16)v[2 * e + 1]};
+        h[e] = as_u32(a);
+        asm("" : "+v"(h[e]));
+        a = as_f16x2(h[e]);
+        l[e] = as_u32(f16x2{(_Float16)fmaf((float)a[0], minus, v[2 * e]),
+                            (_Float16)fmaf((float)a[1], minus, v[2 * e + 1])});
+    }
+    hi = __builtin_bit_cast(f16x8, h);
+    lo = __builtin_bit_cast(f16x8, l);
 }
 
 // V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16.
@@ -805,19 +815,17 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
         const int w_all_end = max(0, t.first + w0 / R + 1);
         const int w_all_begin = a.window ? max(0, t.first + wl / R + 1 - a.window) : 0;
 
-        f32x4 o[NQ][D / 16], l[NQ];
+        f32x4 o[NQ][D / 16];
         f16x8 p[NQ][XT / 2], pl[NQ][XT / 2];
-        float m[NQ];
+        float m[NQ], l[NQ];   // l: the lane's tokens' part of the weights' sum
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
                 o[u][i] = f32x4{0, 0, 0, 0};
-            l[u] = f32x4{0, 0, 0, 0};
+            l[u] = 0.0f;
             m[u] = M_NONE;
         }
-        const _Float16 one = (_Float16)1.0f;
-        const f16x8 ones = {one, one, one, one, one, one, one, one};
 
         u32x2 kw;
         _Float16 ks[2], kl[2];
@@ -971,7 +979,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                     const float mn = fmaxf(m[u], top);
                     const float f = __builtin_amdgcn_exp2f(m[u] - mn);
                     m[u] = mn;
-                    l[u][0] *= f;
+                    l[u] *= f;
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x)
                         o[u][x] *= f;
@@ -983,6 +991,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         w[e] = __builtin_amdgcn_exp2f(fmaf(s[u][2 * y + e / 4][e % 4], kappa, shift));
+                    l[u] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
                     two_terms(w, p[u][y], pl[u][y]);
                 }
             }
@@ -1004,13 +1013,6 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                         to[x][y] = vt[vb][4 * y + kg][16 * (x0 + x) + n];
             };
             read(f, 0);
-#pragma unroll
-            for (int u = 0; u < NQ; ++u)
-#pragma unroll
-                for (int y = 0; y < XT / 2; ++y) {
-                    l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u][y], l[u], 0, 0, 0);
-                    l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[u][y], l[u], 0, 0, 0);
-                }
 #pragma unroll
             for (int x0 = 0; x0 < D / 16; x0 += STEP) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -1078,8 +1080,10 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
             const int idx = tile * PER + (wave * NQ + u) * 16 + n, i = idx / R, row = b.starts[seq] + i;
+            float sum = l[u] + __shfl_xor(l[u], 16, WAVE);
+            sum += __shfl_xor(sum, 32, WAVE);
             if (i < t.rows && row < a.rows) {
-                const float inv = l[u][0] > 0.0f ? 1.0f / l[u][0] : 0.0f;
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
                 _Float16* to = a.out + ((int64_t)row * a.q_heads + head * R + idx % R) * D;
                 // o's tile x, register r: d = 16 x + 4 kg + r
 #pragma unroll
