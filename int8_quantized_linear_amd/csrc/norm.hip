@@ -7,7 +7,13 @@
 // in y / (max|y| / 127): the codes are those of t = h * gamma with s = max|t| / 127, and r
 // enters the row's scale only, scale = s * r. The codes therefore need one rounding each for h,
 // t, s and t / s, whatever the order in which the squares are summed, and the kernel needs one
-// reduction (the maximum and the sum of squares together) and one pass over the row.
+// reduction (the maximum and the sum of squares together) and one pass over the row. (The squares
+// and their sum are fp32.)
+//
+// Bound by memory: every value is read and written once. 2048 rows of 11008 (fp16 x and residual,
+// in and out, int8 codes: 158 MB) take 36 us, 4.4 TB/s, where a large copy reaches 5.0; 2048 of
+// 4096 15.2 us from cold memory, 11 us where the caches hold part of it; one row of 4096 3.0 us,
+// a launch and the row's one chain of load, reduction and store.
 #include "quant_codes.h"
 
 namespace ql {
@@ -49,8 +55,12 @@ __device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
 enum { R_NONE = 0, R_F16 = 1, R_F32 = 2 };
 
 // One workgroup per row of K = 8 * nch values. NC > 0: rows of up to NT * NC chunks of 8 stay in
-// registers. NC == 0: longer rows are read twice (the statistics, then h and the codes; h is
-// written in the second pass only, so that res_out may be the residual itself).
+// registers. Short rows get a smaller NC, which leaves the CUs room for more of them: 8192 rows of
+// 1024 take 14.7 us with NC = 1 and 22.3 with 8, 2048 of 4096 15.2 with 2 and 15.6 with 8. (4 for
+// rows up to 8192 lost: 2048 of 8192 29.5, with 8 27.0. So did loading all chunks before the first
+// store, which doubles the registers: 2048 of 16384 52.5, chunk by chunk 47.5.) NC == 0: longer rows
+// are read twice (the statistics, then h and the codes; h is written in the second pass only, so
+// that res_out may be the residual itself): 2048 rows of 16384 take 64 us so.
 template <bool XF16, int RES, bool E4M3, int NC>
 __global__ __launch_bounds__(NT) void rms_norm_quant_kernel(const void* __restrict__ x, const void* residual,
                                                             const float* __restrict__ gamma, float eps, int64_t K,
@@ -156,8 +166,6 @@ void launch_typed(const void* x, const void* residual, const float* gamma, float
         go(rms_norm_quant_kernel<XF16, RES, E4M3, 1>);
     else if (nch <= 2 * NT)
         go(rms_norm_quant_kernel<XF16, RES, E4M3, 2>);
-    else if (nch <= 4 * NT)
-        go(rms_norm_quant_kernel<XF16, RES, E4M3, 4>);
     else if (nch <= 8 * NT)
         go(rms_norm_quant_kernel<XF16, RES, E4M3, 8>);
     else
