@@ -1109,16 +1109,28 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
 constexpr int64_t FILL = 512;                      // workgroups that two on each CU make
 constexpr int64_t MAX_GROUPS = (int64_t)1 << 22;   // of a launch (threads stay below 2^32); the kernels loop
 
-// Whether the prompt kernel takes a call: its workgroups each hold a CU and are not split over the
-// length, so it needs nearly a chip of them. Cycles a token of the length, as measured on 8 kv
-// heads with 4 query heads each: a round of prompt workgroups, and a decode tile of 32 rows as a
-// share of the whole chip. (D = 128: 4 sequences of 2048 rows take 265 us against the decode
-// kernel's 392, 17 rows over 65536 tokens 2680 us against 98.)
-inline int prompt_rows(int D) { return D == 256 ? 128 : 256; }
-inline bool use_prompt(int64_t pairs, int64_t heads, int D) {
-    const double round = D == 64 ? 80.0 : D == 128 ? 106.0 : 118.0, tile = D == 64 ? 0.043 : D == 128 ? 0.086 : 0.164;
-    const int64_t workgroups = heads * ((pairs + prompt_rows(D) - 1) / prompt_rows(D));
-    return tile * (double)(heads * ((pairs + 31) / 32)) > round * (double)((workgroups + 255) / 256);
+// Blocks of 16 (row, head) pairs that each wave of the prompt kernel takes, or 0 for the decode
+// kernel. Costs in cycles a token of the longest length, as measured on 8 kv heads with 1 and 4 query heads each:
+// a round of prompt workgroups, which each hold a CU and are not split over the length, and a decode
+// tile of 32 pairs as a share of the whole chip. Rows see `mean` of the longest length on average;
+// decode tiles and prompt workgroups past the first round make use of that, a first round lasts as
+// long as its longest. In us, 1 x 2048 rows of 2048 positions (D = 128): one block a wave 88, two
+// 104, decode 109; 1 x 2048 of 4096: 210, 192, 242; 4 x 1024 of 1024: 101, 78, 128; 1 x 512 of
+// 8192: 234, 334, 150; 16 x 64 of 2048: 71, 98, 73. D = 64 in blocks of two gains nowhere (4 x 2048
+// of 2048: 178, 183, 225; 16 x 500 of 500: 61, 72, 100), D = 256 has registers for one only.
+inline int prompt_blocks(int64_t pairs, int64_t heads, int D, int max_q, int max_len, int window) {
+    const double one = D == 64 ? 30.0 : D == 128 ? 76.0 : 100.0, two = 106.0;
+    const double first = D == 64 ? 13.5 : 0.0;   // two workgroups share a CU: a round alone costs more
+    const double tile = D == 64 ? 0.043 : D == 128 ? 0.086 : 0.164;
+    const double longest = window > 0 ? std::min(max_len, window) : max_len;
+    const double mean = std::min(max_len - 0.5 * std::min(max_q, max_len), longest) / longest;
+    const auto cost = [&](double round, int64_t per) {
+        const int64_t workgroups = heads * ((pairs + per - 1) / per);
+        return first + round * std::max(1.0, mean * (double)((workgroups + 255) / 256));
+    };
+    const double decode = mean * tile * (double)(heads * ((pairs + 31) / 32));
+    const double of_one = cost(one, 128), of_two = D == 128 ? cost(two, 256) : of_one;
+    return decode <= std::min(of_one, of_two) ? 0 : of_two < of_one ? 2 : 1;
 }
 
 // Rows of a decode tile: 16, or 32 where a sequence has more and two tiles' O and Q fit in the
@@ -1154,7 +1166,7 @@ Split plan(int q_heads, int kv_heads, int D, int batch, int max_q, int max_len, 
 int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
                                 int window) {
     max_q = (int)std::min<int64_t>(max_q, std::max<int64_t>(rows, 1));
-    if (use_prompt((int64_t)max_q * (q_heads / kv_heads), (int64_t)batch * kv_heads, D))
+    if (prompt_blocks((int64_t)max_q * (q_heads / kv_heads), (int64_t)batch * kv_heads, D, max_q, max_len, window))
         return 0;
     const Split s = plan(q_heads, kv_heads, D, batch, max_q, max_len, window);
     return s.n == 1 ? 0 : s.n * rows * q_heads * (D + 2);
@@ -1164,17 +1176,26 @@ ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G
                                hipStream_t stream) {
     const int max_q = std::min(a.max_q, a.rows);
     const int64_t pairs = (int64_t)max_q * (a.q_heads / c.heads);
-    if (use_prompt(pairs, (int64_t)b.batch * c.heads, D))
+    const int nq = prompt_blocks(pairs, (int64_t)b.batch * c.heads, D, max_q, a.max_len, a.window);
+    if (nq)
         return kv4_dispatch(D, G, [&](auto d, auto g) {
-            constexpr int DD = decltype(d)::value, GG = decltype(g)::value, NQ = DD == 256 ? 1 : 2;
-            const int64_t heads = (int64_t)c.heads * b.batch;
-            const int tiles = (int)std::min((pairs + prompt_rows(DD) - 1) / prompt_rows(DD), std::max<int64_t>(1, MAX_GROUPS / heads));
-            const int P = 1 << c.page_log2;
+            constexpr int DD = decltype(d)::value, GG = decltype(g)::value;
+            const int64_t heads = (int64_t)c.heads * b.batch, rows = 128 * nq;
+            const int tiles = (int)std::min((pairs + rows - 1) / rows, std::max<int64_t>(1, MAX_GROUPS / heads));
             const dim3 grid((uint32_t)(heads * tiles));
-            if (P >= prompt_block(DD))
-                attention_kv4_prompt_kernel<DD, GG, true, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
-            else
-                attention_kv4_prompt_kernel<DD, GG, false, NQ><<<grid, PT, 0, stream>>>(a, c, b, tiles);
+            const bool big = (1 << c.page_log2) >= prompt_block(DD);
+            auto go = [&](auto kernel) { kernel<<<grid, PT, 0, stream>>>(a, c, b, tiles); };
+            if (nq == 1) {
+                if (big)
+                    go(attention_kv4_prompt_kernel<DD, GG, true, 1>);
+                else
+                    go(attention_kv4_prompt_kernel<DD, GG, false, 1>);
+            } else if constexpr (DD == 128) {
+                if (big)
+                    go(attention_kv4_prompt_kernel<DD, GG, true, 2>);
+                else
+                    go(attention_kv4_prompt_kernel<DD, GG, false, 2>);
+            }
             return launch_status();
         });
     const int per = rows_per_tile(pairs, D);
