@@ -432,9 +432,13 @@ ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, i
  *   out[r,h] = sum_j softmax_j(scale * q[r,h] . k[j,h']) v[j,h'],  h' = h / (q_heads / kv_heads)
  * over the positions j that row r sees: j <= p for a row at position p, and j > p - window if
  * window > 0. Keys of the call's own rows have to be in the cache already. A row without a
- * position sees nothing and gives zeros; what the cache holds at positions that a row does not
- * see (stale values, NaN) does not reach it. Products in fp16 on the matrix cores with fp32
- * sums, softmax statistics in fp32.
+ * position sees nothing and gives zeros. Bytes at positions that no row of the sequence sees may
+ * be anything (stale values, NaN); those that one row sees and another does not have to be pairs
+ * as kv4_append writes them (finite), and reach only the rows that see them, however large.
+ * Products in fp16 on the matrix cores with fp32 sums, softmax statistics in fp32. V enters as
+ * fp16 values, each rounded once; rows beside a value past fp16's 65504 (a pair stands for up to
+ * 1048064) take 1/16 of all their values, rounded to multiples of 2^-20 at least. An output past
+ * fp16 is infinite.
  *
  * q       [rows][q_heads][D] fp16, row r at q + r * q_stride elements; 16-byte aligned,
  *         q_stride a multiple of 8 and at least q_heads * D

@@ -301,14 +301,40 @@ __device__ inline void two_terms(const float (&v)[8], f16x8& hi, f16x8& lo) {
     lo = __builtin_bit_cast(f16x8, l);
 }
 
-// V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16.
-template <int JJ>
+// V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16. A stored
+// pair goes up to 15 * 65504 + 65504, past fp16 (fp32 rows that large, and pairs of rows near 65504
+// whose rounding passes it by up to 32), and an infinite value times another row's weight of 0 is
+// NaN. Operands are therefore taken as they are at first. Only if that leaves a sum that is not
+// finite (an infinite operand always does), the rows are done again with WIDE: 1 / 16 of every
+// value, which holds all that a pair can stand for, low / 16 and the value rounded to multiples of
+// 2^-24 at least.
+template <int JJ, bool WIDE>
 __device__ inline f16x8 v_values(u32x4 w, u32x4 s, u32x4 l, const Masks& mk) {
+    const f16x2 part = {(_Float16)0.0625f, (_Float16)0.0625f};
     u32x4 r;
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-        r[p] = as_u32(__builtin_elementwise_fma(codes_int<JJ>(w[p], mk), as_f16x2(s[p]), as_f16x2(l[p])));
+    for (int p = 0; p < 4; ++p) {
+        f16x2 c = codes_int<JJ>(w[p], mk), low = as_f16x2(l[p]);
+        if constexpr (WIDE)
+            c *= part, low *= part;
+        r[p] = as_u32(__builtin_elementwise_fma(c, as_f16x2(s[p]), low));
+    }
     return __builtin_bit_cast(f16x8, r);
+}
+constexpr float WIDE_UNIT = 16.0f;
+
+// Whether a sum of the wave is infinite or NaN.
+template <int N, int M>
+__device__ inline bool any_not_finite(const f32x4 (&o)[N][M]) {
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                z = fmaf(o[i][j][r], 0.0f, z);
+    return __any(z != 0.0f);
 }
 
 __device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2])[i & 1]; }
@@ -369,22 +395,26 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         uint8_t* slots = lds + wave * (SLOTS * RG::BYTES);
         const uint32_t k_at = lds_addr(slots) + RG::k_at(), v_at = lds_addr(slots) + RG::v_at(),
                        p_at = lds_addr(slots) + RG::p_at();
-        int t0 = from + wave * TB;   // the block in use
-        uint32_t pa = 0, pb = 0;     // pages of the block to be copied next
+        int t0;                    // the block in use
+        uint32_t pa = 0, pb = 0;   // pages of the block to be copied next
         auto pages = [&](int pos) {
             if (pos < to) {
                 pa = ring.page_of(pos);
                 pb = BIG ? pa : ring.page_of(pos + 16);
             }
         };
-        __syncthreads();   // the last tile's partial results have been read
+        auto begin = [&] {
+            t0 = from + wave * TB;
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            pages(t0 + i * AW * TB);
-            if (t0 + i * AW * TB < to)
-                ring.copy(slots + i * RG::BYTES, t0 + i * AW * TB, pa, pb);
-        }
-        pages(t0 + SLOTS * AW * TB);
+            for (int i = 0; i < SLOTS; ++i) {
+                pages(t0 + i * AW * TB);
+                if (t0 + i * AW * TB < to)
+                    ring.copy(slots + i * RG::BYTES, t0 + i * AW * TB, pa, pb);
+            }
+            pages(t0 + SLOTS * AW * TB);
+        };
+        __syncthreads();   // the last tile's partial results have been read
+        begin();
 
         // Q's operand: column n of each row tile, slots 2, 3, 6, 7 of every 8 divided by 16
         f16x8 q[NQ][NI];
@@ -424,18 +454,11 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 
         f32x4 o[NQ][D / 16], l[NQ];
         float m[NQ];
-#pragma unroll
-        for (int u = 0; u < NQ; ++u) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                o[u][i] = f32x4{0, 0, 0, 0};
-            l[u] = f32x4{0, 0, 0, 0};
-            m[u] = M_NONE;
-        }
         const _Float16 one = (_Float16)1.0f;
         const f16x8 ones = {one, one, one, one, one, one, one, one};
 
-        auto step = [&](uint32_t at) {
+        auto step = [&](uint32_t at, auto wide) {
+            constexpr bool WIDE = decltype(wide)::value;
             const bool edge = t0 < t.all_begin || t0 + TB > t.all_end;   // some row does not see all of it
             f32x4 s[NQ][2];
             uint32_t kw[2][NI];
@@ -536,8 +559,9 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) {
                 const int g0 = 64 * ch / G, g1 = (64 * ch + 32) / G;
-                const f16x8 vv[4] = {v_values<0>(vw[ch], vs[g0], vl[g0], mk), v_values<1>(vw[ch], vs[g0], vl[g0], mk),
-                                     v_values<2>(vw[ch], vs[g1], vl[g1], mk), v_values<3>(vw[ch], vs[g1], vl[g1], mk)};
+                const f16x8 vv[4] = {
+                    v_values<0, WIDE>(vw[ch], vs[g0], vl[g0], mk), v_values<1, WIDE>(vw[ch], vs[g0], vl[g0], mk),
+                    v_values<2, WIDE>(vw[ch], vs[g1], vl[g1], mk), v_values<3, WIDE>(vw[ch], vs[g1], vl[g1], mk)};
                 // the second terms after all first ones: a product that waits for the one before
                 // it on the same sum would stall
                 auto add = [&](const f16x8(&w)[NQ]) {
@@ -552,19 +576,36 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             }
         };
 
-        for (uint32_t at = 0; t0 < to; t0 += AW * TB) {
-            // the block's copies have landed when only the younger slots' are pending
-            if (t0 + (SLOTS - 1) * AW * TB < to)
-                __builtin_amdgcn_s_waitcnt(vmcnt_le((SLOTS - 1) * RG::COPIES));
-            else
-                __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
-            __builtin_amdgcn_sched_barrier(0);
-            step(at);
-            __builtin_amdgcn_sched_barrier(0);
-            if (t0 + SLOTS * AW * TB < to)
-                ring.copy(slots + at, t0 + SLOTS * AW * TB, pa, pb);
-            pages(t0 + (SLOTS + 1) * AW * TB);
-            at = at + RG::BYTES == SLOTS * RG::BYTES ? 0 : at + RG::BYTES;
+        auto walk = [&](auto wide) {
+#pragma unroll
+            for (int u = 0; u < NQ; ++u) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    o[u][i] = f32x4{0, 0, 0, 0};
+                l[u] = f32x4{0, 0, 0, 0};
+                m[u] = M_NONE;
+            }
+            for (uint32_t at = 0; t0 < to; t0 += AW * TB) {
+                // the block's copies have landed when only the younger slots' are pending
+                if (t0 + (SLOTS - 1) * AW * TB < to)
+                    __builtin_amdgcn_s_waitcnt(vmcnt_le((SLOTS - 1) * RG::COPIES));
+                else
+                    __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
+                __builtin_amdgcn_sched_barrier(0);
+                step(at, wide);
+                __builtin_amdgcn_sched_barrier(0);
+                if (t0 + SLOTS * AW * TB < to)
+                    ring.copy(slots + at, t0 + SLOTS * AW * TB, pa, pb);
+                pages(t0 + (SLOTS + 1) * AW * TB);
+                at = at + RG::BYTES == SLOTS * RG::BYTES ? 0 : at + RG::BYTES;
+            }
+        };
+        walk(std::false_type{});
+        float unit = 1.0f;   // of the wave's sums
+        if (any_not_finite(o)) {
+            begin();   // the last copies have landed and been read
+            walk(std::true_type{});
+            unit = WIDE_UNIT;
         }
 
         // join the waves: each brings its O to the largest maximum
@@ -580,7 +621,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 #pragma unroll
             for (int w = 1; w < AW; ++w)
                 top = fmaxf(top, stats[w][n][0]);
-            const float f = __builtin_amdgcn_exp2f(m[u] - top);
+            const float f = __builtin_amdgcn_exp2f(m[u] - top) * unit;
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch)
 #pragma unroll
@@ -740,8 +781,9 @@ __device__ inline bf16x8 bf16_terms(float a, float b, float c, float d, float e,
     return __builtin_bit_cast(bf16x8, (u32x4){two(a, b), two(c, d), two(e, f), 0u});
 }
 
+// Two workgroups of a CU for D = 64, whose LDS has room for them: 128 registers.
 template <int D, int G, bool BIG, int NQ>
-__global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b, int tiles) {
+__global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kernel(Kv4Attn a, Kv4Cache c, Kv4Batch b, int tiles) {
     using L = Kv4Layout<D, G>;
     constexpr int PB = prompt_block(D), XT = PB / 16, NI = D / 32, NG = D / G, NL = (NG + 3) / 4, PER = 128 * NQ;
     constexpr int PARTS = D * PB / 16;   // threads' parts of a block
@@ -749,6 +791,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
     __shared__ __attribute__((aligned(16))) f16x8 kt[3][D / 8][PB], vt[4][PB / 8][D];
     __shared__ __attribute__((aligned(16))) u32x4 lowt[3][NG][PB];   // low's terms
     __shared__ __attribute__((aligned(16))) _Float16 sct[3][NG][PB];
+    __shared__ int again;   // some wave's sums are not finite
     const int R = a.q_heads / c.heads, P = 1 << c.page_log2;
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), n = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -825,14 +868,6 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
         f32x4 o[NQ][D / 16];
         f16x8 p[NQ][XT / 2], pl[NQ][XT / 2];
         float m[NQ], l[NQ];   // l: the lane's tokens' part of the weights' sum
-#pragma unroll
-        for (int u = 0; u < NQ; ++u) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                o[u][i] = f32x4{0, 0, 0, 0};
-            l[u] = 0.0f;
-            m[u] = M_NONE;
-        }
 
         u32x2 kw;
         _Float16 ks[2], kl[2];
@@ -865,7 +900,8 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                 vl = *reinterpret_cast<const u32x4*>(pv + (L::v_low(P, g) + 2 * vslot));
             }
         };
-        auto put = [&](int i, int kb, int vb) {
+        auto put = [&](int i, int kb, int vb, auto wide) {
+            constexpr bool WIDE = decltype(wide)::value;
             const int t0 = from + i * PB;
             if (mine) {
 #pragma unroll
@@ -896,8 +932,8 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                 for (int x = 0; x < 4; ++x)
                     w[x] >>= 8 * half;
                 f16x8* to = &vt[vb][t8][quad / 16 * 64 + half * 32 + quad % 16 * 2];
-                to[0] = v_values<0>(w, vs, vl, mk);
-                to[1] = v_values<1>(w, vs, vl, mk);
+                to[0] = v_values<0, WIDE>(w, vs, vl, mk);
+                to[1] = v_values<1, WIDE>(w, vs, vl, mk);
             }
         };
         // The operands of the next rows of products are read while the present ones run; the
@@ -1047,13 +1083,22 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        __syncthreads();   // the last tile's blocks have been read
-        if (nb > 0) {
+        auto walk = [&](auto wide) {
+#pragma unroll
+            for (int u = 0; u < NQ; ++u) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    o[u][i] = f32x4{0, 0, 0, 0};
+                l[u] = 0.0f;
+                m[u] = M_NONE;
+            }
+            if (nb == 0)
+                return;
             load(0);
-            put(0, 0, 0);
+            put(0, 0, 0, wide);
             if (nb > 1) {
                 load(1);
-                put(1, 1, 1);
+                put(1, 1, 1, wide);
             }
             if (nb > 2)
                 load(2);
@@ -1072,7 +1117,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
                 phase_end();
                 softmax(s, i);
                 if (i + 2 < nb) {
-                    put(i + 2, kb == 0 ? 2 : kb - 1, (i + 2) & 3);
+                    put(i + 2, kb == 0 ? 2 : kb - 1, (i + 2) & 3, wide);
                     if (i + 3 < nb)
                         load(i + 3);
                 }
@@ -1082,6 +1127,22 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
             values((nb - 1) & 3);
             if (wave < 4)
                 phase_end();
+        };
+        __syncthreads();   // the last tile's blocks have been read, and its `again`
+        if (tid == 0)
+            again = 0;
+        float unit = 1.0f;   // of the sums
+        walk(std::false_type{});
+        if (nb > 0) {
+            // the operands are shared, so all waves go again (a barrier at least lies between the
+            // walk's start and its end)
+            if (any_not_finite(o) && lane == 0)
+                again = 1;
+            __syncthreads();
+            if (__builtin_amdgcn_readfirstlane(again)) {
+                walk(std::true_type{});
+                unit = WIDE_UNIT;
+            }
         }
 
 #pragma unroll
@@ -1090,7 +1151,7 @@ __global__ __launch_bounds__(PT, 2) void attention_kv4_prompt_kernel(Kv4Attn a, 
             float sum = l[u] + __shfl_xor(l[u], 16, WAVE);
             sum += __shfl_xor(sum, 32, WAVE);
             if (i < t.rows && row < a.rows) {
-                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                const float inv = sum > 0.0f ? unit / sum : 0.0f;
                 _Float16* to = a.out + ((int64_t)row * a.q_heads + head * R + idx % R) * D;
                 // o's tile x, register r: d = 16 x + 4 kg + r
 #pragma unroll
