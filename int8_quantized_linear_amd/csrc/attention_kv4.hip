@@ -326,15 +326,15 @@ constexpr float WIDE_UNIT = 16.0f;
 // Whether a sum of the wave is infinite or NaN.
 template <int N, int M>
 __device__ inline bool any_not_finite(const f32x4 (&o)[N][M]) {
-    float z = 0.0f;
+    float z[4] = {};   // four chains
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < M; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                z = fmaf(o[i][j][r], 0.0f, z);
-    return __any(z != 0.0f);
+                z[r] = fmaf(o[i][j][r], 0.0f, z[r]);
+    return __any((z[0] + z[1]) + (z[2] + z[3]) != 0.0f);
 }
 
 __device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2])[i & 1]; }
