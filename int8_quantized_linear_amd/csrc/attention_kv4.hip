@@ -12,7 +12,8 @@
 // joined through LDS at the end, the stretches' by a second kernel.
 //   S^T = K Q^T   16x16x32 fp16: rows are tokens, columns the tile's rows. K's codes enter as
 //                 fp16 integers (the masked nibbles are fp16 subnormals c 2^-24 or 16 c 2^-24,
-//                 which the matrix cores take exactly; q's slots carry the 1/16), one product
+//                 which the matrix cores take exactly; q's slots carry the 1/16, and a power of
+//                 two where q is small enough to lose bits by it), one product
 //                 for each group of G values, and scale and low are applied to the fp32 product:
 //                 s_t sum_d c q_d + low_t sum_d q_d.
 //   O^T = V^T P^T the products' layout hands each lane the weights of 8 consecutive tokens for
@@ -37,6 +38,7 @@ namespace ql {
 namespace {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int AT = 256, AW = AT / WAVE;   // threads and waves of a decode workgroup
 constexpr int TB = 32;                    // tokens of a step
@@ -301,6 +303,69 @@ __device__ inline void two_terms(const float (&v)[8], f16x8& hi, f16x8& lo) {
     lo = __builtin_bit_cast(f16x8, l);
 }
 
+// Q's operand of one column, lane kg's d = 32 i + 8 kg + 0 .. 7, from q at `src` (zeros if !ok), and
+// for each group the sum of q over it: both 2^e times as large, the operand times `sign`, its slots
+// 2, 3, 6 and 7 divided by 16 for codes that stand 16 times as high, the sums times sign 2^-24.
+// Returns e. The division rounds to 2^-24, which costs q below 2^-10 bits. Beside others of 1/4 and
+// more that is less than the fp32 sums' own rounding, and e is 0; a wave with a lane whose q are all
+// smaller brings the largest |q| of each column to 2^14 (by 2^30 at most, with which the smallest
+// fp16 number is 64). Done in every wave, that took 0.25 us of a call.
+template <int D, int G>
+__device__ inline int q_column(const _Float16* src, bool ok, float sign, f16x8 (&q)[D / 32], float (&qsum)[D / G]) {
+    f16x8 big = {};
+#pragma unroll
+    for (int g = 0; g < D / G; ++g)
+        qsum[g] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        f16x8 x = {};
+        if (ok)
+            x = *reinterpret_cast<const f16x8*>(src + 32 * i);
+        big = __builtin_elementwise_max(big, __builtin_elementwise_abs(x));
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s += (float)x[e];
+        q[i] = x;
+        qsum[i / (G / 32)] += s;
+    }
+#pragma unroll
+    for (int g = 0; g < D / G; ++g) {
+        qsum[g] += __shfl_xor(qsum[g], 16, WAVE);
+        qsum[g] += __shfl_xor(qsum[g], 32, WAVE);
+        qsum[g] *= sign * 5.9604644775390625e-08f;   // 2^-24
+    }
+    const f16x4 four = __builtin_elementwise_max(__builtin_shufflevector(big, big, 0, 1, 2, 3),
+                                                 __builtin_shufflevector(big, big, 4, 5, 6, 7));
+    const f16x2 two = __builtin_elementwise_max(__builtin_shufflevector(four, four, 0, 1),
+                                                __builtin_shufflevector(four, four, 2, 3));
+    float top = fmaxf((float)two[0], (float)two[1]);
+    int e = 0;
+    if (__any(ok && top < 0.25f)) {
+        top = fmaxf(top, __shfl_xor(top, 16, WAVE));
+        top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+        e = min(max(127 + 14 - (int)(__float_as_uint(top) >> 23), 0), 30);
+        const _Float16 a = (_Float16)ldexpf(1.0f, e / 2), b = (_Float16)ldexpf(1.0f, e - e / 2);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            q[i] = q[i] * (f16x8){a, a, a, a, a, a, a, a} * (f16x8){b, b, b, b, b, b, b, b};
+#pragma unroll
+        for (int g = 0; g < D / G; ++g)
+            qsum[g] = ldexpf(qsum[g], e);
+    }
+    const _Float16 one = (_Float16)sign, part = (_Float16)(sign * 0.0625f);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        q[i] *= (f16x8){one, one, part, part, one, one, part, part};
+    return e;
+}
+
+// What a score's sums are multiplied by for the softmax in base 2: the codes' 2^-24 and q's 2^e
+// taken out. Not 0, so that a masked score stays the smallest.
+__device__ inline float to_base2(float scale, int e) {
+    return fmaxf(ldexpf(fabsf(scale) * 1.44269504088896f, 24 - e), 1e-30f);
+}
+
 // V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16. A stored
 // pair goes up to 15 * 65504 + 65504, past fp16 (fp32 rows that large, and pairs of rows near 65504
 // whose rounding passes it by up to 32), and an infinite value times another row's weight of 0 is
@@ -364,8 +429,6 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
     const int lane = threadIdx.x & (WAVE - 1), n = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const Masks mk;
-    // the codes' 2^-24 taken out; not 0, so that a masked score stays the smallest
-    const float kappa = fmaxf(fabsf(a.scale) * 1.44269504088896f * 16777216.0f, 1e-30f);
     const float sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
 
     for (int tile = tile0;; tile += sp.tiles) {
@@ -416,9 +479,9 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         __syncthreads();   // the last tile's partial results have been read
         begin();
 
-        // Q's operand: column n of each row tile, slots 2, 3, 6, 7 of every 8 divided by 16
+        // Q's operand: column n of each row tile
         f16x8 q[NQ][NI];
-        float qsum[NQ][NG];
+        float qsum[NQ][NG], kappa[NQ];
         int rbeg[NQ], rend[NQ];
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
@@ -427,29 +490,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             rend[u] = ok ? max(0, t.first + i + 1) : 0;
             rbeg[u] = a.window ? max(0, rend[u] - a.window) : 0;
             const _Float16* src = a.q + (int64_t)(ok ? row : 0) * a.q_stride + (int64_t)(head * R + idx % R) * D + kg * 8;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                qsum[u][g] = 0.0f;
-#pragma unroll
-            for (int i8 = 0; i8 < NI; ++i8) {
-                f16x8 x = {};
-                if (ok)
-                    x = *reinterpret_cast<const f16x8*>(src + 32 * i8);
-                float s = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s += (float)x[e];
-                    x[e] *= (_Float16)(e & 2 ? sign * 0.0625f : sign);
-                }
-                q[u][i8] = x;
-                qsum[u][i8 / (G / 32)] += s;
-            }
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                qsum[u][g] += __shfl_xor(qsum[u][g], 16, WAVE);
-                qsum[u][g] += __shfl_xor(qsum[u][g], 32, WAVE);
-                qsum[u][g] *= sign * 5.9604644775390625e-08f;   // 2^-24
-            }
+            kappa[u] = to_base2(a.scale, q_column<D, G>(src, ok, sign, q[u], qsum[u]));
         }
 
         f32x4 o[NQ][D / 16], l[NQ];
@@ -512,7 +553,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         top = fmaxf(top, s[u][h][r]);
-                top *= kappa;
+                top *= kappa[u];
                 if (__any(top > m[u] + M_SLACK)) {
                     top = fmaxf(top, __shfl_xor(top, 16, WAVE));
                     top = fmaxf(top, __shfl_xor(top, 32, WAVE));
@@ -531,7 +572,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        w[4 * h + r] = __builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa, shift));
+                        w[4 * h + r] = __builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa[u], shift));
                 two_terms(w, p[u], pl[u]);
                 l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u], l[u], 0, 0, 0);
                 l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[u], l[u], 0, 0, 0);
@@ -763,7 +804,6 @@ __global__ __launch_bounds__(AT) void attention_kv4_join_kernel(const float* __r
 constexpr int PT = 512;   // threads
 constexpr int prompt_block(int D) { return D == 256 ? 32 : 64; }   // tokens of a block: 126 KB of LDS
 
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Workgroup barrier for LDS alone: loads into registers stay in flight across it.
@@ -802,7 +842,6 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
     // the sequence's last tiles see most: they start first
     const int tile0 = tiles - 1 - id / b.batch;
     const Masks mk;
-    const float kappa = fmaxf(fabsf(a.scale) * 1.44269504088896f * 16777216.0f, 1e-30f);   // as in the decode kernel
     const float sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
 
     // The thread's part of a block: of K two words, d = 32 (2 j + z) + 8 kgk .., of one token; of V
@@ -820,6 +859,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
 
         f16x8 q[NQ][NI];
         bf16x8 ql[NQ][NL];   // lane (n, kg): the terms of the sum of q over group kg (+ 4)
+        float kappa[NQ];
         int rbeg[NQ], rend[NQ];
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
@@ -829,33 +869,13 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
             rbeg[u] = a.window ? max(0, rend[u] - a.window) : 0;
             const _Float16* src = a.q + (int64_t)(ok ? row : 0) * a.q_stride + (int64_t)(head * R + idx % R) * D + kg * 8;
             float qsum[NG];
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                qsum[g] = 0.0f;
-#pragma unroll
-            for (int i8 = 0; i8 < NI; ++i8) {
-                f16x8 x = {};
-                if (ok)
-                    x = *reinterpret_cast<const f16x8*>(src + 32 * i8);
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sum += (float)x[e];
-                    x[e] *= (_Float16)(e & 2 ? sign * 0.0625f : sign);
-                }
-                q[u][i8] = x;
-                qsum[i8 / (G / 32)] += sum;
-            }
+            kappa[u] = to_base2(a.scale, q_column<D, G>(src, ok, sign, q[u], qsum));
 #pragma unroll
             for (int y = 0; y < NL; ++y) {
                 float own = 0.0f;
 #pragma unroll
-                for (int g = 4 * y; g < NG && g < 4 * y + 4; ++g) {
-                    qsum[g] += __shfl_xor(qsum[g], 16, WAVE);
-                    qsum[g] += __shfl_xor(qsum[g], 32, WAVE);
+                for (int g = 4 * y; g < NG && g < 4 * y + 4; ++g)
                     own = kg == g - 4 * y ? qsum[g] : own;
-                }
-                own *= sign * 5.9604644775390625e-08f;   // 2^-24
                 const float q1 = bf16_part(own), q2 = bf16_part(own - q1), q3 = own - q1 - q2;
                 ql[u][y] = bf16_terms(q1, q2, q3, q1, q2, q3);
             }
@@ -1015,7 +1035,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         top = fmaxf(top, s[u][x][r]);
-                top *= kappa;
+                top *= kappa[u];
                 if (__any(top > m[u] + M_SLACK)) {
                     top = fmaxf(top, __shfl_xor(top, 16, WAVE));
                     top = fmaxf(top, __shfl_xor(top, 32, WAVE));
@@ -1033,7 +1053,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
                     float w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        w[e] = __builtin_amdgcn_exp2f(fmaf(s[u][2 * y + e / 4][e % 4], kappa, shift));
+                        w[e] = __builtin_amdgcn_exp2f(fmaf(s[u][2 * y + e / 4][e % 4], kappa[u], shift));
                     l[u] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
                     two_terms(w, p[u][y], pl[u][y]);
                 }
