@@ -361,7 +361,8 @@ __device__ inline int q_column(const _Float16* src, bool ok, float sign, f16x8 (
 }
 
 // What a score's sums are multiplied by for the softmax in base 2: the codes' 2^-24 and q's 2^e
-// taken out. Not 0, so that a masked score stays the smallest.
+// taken out. Not 0, so that a hidden score, -inf, keeps its weight of 0 with a scale of 0 too (what
+// the bound makes of a smaller scale is still below 2^-50).
 __device__ inline float to_base2(float scale, int e) {
     return fmaxf(ldexpf(fabsf(scale) * 1.44269504088896f, 24 - e), 1e-30f);
 }
@@ -531,7 +532,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
                 }
             }
             if (edge) {
-                // a score far below all others: its weight is exactly 0
+                // a score below all others at every scale: its weight is exactly 0
                 int tb = t0;
                 asm volatile("" : "+s"(tb));   // a branch, not selects in every step
 #pragma unroll
@@ -541,7 +542,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int j = tb + kg * 8 + 4 * h + r;
-                            s[u][h][r] = j >= rbeg[u] && j < rend[u] ? s[u][h][r] : -3.0e38f;
+                            s[u][h][r] = j >= rbeg[u] && j < rend[u] ? s[u][h][r] : -INFINITY;
                         }
             }
             f16x8 p[NQ], pl[NQ];
@@ -1024,7 +1025,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int at = tb + (x >> 1) * 32 + kg * 8 + (x & 1) * 4 + r;
-                            s[u][x][r] = at >= rbeg[u] && at < rend[u] ? s[u][x][r] : -3.0e38f;
+                            s[u][x][r] = at >= rbeg[u] && at < rend[u] ? s[u][x][r] : -INFINITY;
                         }
             }
 #pragma unroll
