@@ -437,8 +437,8 @@ ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, i
  * as kv4_append writes them (finite), and reach only the rows that see them, however large.
  * Products in fp16 on the matrix cores with fp32 sums, softmax statistics in fp32. V enters as
  * fp16 values, each rounded once; rows beside a value past fp16's 65504 (a pair stands for up to
- * 1048064) take 1/16 of all their values, rounded to multiples of 2^-20 at least. An output past
- * fp16 is infinite.
+ * 1048064), or with scores past 2^22, take 1/16 of all their values, rounded to multiples of 2^-20 at
+ * least. An output past fp16 is infinite.
  *
  * q       [rows][q_heads][D] fp16, row r at q + r * q_stride elements; 16-byte aligned,
  *         q_stride a multiple of 8 and at least q_heads * D

@@ -42,7 +42,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int AT = 256, AW = AT / WAVE;   // threads and waves of a decode workgroup
 constexpr int TB = 32;                    // tokens of a step
-constexpr float M_NONE = -1e30f;          // running maximum before the first score
+constexpr float M_NONE = -3.402823466e38f;   // running maximum before the first score, fp32's least
 constexpr float P_SHIFT = 6.0f;           // weights are 2^(score - max + P_SHIFT)
 constexpr float M_SLACK = 8.0f;           // and may exceed 2^P_SHIFT by 2^M_SLACK before a rescale
 
@@ -362,36 +362,58 @@ __device__ inline int q_column(const _Float16* src, bool ok, float sign, f16x8 (
 
 // What a score's sums are multiplied by for the softmax in base 2: the codes' 2^-24 and q's 2^e
 // taken out. Not 0, so that a hidden score, -inf, keeps its weight of 0 with a scale of 0 too (what
-// the bound makes of a smaller scale is still below 2^-50).
+// the bound makes of a smaller scale is still below 2^-50), and not so large that a product (a sum
+// is below 2^20) passes fp32: at 1e30, sums that differ in fp32 are far enough apart for a weight of 0.
 __device__ inline float to_base2(float scale, int e) {
-    return fmaxf(ldexpf(fabsf(scale) * 1.44269504088896f, 24 - e), 1e-30f);
+    return __builtin_amdgcn_fmed3f(ldexpf(fabsf(scale) * 1.44269504088896f, 24 - e), 1e-30f, 1e30f);
+}
+
+// A weight, 2^(s kappa - m + P_SHIFT), `shift` the last two. Past 2^22 or so a maximum m is rounded by
+// enough that the exact product lies far above it or below: all weights of a row pass fp16, or
+// vanish. With CARE the product is rounded as the maximum is.
+template <bool CARE>
+__device__ inline float weight(float s, float kappa, float m, float shift) {
+    if constexpr (CARE) {
+#pragma clang fp contract(off)
+        const float product = s * kappa;
+        return __builtin_amdgcn_exp2f(fminf(product - m, M_SLACK) + P_SHIFT);
+    } else {
+        return __builtin_amdgcn_exp2f(fmaf(s, kappa, shift));
+    }
 }
 
 // V's operand for nibble JJ of chunk words w: one d of 8 tokens, scale * code + low in fp16. A stored
 // pair goes up to 15 * 65504 + 65504, past fp16 (fp32 rows that large, and pairs of rows near 65504
 // whose rounding passes it by up to 32), and an infinite value times another row's weight of 0 is
-// NaN. Operands are therefore taken as they are at first. Only if that leaves a sum that is not
-// finite (an infinite operand always does), the rows are done again with WIDE: 1 / 16 of every
-// value, which holds all that a pair can stand for, low / 16 and the value rounded to multiples of
-// 2^-24 at least.
-template <int JJ, bool WIDE>
+// NaN. Operands are taken as they are at first; CARE makes them 1 / 16 of every value, which holds
+// all that a pair can stand for, low / 16 and the value rounded to multiples of 2^-24 at least.
+//
+// Steps without CARE leave a sum that is not finite wherever a value or a weight passed fp16, and a
+// sum of weights below 2^P_SHIFT where they vanished (the largest is 2^P_SHIFT and more). Such rows
+// are gone through again with CARE, and no others pay for it.
+template <int JJ, bool CARE>
 __device__ inline f16x8 v_values(u32x4 w, u32x4 s, u32x4 l, const Masks& mk) {
     const f16x2 part = {(_Float16)0.0625f, (_Float16)0.0625f};
     u32x4 r;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         f16x2 c = codes_int<JJ>(w[p], mk), low = as_f16x2(l[p]);
-        if constexpr (WIDE)
+        if constexpr (CARE)
             c *= part, low *= part;
         r[p] = as_u32(__builtin_elementwise_fma(c, as_f16x2(s[p]), low));
     }
     return __builtin_bit_cast(f16x8, r);
 }
-constexpr float WIDE_UNIT = 16.0f;
+constexpr float CARE_UNIT = 16.0f;
 
-// Whether a sum of the wave is infinite or NaN.
+// Whether a column's sums of values are infinite or NaN, or its weights' sum is not what a row that
+// has a maximum must have. `sum` is the column's, the same in its lanes.
 template <int N, int M>
-__device__ inline bool any_not_finite(const f32x4 (&o)[N][M]) {
+__device__ inline bool needs_care(const f32x4 (&o)[N][M], const float (&sum)[N], const float (&m)[N]) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        bad |= m[i] != M_NONE && !(sum[i] > 32.0f);   // half of 2^P_SHIFT, past all roundings
     float z[4] = {};   // four chains
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -400,7 +422,7 @@ __device__ inline bool any_not_finite(const f32x4 (&o)[N][M]) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 z[r] = fmaf(o[i][j][r], 0.0f, z[r]);
-    return __any((z[0] + z[1]) + (z[2] + z[3]) != 0.0f);
+    return __any(bad || (z[0] + z[1]) + (z[2] + z[3]) != 0.0f);
 }
 
 __device__ inline float half_of(u32x4 w, int i) { return (float)as_f16x2(w[i / 2])[i & 1]; }
@@ -499,8 +521,8 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         const _Float16 one = (_Float16)1.0f;
         const f16x8 ones = {one, one, one, one, one, one, one, one};
 
-        auto step = [&](uint32_t at, auto wide) {
-            constexpr bool WIDE = decltype(wide)::value;
+        auto step = [&](uint32_t at, auto care) {
+            constexpr bool CARE = decltype(care)::value;
             const bool edge = t0 < t.all_begin || t0 + TB > t.all_end;   // some row does not see all of it
             f32x4 s[NQ][2];
             uint32_t kw[2][NI];
@@ -570,10 +592,8 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
                 const float shift = m[u] > M_NONE ? P_SHIFT - m[u] : 0.0f;
                 float w[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        w[4 * h + r] = __builtin_amdgcn_exp2f(fmaf(s[u][h][r], kappa[u], shift));
+                for (int e = 0; e < 8; ++e)
+                    w[e] = weight<CARE>(s[u][e / 4][e % 4], kappa[u], m[u], shift);
                 two_terms(w, p[u], pl[u]);
                 l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[u], l[u], 0, 0, 0);
                 l[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[u], l[u], 0, 0, 0);
@@ -602,8 +622,8 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             for (int ch = 0; ch < NC; ++ch) {
                 const int g0 = 64 * ch / G, g1 = (64 * ch + 32) / G;
                 const f16x8 vv[4] = {
-                    v_values<0, WIDE>(vw[ch], vs[g0], vl[g0], mk), v_values<1, WIDE>(vw[ch], vs[g0], vl[g0], mk),
-                    v_values<2, WIDE>(vw[ch], vs[g1], vl[g1], mk), v_values<3, WIDE>(vw[ch], vs[g1], vl[g1], mk)};
+                    v_values<0, CARE>(vw[ch], vs[g0], vl[g0], mk), v_values<1, CARE>(vw[ch], vs[g0], vl[g0], mk),
+                    v_values<2, CARE>(vw[ch], vs[g1], vl[g1], mk), v_values<3, CARE>(vw[ch], vs[g1], vl[g1], mk)};
                 // the second terms after all first ones: a product that waits for the one before
                 // it on the same sum would stall
                 auto add = [&](const f16x8(&w)[NQ]) {
@@ -618,7 +638,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             }
         };
 
-        auto walk = [&](auto wide) {
+        auto walk = [&](auto care) {
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
 #pragma unroll
@@ -634,7 +654,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
                 else
                     __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
                 __builtin_amdgcn_sched_barrier(0);
-                step(at, wide);
+                step(at, care);
                 __builtin_amdgcn_sched_barrier(0);
                 if (t0 + SLOTS * AW * TB < to)
                     ring.copy(slots + at, t0 + SLOTS * AW * TB, pa, pb);
@@ -643,11 +663,14 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             }
         };
         walk(std::false_type{});
-        float unit = 1.0f;   // of the wave's sums
-        if (any_not_finite(o)) {
+        float unit = 1.0f, sums[NQ];   // unit: of the wave's sums of values
+#pragma unroll
+        for (int u = 0; u < NQ; ++u)
+            sums[u] = l[u][0];
+        if (needs_care(o, sums, m)) {
             begin();   // the last copies have landed and been read
             walk(std::true_type{});
-            unit = WIDE_UNIT;
+            unit = CARE_UNIT;
         }
 
         // join the waves: each brings its O to the largest maximum
@@ -832,7 +855,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
     __shared__ __attribute__((aligned(16))) f16x8 kt[3][D / 8][PB], vt[4][PB / 8][D];
     __shared__ __attribute__((aligned(16))) u32x4 lowt[3][NG][PB];   // low's terms
     __shared__ __attribute__((aligned(16))) _Float16 sct[3][NG][PB];
-    __shared__ int again;   // some wave's sums are not finite
+    __shared__ int again;   // some wave's columns need care
     const int R = a.q_heads / c.heads, P = 1 << c.page_log2;
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), n = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -921,8 +944,8 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
                 vl = *reinterpret_cast<const u32x4*>(pv + (L::v_low(P, g) + 2 * vslot));
             }
         };
-        auto put = [&](int i, int kb, int vb, auto wide) {
-            constexpr bool WIDE = decltype(wide)::value;
+        auto put = [&](int i, int kb, int vb, auto care) {
+            constexpr bool CARE = decltype(care)::value;
             const int t0 = from + i * PB;
             if (mine) {
 #pragma unroll
@@ -953,8 +976,8 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
                 for (int x = 0; x < 4; ++x)
                     w[x] >>= 8 * half;
                 f16x8* to = &vt[vb][t8][quad / 16 * 64 + half * 32 + quad % 16 * 2];
-                to[0] = v_values<0, WIDE>(w, vs, vl, mk);
-                to[1] = v_values<1, WIDE>(w, vs, vl, mk);
+                to[0] = v_values<0, CARE>(w, vs, vl, mk);
+                to[1] = v_values<1, CARE>(w, vs, vl, mk);
             }
         };
         // The operands of the next rows of products are read while the present ones run; the
@@ -1013,7 +1036,8 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
             }
             __builtin_amdgcn_sched_barrier(0);
         };
-        auto softmax = [&](f32x4(&s)[NQ][XT], int i) {
+        auto softmax = [&](f32x4(&s)[NQ][XT], int i, auto care) {
+            constexpr bool CARE = decltype(care)::value;
             const int t0 = from + i * PB;
             if (t0 < w_all_begin || t0 + PB > w_all_end) {
                 int tb = t0;
@@ -1054,7 +1078,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
                     float w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        w[e] = __builtin_amdgcn_exp2f(fmaf(s[u][2 * y + e / 4][e % 4], kappa[u], shift));
+                        w[e] = weight<CARE>(s[u][2 * y + e / 4][e % 4], kappa[u], m[u], shift);
                     l[u] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
                     two_terms(w, p[u][y], pl[u][y]);
                 }
@@ -1104,7 +1128,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        auto walk = [&](auto wide) {
+        auto walk = [&](auto care) {
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
 #pragma unroll
@@ -1116,10 +1140,10 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
             if (nb == 0)
                 return;
             load(0);
-            put(0, 0, 0, wide);
+            put(0, 0, 0, care);
             if (nb > 1) {
                 load(1);
-                put(1, 1, 1, wide);
+                put(1, 1, 1, care);
             }
             if (nb > 2)
                 load(2);
@@ -1136,9 +1160,9 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
                 scores(s, kb);
                 __builtin_amdgcn_s_setprio(0);
                 phase_end();
-                softmax(s, i);
+                softmax(s, i, care);
                 if (i + 2 < nb) {
-                    put(i + 2, kb == 0 ? 2 : kb - 1, (i + 2) & 3, wide);
+                    put(i + 2, kb == 0 ? 2 : kb - 1, (i + 2) & 3, care);
                     if (i + 3 < nb)
                         load(i + 3);
                 }
@@ -1152,17 +1176,23 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
         __syncthreads();   // the last tile's blocks have been read, and its `again`
         if (tid == 0)
             again = 0;
-        float unit = 1.0f;   // of the sums
+        float unit = 1.0f;   // of the sums of values
         walk(std::false_type{});
         if (nb > 0) {
             // the operands are shared, so all waves go again (a barrier at least lies between the
             // walk's start and its end)
-            if (any_not_finite(o) && lane == 0)
+            float sums[NQ];
+#pragma unroll
+            for (int u = 0; u < NQ; ++u) {
+                sums[u] = l[u] + __shfl_xor(l[u], 16, WAVE);
+                sums[u] += __shfl_xor(sums[u], 32, WAVE);
+            }
+            if (needs_care(o, sums, m) && lane == 0)
                 again = 1;
             __syncthreads();
             if (__builtin_amdgcn_readfirstlane(again)) {
                 walk(std::true_type{});
-                unit = WIDE_UNIT;
+                unit = CARE_UNIT;
             }
         }
 
