@@ -72,20 +72,22 @@ __device__ inline RowTile row_tile(const Kv4Batch& b, const Kv4Cache& c, int seq
     t.all_end = max(0, t.first + i0 + 1);
     const int seen = max(i0, -t.first);   // the first row with a position
     t.begin = window ? max(0, t.first + seen + 1 - window) : 0;
-    t.all_begin = window ? max(0, t.first + i1 + 1 - window) : 0;
+    t.all_begin = window ? max(0, t.end - window) : 0;
     return t;
 }
 
 // Tokens of one split: the launch's stretch, or more where the splits would not reach the end.
-__device__ inline int split_tokens(const RowTile& t, int stretch, int nsplit) {
+// Positions are below 2^31; sums of them and of stretches are unsigned, below 2^32.
+__device__ inline uint32_t split_tokens(const RowTile& t, uint32_t stretch, int nsplit) {
     const int base = t.begin & ~(TB - 1);
-    const int need = (t.end - base + nsplit - 1) / nsplit;
-    return max(stretch, (need + TB * AW - 1) & ~(TB * AW - 1));
+    const uint32_t need = ((uint32_t)(t.end - base) + nsplit - 1) / nsplit;
+    return max(stretch, (need + TB * AW - 1) & ~(uint32_t)(TB * AW - 1));
 }
 
 struct Split {
-    int n, stretch;   // splits, and tokens of each at the launch's max_len
-    int tiles;        // row tiles a sequence and kv head at the launch's max_q
+    int n;              // splits
+    uint32_t stretch;   // tokens of each at the launch's max_len
+    int tiles;          // row tiles a sequence and kv head at the launch's max_q
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -458,14 +460,14 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         const RowTile t = row_tile(b, c, seq, tile, PER, R, a.window);
         if (tile * PER >= t.rows * R)
             return;
-        const int base = t.begin & ~(TB - 1);
-        const int stretch = split_tokens(t, sp.stretch, sp.n);
-        const int from = base + split * stretch, to = min(from + stretch, t.end);
+        const uint32_t end = t.end, stretch = split_tokens(t, sp.stretch, sp.n);
+        const uint32_t from = (uint32_t)(t.begin & ~(TB - 1)) + split * stretch;
+        const uint32_t to = from < end ? from + min(stretch, end - from) : from;
         // a split's maximum and sum for one (row, head), behind all splits' sums of values
         auto split_stats = [&](int64_t at) {
             return a.ws + ((int64_t)sp.n * a.rows * a.q_heads * D + (at * sp.n + split) * 2);
         };
-        if (split > 0 && from >= t.end) {
+        if (split > 0 && from >= end) {
             // no tokens: a sum of 0, whose values nobody reads
             for (int idx = tile * PER + threadIdx.x; idx < min(tile * PER + PER, t.rows * R); idx += AT) {
                 const int row = b.starts[seq] + idx / R;
@@ -481,9 +483,9 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         uint8_t* slots = lds + wave * (SLOTS * RG::BYTES);
         const uint32_t k_at = lds_addr(slots) + RG::k_at(), v_at = lds_addr(slots) + RG::v_at(),
                        p_at = lds_addr(slots) + RG::p_at();
-        int t0;                    // the block in use
+        uint32_t t0;               // the block in use
         uint32_t pa = 0, pb = 0;   // pages of the block to be copied next
-        auto pages = [&](int pos) {
+        auto pages = [&](uint32_t pos) {
             if (pos < to) {
                 pa = ring.page_of(pos);
                 pb = BIG ? pa : ring.page_of(pos + 16);
@@ -523,7 +525,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 
         auto step = [&](uint32_t at, auto care) {
             constexpr bool CARE = decltype(care)::value;
-            const bool edge = t0 < t.all_begin || t0 + TB > t.all_end;   // some row does not see all of it
+            const bool edge = t0 < (uint32_t)t.all_begin || t0 + TB > (uint32_t)t.all_end;   // some row does not see all of it
             f32x4 s[NQ][2];
             uint32_t kw[2][NI];
             u32x4 sc[NG], low[NG];
@@ -601,7 +603,7 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             u32x4 vs[NG], vl[NG], vw[NC];
             RG::v_words(vw, v_at + at);
             RG::template params<1>(vs, vl, p_at + at);
-            if (edge && (t0 < t.begin || t0 + TB > t.end)) {
+            if (edge && (t0 < (uint32_t)t.begin || t0 + TB > end)) {
                 // what lies at positions that no row sees may be anything: a weight of 0 must
                 // not meet an infinite or NaN value
                 int tb = t0;
@@ -879,7 +881,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
         const RowTile t = row_tile(b, c, seq, tile, PER, R, a.window);
         if (tile * PER >= t.rows * R)
             return;
-        const int from = t.begin & ~(PB - 1), nb = t.end > from ? (t.end - from + PB - 1) / PB : 0;
+        const int from = t.begin & ~(PB - 1), nb = ((uint32_t)(t.end - from) + PB - 1) / PB;
 
         f16x8 q[NQ][NI];
         bf16x8 ql[NQ][NL];   // lane (n, kg): the terms of the sum of q over group kg (+ 4)
@@ -907,7 +909,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
         // positions that all of the wave's rows see
         const int w0 = tile * PER + wave * 16 * NQ, wl = min(w0 + 16 * NQ - 1, t.rows * R - 1);
         const int w_all_end = max(0, t.first + w0 / R + 1);
-        const int w_all_begin = a.window ? max(0, t.first + wl / R + 1 - a.window) : 0;
+        const int w_all_begin = a.window ? max(0, max(0, t.first + wl / R + 1) - a.window) : 0;
 
         f32x4 o[NQ][D / 16];
         f16x8 p[NQ][XT / 2], pl[NQ][XT / 2];
@@ -958,7 +960,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
                         lowt[kb][g][place] = __builtin_bit_cast(u32x4, bf16_terms(l1, l1, l1, l2, l2, l2));
                     }
                 }
-                if (t0 < t.begin || t0 + PB > t.end) {
+                if (t0 < t.begin || (uint32_t)t0 + PB > (uint32_t)t.end) {
                     // what lies at positions that no row sees may be anything
                     int tb = t0 + 8 * t8;
                     asm volatile("" : "+v"(tb));   // a branch, not selects in every block
@@ -1039,7 +1041,7 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
         auto softmax = [&](f32x4(&s)[NQ][XT], int i, auto care) {
             constexpr bool CARE = decltype(care)::value;
             const int t0 = from + i * PB;
-            if (t0 < w_all_begin || t0 + PB > w_all_end) {
+            if (t0 < w_all_begin || (uint32_t)t0 + PB > (uint32_t)w_all_end) {
                 int tb = t0;
                 asm volatile("" : "+s"(tb));
 #pragma unroll
@@ -1268,7 +1270,7 @@ Split plan(int q_heads, int kv_heads, int D, int batch, int max_q, int max_len, 
     want = want < MAX_SPLITS ? want : MAX_SPLITS;
     int64_t stretch = max_len <= 5 * unit ? max_len : (max_len + want - 1) / want;
     stretch = stretch < 2 * unit ? 2 * unit : (stretch + unit - 1) / unit * unit;
-    s.stretch = (int)stretch;
+    s.stretch = (uint32_t)stretch;
     s.n = (int)((max_len + stretch - 1) / stretch);
     return s;
 }
