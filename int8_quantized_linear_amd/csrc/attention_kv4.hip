@@ -65,7 +65,8 @@ struct RowTile {
 __device__ inline RowTile row_tile(const Kv4Batch& b, const Kv4Cache& c, int seq, int tile, int per, int R, int window) {
     RowTile t;
     const int len = kv4_len(b, c, seq);
-    t.rows = min(b.starts[seq + 1] - b.starts[seq], b.rows);
+    const int64_t rows = (int64_t)b.starts[seq + 1] - b.starts[seq];   // whatever the starts are
+    t.rows = rows < 0 ? 0 : rows > b.rows ? b.rows : (int)rows;
     t.first = len - t.rows;
     const int i0 = tile * per / R, i1 = min((tile * per + per - 1) / R, t.rows - 1);
     t.end = max(0, t.first + i1 + 1);
@@ -75,6 +76,10 @@ __device__ inline RowTile row_tile(const Kv4Batch& b, const Kv4Cache& c, int seq
     t.all_begin = window ? max(0, t.end - window) : 0;
     return t;
 }
+
+// Row i of a sequence in the call's rows, or a number outside them (unsigned: also below 0) where
+// the caller's starts lead there.
+__device__ inline uint32_t row_of(const Kv4Batch& b, int seq, int i) { return (uint32_t)b.starts[seq] + (uint32_t)i; }
 
 // Tokens of one split: the launch's stretch, or more where the splits would not reach the end.
 // Positions are below 2^31; sums of them and of stretches are unsigned, below 2^32.
@@ -470,8 +475,8 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         if (split > 0 && from >= end) {
             // no tokens: a sum of 0, whose values nobody reads
             for (int idx = tile * PER + threadIdx.x; idx < min(tile * PER + PER, t.rows * R); idx += AT) {
-                const int row = b.starts[seq] + idx / R;
-                if (row < a.rows) {
+                const uint32_t row = row_of(b, seq, idx / R);
+                if (row < (uint32_t)a.rows) {
                     float* st = split_stats((int64_t)row * a.q_heads + head * R + idx % R);
                     st[0] = M_NONE, st[1] = 0.0f;
                 }
@@ -510,8 +515,9 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
         int rbeg[NQ], rend[NQ];
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
-            const int idx = tile * PER + u * 16 + n, i = idx / R, row = b.starts[seq] + i;
-            const bool ok = i < t.rows && row < a.rows;
+            const int idx = tile * PER + u * 16 + n, i = idx / R;
+            const uint32_t row = row_of(b, seq, i);
+            const bool ok = i < t.rows && row < (uint32_t)a.rows;
             rend[u] = ok ? max(0, t.first + i + 1) : 0;
             rbeg[u] = a.window ? max(0, rend[u] - a.window) : 0;
             const _Float16* src = a.q + (int64_t)(ok ? row : 0) * a.q_stride + (int64_t)(head * R + idx % R) * D + kg * 8;
@@ -699,8 +705,9 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
             __syncthreads();
             constexpr int E = D / 16;   // values of one thread: row tid / 16, E neighbouring d
             const int rr = threadIdx.x / 16, d0 = (threadIdx.x % 16) * E;
-            const int idx = tile * PER + u * 16 + rr, i = idx / R, row = b.starts[seq] + i;
-            if (i < t.rows && row < a.rows) {
+            const int idx = tile * PER + u * 16 + rr, i = idx / R;
+            const uint32_t row = row_of(b, seq, i);
+            if (i < t.rows && row < (uint32_t)a.rows) {
                 float mx = stats[0][rr][0], sum = 0.0f, v[E];
 #pragma unroll
                 for (int w = 1; w < AW; ++w)
@@ -889,8 +896,9 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
         int rbeg[NQ], rend[NQ];
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
-            const int idx = tile * PER + (wave * NQ + u) * 16 + n, i = idx / R, row = b.starts[seq] + i;
-            const bool ok = i < t.rows && row < a.rows;
+            const int idx = tile * PER + (wave * NQ + u) * 16 + n, i = idx / R;
+            const uint32_t row = row_of(b, seq, i);
+            const bool ok = i < t.rows && row < (uint32_t)a.rows;
             rend[u] = ok ? max(0, t.first + i + 1) : 0;
             rbeg[u] = a.window ? max(0, rend[u] - a.window) : 0;
             const _Float16* src = a.q + (int64_t)(ok ? row : 0) * a.q_stride + (int64_t)(head * R + idx % R) * D + kg * 8;
@@ -1200,10 +1208,11 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
 
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
-            const int idx = tile * PER + (wave * NQ + u) * 16 + n, i = idx / R, row = b.starts[seq] + i;
+            const int idx = tile * PER + (wave * NQ + u) * 16 + n, i = idx / R;
+            const uint32_t row = row_of(b, seq, i);
             float sum = l[u] + __shfl_xor(l[u], 16, WAVE);
             sum += __shfl_xor(sum, 32, WAVE);
-            if (i < t.rows && row < a.rows) {
+            if (i < t.rows && row < (uint32_t)a.rows) {
                 const float inv = sum > 0.0f ? unit / sum : 0.0f;
                 _Float16* to = a.out + ((int64_t)row * a.q_heads + head * R + idx % R) * D;
                 // o's tile x, register r: d = 16 x + 4 kg + r
