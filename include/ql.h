@@ -386,6 +386,7 @@ ql_status rms_norm_quantize_e4m3(const void* x, ql_dtype x_dtype, const void* re
  * scale and an fp16 low for each token, head and group of `group` values along the head's D:
  *   low = fp16(min x),  scale = max(fp16((max x - low) / 15), 2^-24)     (fp16 saturates)
  *   code = clamp(round_half_even((x - low) / scale), 0, 15),  x ~ scale * code + low
+ * Infinite values saturate the same way; a NaN is not kept (a finite value is stored for it).
  * (The order of the bytes in a page is stated in csrc/kv4.h.)
  *
  * The three calls below share these arguments:

@@ -37,6 +37,11 @@ struct Eight {
     }
 };
 
+// +inf as fp32's largest number, whose scale and code saturate as the definition has it (the
+// refined quotients below make NaN of infinite ones).
+constexpr float FINITE = 3.402823466e38f;
+__device__ inline float to_finite(float v) { return v > FINITE ? FINITE : v; }
+
 // fp16 of a float, kept within fp16's finite range.
 __device__ inline _Float16 to_f16_sat(float v) {
     return (_Float16)__builtin_amdgcn_fmed3f(v, -65504.0f, 65504.0f);
@@ -181,6 +186,13 @@ __global__ __launch_bounds__(KT) void kv4_append_kernel(const void* __restrict__
                         hi = fmaxf(hi, x[e]);
                     }
                     group_range<G / 8>(lo, hi);
+                    if (__any(hi > FINITE)) {
+                        hi = to_finite(hi);
+                        lo = to_finite(lo);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = to_finite(x[e]);
+                    }
                     const _Float16 lo16 = to_f16_sat(lo);
                     const float lf = (float)lo16;
                     const _Float16 least = (_Float16)5.9604644775390625e-08f;   // 2^-24
