@@ -363,8 +363,8 @@ ql_status quantize_weight_int4_grouped(const float* w, int64_t K, int64_t N, int
  *          looked at)
  * gamma    [K] fp32, 16-byte aligned
  * eps      finite and > 0, else QL_ERR_SHAPE
- * res_out  [M,K] of res_dtype: h rounded to it (out); it may be the residual itself. NULL with
- *          a NULL residual, else required
+ * res_out  [M,K] of res_dtype: h rounded to it (out); it may be the residual itself, or x itself
+ *          if that has the same type. NULL with a NULL residual, else required
  * xq       [M,K] int8 row-major (out);  x_scale [M] fp32 (out)
  * Requires K > 0 and K % 16 == 0.
  */

@@ -252,7 +252,8 @@ def rms_norm_quantize_int8(x, gamma, residual=None, eps: float = 1e-6, res_out=N
     """Root-mean-square norm of residual + x as int8 codes per row: x [M, K] (fp16 or fp32), gamma
     fp32 [K], residual [M, K] (fp16 or fp32) or None. Returns (xq int8 [M, K], x_scale fp32 [M])
     with x_scale * xq ~ h / sqrt(mean(h^2) + eps) * gamma, and with a residual also h = residual +
-    x in the residual's dtype, written to res_out (which may be the residual) or a new tensor."""
+    x in the residual's dtype, written to res_out (which may be the residual, or x if that has its
+    dtype) or a new tensor."""
     return _rms_norm(x, gamma, residual, eps, res_out, "rms_norm_quantize_int8", torch.int8)
 
 

@@ -59,10 +59,11 @@ enum { R_NONE = 0, R_F16 = 1, R_F32 = 2 };
 // 1024 take 14.7 us with NC = 1 and 22.3 with 8, 2048 of 4096 15.2 with 2 and 15.6 with 8. (4 for
 // rows up to 8192 lost: 2048 of 8192 29.5, with 8 27.0. So did loading all chunks before the first
 // store, which doubles the registers: 2048 of 16384 52.5, chunk by chunk 47.5.) NC == 0: longer rows
-// are read twice (the statistics, then h and the codes; h is written in the second pass only, so
-// that res_out may be the residual itself): 2048 rows of 16384 take 64 us so.
+// are read twice (the statistics, then h and the codes): 2048 rows of 16384 take 64 us so. A chunk of h
+// is written by the thread that has read it, and in the second pass only, so that res_out may be
+// the residual or x itself.
 template <bool XF16, int RES, bool E4M3, int NC>
-__global__ __launch_bounds__(NT) void rms_norm_quant_kernel(const void* __restrict__ x, const void* residual,
+__global__ __launch_bounds__(NT) void rms_norm_quant_kernel(const void* x, const void* residual,
                                                             const float* __restrict__ gamma, float eps, int64_t K,
                                                             void* res_out, int8_t* __restrict__ q,
                                                             float* __restrict__ scale) {
