@@ -1295,6 +1295,12 @@ int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, 
     return s.n == 1 ? 0 : s.n * rows * q_heads * (D + 2);
 }
 
+extern "C" int ql_attention_kv4_kernel(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
+                                       int window) {
+    max_q = (int)std::min<int64_t>(max_q, std::max<int64_t>(rows, 1));
+    return prompt_blocks((int64_t)max_q * (q_heads / kv_heads), (int64_t)batch * kv_heads, D, max_q, max_len, window);
+}
+
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream) {
     const int max_q = std::min(a.max_q, a.rows);

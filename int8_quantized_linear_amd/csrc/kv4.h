@@ -125,6 +125,10 @@ struct Kv4Attn {
 // Floats of workspace that launch_attention_kv4 uses for these sizes.
 int64_t attention_kv4_workspace(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
                                 int window);
+// Kernel of launch_attention_kv4 for these sizes: 0 decode, 1 or 2 prompt with as many blocks of 16
+// (row, head) pairs a wave. For tests; not part of the interface.
+extern "C" int ql_attention_kv4_kernel(int64_t rows, int q_heads, int kv_heads, int D, int batch, int max_q, int max_len,
+                                       int window);
 ql_status launch_attention_kv4(const Kv4Attn& a, const Kv4Cache& c, int D, int G, const Kv4Batch& b,
                                hipStream_t stream);
 

@@ -30,7 +30,7 @@ def test_prompt(ql, H, D, G, scale):  # noqa: F811
 def test_scores_of_one_sign(ql, rows, H, scale):  # noqa: F811
     """Scores around 10 to 20 times the scale, all positive or all negative (q along K's mean direction): the largest has
     all the weight wherever the next one is further away than fp32's roundings of it."""
-    P, D, G, n = 16, 64, 32, 90
+    P, D, G, n, R = 16, 64, 32, 300, 4
     rng = np.random.default_rng(7)
     b = ref.Batch(rng, [n], [rows], P)
     cache = _cache(rng, b, H, D, G)
@@ -39,17 +39,17 @@ def test_scores_of_one_sign(ql, rows, H, scale):  # noqa: F811
     par[..., 1, :] += np.float16(8)              # K around 8
     cache[:, :, P * D // 2:P * D // 2 + 4 * n_par] = par.reshape(b.pages, H, -1).view(np.uint8)
     k, v = ref.read_rows(cache, b.table[0], P, D, G, n)
-    q = np.abs(rng.standard_normal((rows, H, D))).astype(np.float16)
+    q = np.abs(rng.standard_normal((rows, H * R, D))).astype(np.float16)
     got = host(ql.attention_kv4(dev(q), dev(cache), *(dev(a) for a in b.arrays()), page_size=P, group=G, scale=scale))
     assert np.isfinite(got).all()
     sure = 0
     for i in range(0, rows, max(1, rows // 4)):
-        for h in range(min(H, 3)):
-            s = k[:n - rows + i + 1, h] @ q[i, h].astype(np.float64) * scale
+        for h in range(min(H * R, 6)):
+            s = k[:n - rows + i + 1, h // R] @ q[i, h].astype(np.float64) * scale
             assert np.all(s * scale > 0)
             first, second = np.sort(s)[::-1][:2]
             if first - second > 1e-4 * np.abs(s).max():
                 sure += 1
-                want = v[np.argmax(s), h]
+                want = v[np.argmax(s), h // R]
                 assert np.all(np.abs(got[i, h] - want) <= 2 * U * np.abs(want) + 2.0 ** -24)
     assert sure

@@ -97,7 +97,7 @@ def test_a_value_left_of_the_window(ql, kind):  # noqa: F811
 def test_a_later_rows_value_in_a_prompt(ql, D, G, kind):  # noqa: F811
     """The prompt kernel, in both of its shapes (D = 128 with 64 and 128 heads)."""
     for H in (64, 128) if D == 128 else (128,):
-        seen, hidden = _check(ql, H + G, [300, 64], [64, 64], 64, H, 2 if H == 128 else 4, D, G,
+        seen, hidden = _check(ql, H + G, [300, 64], [64, 64], 64, H, 4, D, G,
                               [(0, 270), (1, 40), (1, 63)], kind, samples=4, max_q=64, max_len=300)
         assert seen or hidden
 

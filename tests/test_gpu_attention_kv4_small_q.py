@@ -19,11 +19,11 @@ def test_decode(ql, D, G, gain):  # noqa: F811
 @pytest.mark.parametrize("gain", [1e-4, 1e-6])
 @pytest.mark.parametrize("D,G", DG)
 def test_prompt(ql, D, G, gain):  # noqa: F811
-    base._check(ql, D + G, [300, 64], [64, 64], 64, 128, 2, D, G, gain=gain, scale=2.0 / (gain * D ** 0.5),
+    base._check(ql, D + G, [300, 64], [64, 64], 64, 128, 4, D, G, gain=gain, scale=2.0 / (gain * D ** 0.5),
                 max_q=64, max_len=300, samples=3)
 
 
-@pytest.mark.parametrize("H", [2, 64])
+@pytest.mark.parametrize("H", [2, 64, 128])
 def test_sizes_beside_each_other(ql, H, monkeypatch):  # noqa: F811
     """Every (row, head) a size of its own, from subnormal to thousands, over scores of its own size."""
     draw = np.random.default_rng
@@ -44,4 +44,4 @@ def test_sizes_beside_each_other(ql, H, monkeypatch):  # noqa: F811
     monkeypatch.setattr(base.np.random, "default_rng", Rng)
     for scale in (1e-3, 1.0, 1e3):
         base._check(ql, 5, [200, 64], [64 if H > 2 else 4, 64 if H > 2 else 1], 32, H, 4, 128, 64, scale=scale,
-                    samples=4, max_q=64 if H > 2 else None, max_len=200 if H > 2 else None)
+                    samples=4, max_q=64 if H > 2 else None, max_len=300 if H > 2 else None)

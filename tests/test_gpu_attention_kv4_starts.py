@@ -16,10 +16,11 @@ STARTS = [[-3, 2, 6], [-5, -2, 6], [0, 9, 6], [4, 1, 6], [-BIG, BIG, 6], [BIG, -
           [7, 8, 9], [0, 6, -BIG], [BIG - 2, BIG, 6]]
 
 
-@pytest.mark.parametrize("H,max_q,lens", [(2, 6, [40, 30]), (2, 6, [3000, 2000]), (256, 64, [40, 300])])
+@pytest.mark.parametrize("H,rows,lens", [(2, 6, [40, 30]), (2, 6, [3000, 2000]), (256, 64, [90, 300])])
 @pytest.mark.parametrize("starts", STARTS)
-def test_nothing_outside(ql, H, max_q, lens, starts):  # noqa: F811
-    P, D, G, rows, R = 32, 64, 32, 6, 4
+def test_nothing_outside(ql, H, rows, lens, starts):  # noqa: F811
+    P, D, G, R = 32, 64, 32, 4
+    starts = [rows if s == 6 else s for s in starts]
     rng = np.random.default_rng(1)
     b = ref.Batch(rng, lens, [3, 3], P)
     q = Guarded((rows, H * R, D), torch.float16)
@@ -28,7 +29,7 @@ def test_nothing_outside(ql, H, max_q, lens, starts):  # noqa: F811
     cache = dev(_cache(rng, b, H, D, G))
     before = cache.clone()
     meta = [dev(b.table), dev(np.array(lens, np.int32)), dev(np.array(starts, np.int64).astype(np.int32))]
-    ql.attention_kv4(q.view, cache, *meta, page_size=P, group=G, out=out.view, max_q=max_q, max_len=max(lens))
+    ql.attention_kv4(q.view, cache, *meta, page_size=P, group=G, out=out.view, max_q=rows, max_len=max(lens))
     torch.cuda.synchronize()
     out.check()
     assert torch.equal(cache, before)
