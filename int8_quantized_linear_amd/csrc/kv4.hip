@@ -243,21 +243,6 @@ __global__ __launch_bounds__(KT) void kv4_append_kernel(const void* __restrict__
     }
 }
 
-template <bool F16>
-__device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
-    if constexpr (F16) {
-        f16x8 h;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            h[e] = (_Float16)v[e];
-        *reinterpret_cast<f16x8*>(reinterpret_cast<_Float16*>(p) + i) = h;
-    } else {
-        f32x4* f = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i);
-        f[0] = f32x4{v[0], v[1], v[2], v[3]};
-        f[1] = f32x4{v[4], v[5], v[6], v[7]};
-    }
-}
-
 // Values d .. of two chunks c and c + 1, held as halves (0, 32) of c in the even lanes and of c + 1
 // in the odd ones (4 lanes on): the even chunk's halves from both lanes, then the odd chunk's.
 __device__ inline void trade_store(_Float16* to, const float (&v)[2][8], bool odd) {

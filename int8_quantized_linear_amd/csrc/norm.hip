@@ -37,21 +37,6 @@ __device__ inline void load8(float (&v)[8], const void* p, int64_t i) {
     }
 }
 
-template <bool F16>
-__device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
-    if constexpr (F16) {
-        f16x8 h;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            h[j] = (_Float16)v[j];
-        *reinterpret_cast<f16x8*>(reinterpret_cast<_Float16*>(p) + i) = h;
-    } else {
-        f32x4* f = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i);
-        f[0] = f32x4{v[0], v[1], v[2], v[3]};
-        f[1] = f32x4{v[4], v[5], v[6], v[7]};
-    }
-}
-
 enum { R_NONE = 0, R_F16 = 1, R_F32 = 2 };
 
 // One workgroup per row of K = 8 * nch values. NC > 0: rows of up to NT * NC chunks of 8 stay in

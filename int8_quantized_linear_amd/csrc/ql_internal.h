@@ -34,6 +34,22 @@ __device__ inline int8_t requant_code(float y, float s, float r) {
     return (int8_t)__builtin_amdgcn_fmed3f(rintf(qt), -127.0f, 127.0f);
 }
 
+// 8 values to fp16 or fp32 memory, from element i.
+template <bool F16>
+__device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
+    if constexpr (F16) {
+        f16x8 h;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            h[j] = (_Float16)v[j];
+        *reinterpret_cast<f16x8*>(reinterpret_cast<_Float16*>(p) + i) = h;
+    } else {
+        f32x4* f = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i);
+        f[0] = f32x4{v[0], v[1], v[2], v[3]};
+        f[1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+}
+
 // Compute units of the current device (256 on MI355X; 256 if the query fails), read once
 // per device under std::call_once, so concurrent first calls from several host threads are
 // safe. Launch shapes use it to size grids.
