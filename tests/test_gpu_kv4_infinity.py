@@ -25,3 +25,26 @@ def test_infinities(ql, D, G, dtype):  # noqa: F811
         with np.errstate(invalid="ignore", over="ignore"):
             want = _expected(cache, b, D, G, k, v)
         assert np.array_equal(host(_append(ql, cache, b, G, k, v)), want)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("D,G", DG)
+def test_nan_is_not_kept(ql, D, G, dtype):  # noqa: F811
+    """Single NaN, groups of nothing else, and NaN beside infinities: what is stored for them is finite,
+    and every other group's bytes are the definition's."""
+    b, cache, k, v = _case(D * G, [12], [12], 16, 2, D, G, dtype)
+    clean = _expected(cache, b, D, G, k, v)
+    k[0, 0, 3], v[1, 1, ::2] = np.nan, np.nan
+    k[2, 0, :G], v[3, :, :G] = np.nan, np.nan
+    k[4, 0, 1], k[4, 0, 2], v[5, 1, 0], v[5, 1, 1] = np.nan, np.inf, -np.inf, np.nan
+    got = host(_append(ql, cache, b, G, k, v))
+    hit = {0: np.isnan(k.astype(np.float64)).reshape(12, 2, -1, G).any(-1),
+           1: np.isnan(v.astype(np.float64)).reshape(12, 2, -1, G).any(-1)}
+    P = 16
+    for which in (0, 1):
+        at = P * D // 2 * (1 + which) + which * 4 * P * (D // G)
+        par, ref_par = (c[b.table[0, 0], :, at:at + 4 * P * (D // G)].copy().view(np.float16).reshape(2, D // G, 2, P)
+                        for c in (got, clean))
+        par, ref_par = par[..., :12].transpose(3, 0, 1, 2), ref_par[..., :12].transpose(3, 0, 1, 2)
+        assert np.isfinite(par).all()
+        assert np.array_equal(par[~hit[which]], ref_par[~hit[which]])
