@@ -445,7 +445,8 @@ ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, i
  *         q_stride a multiple of 8 and at least q_heads * D
  * out     [rows][q_heads][D] fp16 contiguous (out)
  * max_q   the most rows of a sequence, max_len the longest length: they shape the launch, and
- *         wrong ones cost speed only. Both >= 1.
+ *         wrong ones cost speed only. Both >= 1. The launch takes every sequence for one of max_q
+ *         rows: prompts and single tokens are faster in a call each than in one.
  * scale   finite; window >= 0, 0 for none
  * workspace, workspace_bytes  at least what attention_kv4_workspace_bytes says for the same
  *         sizes (else QL_ERR_SHAPE), 16-byte aligned; may be NULL if that is 0. Its contents

@@ -404,7 +404,7 @@ def attention_kv4(q, cache, block_table, seq_lens, starts, page_size: int, group
     and pages as for kv4_append; q_heads is a multiple of the cache's heads. scale defaults to
     head_dim ** -0.5; window > 0 keeps the last `window` positions of each row. max_q and max_len,
     the most rows of a sequence and the longest length, shape the launch; they default to what the
-    tensors' sizes allow."""
+    tensors' sizes allow. Prompts and single tokens are faster in a call each than in one."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be 3-D [rows, q_heads, head_dim]")
     T, HQ, D = q.shape

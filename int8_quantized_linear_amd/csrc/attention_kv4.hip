@@ -22,14 +22,16 @@
 //                 its scales lie along the summed axis; folding them into P would tie P's fp16
 //                 range to V's magnitude. P enters as two fp16 terms (22 bits): V's rounding and
 //                 the output's are the only ones to fp16. With one term the error against 64
-//                 bits is 1.6 times the output's own rounding, with two 1.4 times, and with V's
+//                 bits is 1.6 times the output's own rounding, with two 1.33 times, and with V's
 //                 codes and scales kept apart as well 1.0 times, but for long sums, whose two parts
 //                 cancel (4 times at 131072 tokens). The second term costs the decode kernel 4 to
-//                 8%.
+//                 7% (517 positions 9.95 -> 10.3 us, 131072 40.0 -> 42.3 us), 15% where the chip is
+//                 full (165 -> 190 us), the prompt kernel 13%.
 // The running maximum is raised only when a score exceeds it by 2^8 (weights up to 2^14, sums
 // in fp32), so most steps have neither a reduction across lanes nor a rescaling of O.
-// 64 tokens of 8 x 8 heads of 128 over 8192 to 16384 positions (902 MB in groups of 64) take 177 us,
-// 5.1 TB/s; the same copies without the arithmetic take 155 us.
+// 64 tokens of 8 x 8 heads of 128 over 8192 to 16384 positions (902 MB in groups of 64) take 172 to
+// 187 us by the card, 4.8 to 5.2 TB/s; where they take 177, the same copies without the arithmetic
+// take 143.
 #include <algorithm>
 
 #include "kv4.h"
@@ -314,9 +316,9 @@ __device__ inline void two_terms(const float (&v)[8], f16x8& hi, f16x8& lo) {
 // for each group the sum of q over it: both 2^e times as large, the operand times `sign`, its slots
 // 2, 3, 6 and 7 divided by 16 for codes that stand 16 times as high, the sums times sign 2^-24.
 // Returns e. The division rounds to 2^-24, which costs q below 2^-10 bits. Beside others of 1/4 and
-// more that is less than the fp32 sums' own rounding, and e is 0; a wave with a lane whose q are all
-// smaller brings the largest |q| of each column to 2^14 (by 2^30 at most, with which the smallest
-// fp16 number is 64). Done in every wave, that took 0.25 us of a call.
+// more that is of the order of the fp32 sums' own rounding, and e is 0; a wave with a lane whose q are
+// all smaller brings the largest |q| of each column to 2^14 (by 2^30 at most, with which the smallest
+// fp16 number is 64). Done in every wave, that took 0.25 us of a call, the look for it 0.1.
 template <int D, int G>
 __device__ inline int q_column(const _Float16* src, bool ok, float sign, f16x8 (&q)[D / 32], float (&qsum)[D / G]) {
     f16x8 big = {};
@@ -745,8 +747,9 @@ __global__ __launch_bounds__(AT, NQ == 1 && D <= 128 && G * 2 >= D ? 3 : D == 25
 // Two launches' latencies (a split's statistics, then its values) are most of it, so nothing
 // else is looked up: splits without tokens have left l = 0. One workgroup for many splits of few
 // rows, one wave for a few splits of many (both kernels together, by workgroups and by waves: 1 row
-// of 32 heads in 64 splits 40.4 and 41.8 us, 65 rows of 28 heads in 3 splits 15.9 and 14.6 us). The
-// join of 33 rows of 32 heads in 2 splits takes 4.6 us.
+// of 32 heads in 64 splits 41.9 and 43.0 us, 2 rows in 32 splits 18.5 and 19.4, 4 rows in 16 splits
+// 18.0 and 18.0, 65 rows of 28 heads in 3 splits 16.7 and 15.7 us). The join of 33 rows of 32 heads in
+// 2 splits takes 4.5 us.
 constexpr int MAX_SPLITS = 256;
 
 template <int D, int WAVES>
@@ -831,9 +834,11 @@ __global__ __launch_bounds__(AT) void attention_kv4_join_kernel(const float* __r
 // either half of the workgroup, and the halves run one phase apart, with a barrier at each
 // phase's end: one wave's products run beside the other's vector work. What block j's operands
 // overwrite has then been read: K's of block j - 3 (three buffers), V's of j - 4 (four). 2048 rows of
-// 8 x 4 heads of 128 after 2048 positions take 180 us, 575 TFLOP/s of the formula's products, or 860
-// with those of P's second term (a library product of 8192 x 8192 x 8192 reaches 1216). Pages of less
-// than a block look each part's page up (taken for pages of 64 as well: 213 us).
+// 8 x 4 heads of 128 after 2048 positions take 180 to 212 us by the card, 575 TFLOP/s of the formula's
+// products at 180, or 860 with those of P's second term (a library product of 8192 x 8192 x 8192 reaches
+// 1216). Pages of less than a block look each part's page up (4 x 1024 rows of 1024: 77.4 us from pages
+// of 16, 76.2 of 64). D = 64, D = 256 in groups of 32 and D = 128 in groups of 32 with two blocks a wave keep
+// 2 to 12 registers in scratch, none of them touched in the loop over the blocks.
 constexpr int PT = 512;   // threads
 constexpr int prompt_block(int D) { return D == 256 ? 32 : 64; }   // tokens of a block: 126 KB of LDS
 
@@ -1229,7 +1234,12 @@ __global__ __launch_bounds__(PT, D == 64 ? 4 : 2) void attention_kv4_prompt_kern
     }
 }
 
-constexpr int64_t FILL = 512;                      // workgroups that two on each CU make
+// Workgroups that a call's splits make: two on each CU. In us, 8 x 4 heads, with 256, 512, 768, 1024:
+// 1 x 65536 tokens, D = 64 22.2, 19.8, 20.9, 21.2; D = 128 28.0, 26.9, 29.1, 32.6; D = 256 41.9, 43.3,
+// 49.1, 54.2 (in groups of 32, one workgroup a CU: 52.9, 63.7, 76.4, 83.3); 33 x 4100 and shorter, D = 64
+// 30.4, 26.3, 24.7, 23.1; D = 128 40.0, 35.2, 34.4, 34.4; D = 256 62.4, 57.7, 63.6, 61.4; 8 x 5 rows over
+// 8192, D = 128 33.1, 31.5, 37.9, 38.8.
+constexpr int64_t FILL = 512;
 constexpr int64_t MAX_GROUPS = (int64_t)1 << 22;   // of a launch (threads stay below 2^32); the kernels loop
 
 // Blocks of 16 (row, head) pairs that each wave of the prompt kernel takes, or 0 for the decode
@@ -1237,10 +1247,11 @@ constexpr int64_t MAX_GROUPS = (int64_t)1 << 22;   // of a launch (threads stay 
 // a round of prompt workgroups, which each hold a CU and are not split over the length, and a decode
 // tile of 32 pairs as a share of the whole chip. Rows see `mean` of the longest length on average;
 // decode tiles and prompt workgroups past the first round make use of that, a first round lasts as
-// long as its longest. In us, 1 x 2048 rows of 2048 positions (D = 128): one block a wave 88, two
-// 104, decode 109; 1 x 2048 of 4096: 210, 192, 242; 4 x 1024 of 1024: 101, 78, 128; 1 x 512 of
-// 8192: 234, 334, 150; 16 x 64 of 2048: 71, 98, 73. D = 64 in blocks of two gains nowhere (4 x 2048
-// of 2048: 178, 183, 225; 16 x 500 of 500: 61, 72, 100), D = 256 has registers for one only.
+// long as its longest. In us, one block a wave, two, decode (8 x 4 heads, D = 128): 1 x 2048 rows of 2048
+// positions 81, 98, 99; 1 x 2048 of 4096 191, 186, 213; 4 x 1024 of 1024 94, 74, 122; 1 x 512 of 8192
+// 237, 332, 146; 16 x 64 of 2048 69, 95, 70. D = 64 in blocks of two gained nowhere, D = 256 has
+// registers for one only. The rule counts max_q rows of max_len positions in every sequence: in a
+// batch that mixes prompts with single tokens it takes the single tokens for prompts.
 inline int prompt_blocks(int64_t pairs, int64_t heads, int D, int max_q, int max_len, int window) {
     const double one = D == 64 ? 30.0 : D == 128 ? 76.0 : 100.0, two = 106.0;
     const double first = D == 64 ? 13.5 : 0.0;   // two workgroups share a CU: a round alone costs more
@@ -1257,14 +1268,15 @@ inline int prompt_blocks(int64_t pairs, int64_t heads, int D, int max_q, int max
 }
 
 // Rows of a decode tile: 16, or 32 where a sequence has more and two tiles' O and Q fit in the
-// registers of two waves a SIMD (5 rows of 4 heads over 8192 tokens, 8 sequences of 8 kv heads,
-// with one term for P: D = 128 27.9 us in tiles of 32, 32.0 of 16; D = 256 64.8 and 51.7).
+// registers of two waves a SIMD. In us, in tiles of 32 and of 16: 8 x 5 rows of 8 x 4 heads over 8192
+// tokens, D = 64 22.7, 24.6; D = 128 31.4, 34.5; D = 256 139, 56; one sequence of 8 rows over 32768,
+// which are few tiles either way, D = 128 29.5, 26.8.
 inline int rows_per_tile(int64_t pairs, int D) { return pairs <= 16 || D == 256 ? 16 : 32; }
 
 // Splits: two workgroups of four waves a CU fill the chip, so that many in all, each with at
 // least 256 tokens, and at most what the second kernel joins. Up to 640 tokens stay whole: the
-// join costs what 256 tokens do (32 heads of 128, 512 tokens 8.7 us whole, 9.5 us in halves;
-// 1024 tokens 12.8 us whole, 9.9 us in quarters).
+// join costs what 256 tokens do (32 heads of 128, 512 tokens 9.4 us whole, 10.3 us in halves; 768
+// tokens 11.6 and 10.9; 1024 tokens 13.8 us whole, 11.1 us in quarters).
 Split plan(int q_heads, int kv_heads, int D, int batch, int max_q, int max_len, int window) {
     const int64_t pairs = (int64_t)max_q * (q_heads / kv_heads);
     constexpr int64_t unit = TB * AW;
