@@ -419,8 +419,8 @@ ql_status kv4_append(const void* k, const void* v, ql_dtype dtype, int64_t k_str
                      const int32_t* seq_lens, const int32_t* starts, int64_t batch, void* stream);
 
 /*
- * Reads rows back: scale * code + low in fp32, rounded once to dtype; zeros for rows without a
- * position.
+ * Reads rows back: scale * code + low in fp32, rounded once to dtype (fp16: infinite past 65519, which
+ * rows near 65504 can pass); zeros for rows without a position.
  * k_out, v_out  [rows][kv_heads][D] contiguous, fp32 or fp16 (dtype) (out)
  */
 ql_status kv4_read(const uint8_t* cache, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
