@@ -462,6 +462,46 @@ ql_status attention_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t k
                                         int64_t batch, int64_t max_q, int64_t max_len, int64_t window,
                                         int64_t* bytes);
 
+/*
+ * E4M3 codes with a scale for each block of 128 values. Blocks start at multiples of 128 along K
+ * (and along N for weights); the last one may be shorter. With kb = ceil(K / 128) blocks of K and
+ * nb = ceil(N / 128) blocks of N:
+ *   activations  codes [M,K], scales fp32 [kb][M] (a block's scales of all rows together)
+ *   weights      codes W [K,N] column-major ([N][K]), scales fp32 [nb][kb], one for 128 x 128
+ *
+ * Activations: per row m and block b, with quantize_per_row_e4m3's arithmetic in the block:
+ *   a = max_{k in b} |x[m,k]|,  x_scale[b][m] = max(a, 1e-10) / 448
+ *   xq[m,k] = e4m3(clamp(x[m,k] / x_scale[b][m], -448, 448))
+ * x  [M,K] row-major, fp32 (QL_F32) or fp16 (QL_F16). Requires K > 0 and K % 16 == 0.
+ */
+ql_status quantize_per_row_block_e4m3(const void* x, ql_dtype x_dtype, int64_t M, int64_t K,
+                                      uint8_t* xq, float* x_scale, void* stream);
+
+/*
+ * Weights, the same per block of 128 x 128, for E matrices at once (the experts of
+ * moe_e4m3_block; 1 for a layer's).
+ * w        [E][N][K] fp32
+ * wq       [E][N][K] codes (out);  w_scale fp32 [E][nb][kb] (out)
+ * Requires E >= 0, K > 0 and K % 16 == 0. E == 0 or N == 0: nothing to do.
+ */
+ql_status quantize_weight_block_e4m3(const float* w, int64_t E, int64_t K, int64_t N, uint8_t* wq,
+                                     float* w_scale, void* stream);
+
+/*
+ * The layer on such codes:
+ *   y[m,n] = act(sum_b x_scale[b][m] * w_scale[n / 128][b] * sum_{k in b} dec(xq[m,k]) * dec(wq[k,n])
+ *                + bias[n])
+ * The inner sums have the precision that gemm_e4m3_per_channel states, each starting from zero; the
+ * outer sum is fp32. Scales are finite; codes must not be NaN (0x7F, 0xFF). A scale's size is free as
+ * long as each block's product and the sum stay in fp32's range.
+ * xq [M,K], x_scale fp32 [kb][M], wq [N][K], w_scale fp32 [nb][kb], bias fp32 [N] or NULL; y [M,N]
+ * row-major, fp32 or fp16; act as ql_activation.
+ * Requires K > 0, K % 64 == 0, K <= 131008 and N <= 2^23.
+ */
+ql_status gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t* wq, const float* w_scale,
+                          const float* bias, ql_activation act, void* y, ql_dtype y_dtype, int64_t M,
+                          int64_t N, int64_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,7 +25,8 @@ __all__ = [
     "quantize_per_row_e4m3", "quantize_weight_per_channel_e4m3", "gemm_e4m3_per_channel",
     "linear_e4m3", "quantize_per_tensor_int8", "gemm_w8a8_requant",
     "rms_norm_quantize_int8", "rms_norm_quantize_e4m3", "kv4_page_bytes", "kv4_append", "kv4_read",
-    "attention_kv4",
+    "attention_kv4", "quantize_per_row_block_e4m3", "quantize_weight_block_e4m3", "gemm_e4m3_block",
+    "linear_e4m3_block",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,6 +75,9 @@ _SIGS = {
     "kv4_read": [_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _P],
     "attention_kv4": [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64,
                       _I64, _F, _I64, _P, _I64, _P],
+    "quantize_per_row_block_e4m3": [_P, _I, _I64, _I64, _P, _P, _P],
+    "quantize_weight_block_e4m3": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "gemm_e4m3_block": [_P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P],
     "attention_kv4_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
 }
 for _name, _args in _SIGS.items():
@@ -608,6 +612,92 @@ def linear_e4m3(x, wq, w_scale, bias=None, act: str = "none", out_dtype=None):
     xq, xs = quantize_per_row_e4m3(x)
     od = out_dtype or (torch.float32 if x.dtype == torch.float32 else torch.float16)
     return gemm_e4m3_per_channel(xq, xs, wq, w_scale, bias, act, od)
+
+
+# ------------------------------------------- E4M3 codes with a scale for each block of 128
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 that n values make, the last one possibly shorter."""
+    return -(-n // 128)
+
+
+def _codes_e4m3(t, name, dims):
+    """E4M3 codes (float8_e4m3fn or their bytes), contiguous, on the GPU, of `dims` dimensions."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _FP8 and t.is_contiguous()):
+        _check(t, name, _FP8)
+    if t.dim() != dims:
+        raise ValueError("%s must be %d-D, has shape %s" % (name, dims, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def quantize_per_row_block_e4m3(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
+                                x_scale: Optional[torch.Tensor] = None):
+    """fp8 (E4M3) codes of x [M, K] (fp16 or fp32) with one scale for each row and 128 values of K:
+    (xq float8_e4m3fn [M, K], x_scale fp32 [ceil(K / 128), M], block by block)."""
+    dt, xp = _float_matrix(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    index = x.get_device()
+    if xq is None:
+        xq = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    elif _codes_e4m3(xq, "xq", 2) and (xq.shape != x.shape or xq.device != x.device):
+        raise ValueError("xq has shape %s on %s, expected %s on %s" % (tuple(xq.shape), xq.device, (M, K), x.device))
+    if x_scale is None:
+        x_scale = x.new_empty((_blocks(K), M), dtype=torch.float32)
+    sp = _same(x_scale, "x_scale", torch.float32, (_blocks(K), M), index)
+    _status("quantize_per_row_block_e4m3", lib.quantize_per_row_block_e4m3(
+        xp, dt, M, K, xq.data_ptr(), sp, _raw_stream(index)))
+    return xq, x_scale
+
+
+def quantize_weight_block_e4m3(w_nk: torch.Tensor):
+    """fp8 (E4M3) codes of W ([N, K] storage, or [E, N, K] for several matrices; fp32) with one scale
+    for each block of 128 x 128: (wq float8_e4m3fn of w's shape, w_scale fp32 [..., ceil(N / 128),
+    ceil(K / 128)])."""
+    _check(w_nk, "w", (torch.float32,))
+    if w_nk.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    N, K = w_nk.shape[-2:]
+    E = w_nk.shape[0] if w_nk.dim() == 3 else 1
+    wq = torch.empty(w_nk.shape, dtype=torch.float8_e4m3fn, device=w_nk.device)
+    ws = torch.empty((*w_nk.shape[:-2], _blocks(N), _blocks(K)), dtype=torch.float32, device=w_nk.device)
+    _call("quantize_weight_block_e4m3", _ptr(w_nk), E, K, N, _ptr(wq), _ptr(ws), _stream(w_nk))
+    return wq, ws
+
+
+def gemm_e4m3_block(xq, x_scale, wq, w_scale, bias=None, act: str = "none", out_dtype=torch.float16, y=None):
+    """y [M, N] = act(sum_b x_scale[b, m] w_scale[n // 128, b] sum_{k in block b} xq[m, k] wq[n, k] +
+    bias[n]) on E4M3 codes (float8_e4m3fn or uint8) with a scale for each block of 128: x_scale
+    fp32 [ceil(K / 128), M], w_scale fp32 [ceil(N / 128), ceil(K / 128)]. act in ACTIVATIONS; y
+    fp16 or fp32."""
+    xp, wp = _codes_e4m3(xq, "xq", 2), _codes_e4m3(wq, "wq", 2)
+    M, K = xq.shape
+    N = wq.shape[0]
+    index = xq.get_device()
+    if wq.shape[1] != K or wq.get_device() != index:
+        raise ValueError("wq has shape %s on %s, expected [N, %d] on %s" % (tuple(wq.shape), wq.device, K, xq.device))
+    kb = _blocks(K)
+    sp = _same(x_scale, "x_scale", torch.float32, (kb, M), index)
+    tp = _same(w_scale, "w_scale", torch.float32, (_blocks(N), kb), index)
+    bp = None if bias is None else _same(bias, "bias", torch.float32, (N,), index)
+    if out_dtype not in _FLOATS:
+        raise TypeError("out_dtype must be float16 or float32")
+    if y is None:
+        y = xq.new_empty((M, N), dtype=out_dtype)
+        yp = y.data_ptr()
+    else:
+        yp = _same(y, "y", out_dtype, (M, N), index)
+    _status("gemm_e4m3_block", lib.gemm_e4m3_block(
+        xp, sp, wp, tp, bp, _act_code(act), yp, QL_F16 if out_dtype is torch.float16 else QL_F32, M, N, K,
+        _raw_stream(index)))
+    return y
+
+
+def linear_e4m3_block(x, wq, w_scale, bias=None, act: str = "none", out_dtype=None):
+    """The block-scaled fp8 layer: quantize_per_row_block_e4m3 of x, then gemm_e4m3_block."""
+    xq, xs = quantize_per_row_block_e4m3(x)
+    return gemm_e4m3_block(xq, xs, wq, w_scale, bias, act, out_dtype or x.dtype)
 
 
 def linear_w8a8_asym(x, wq, w_scale, w_colsum, bias=None, act: str = "none", out_dtype=None):

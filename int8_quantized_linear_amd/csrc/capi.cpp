@@ -5,6 +5,7 @@
 
 #include <cmath>
 
+#include "e4m3_block.h"
 #include "kv4.h"
 
 namespace {
@@ -533,6 +534,52 @@ ql_status attention_kv4(const void* q, int64_t q_stride, void* out, int64_t rows
     a.ws_floats = workspace_bytes / 4;
     return ql::launch_attention_kv4(a, kv4_cache(cache, num_pages, page_size, kv_heads, D, group), (int)D, (int)group,
                                     kv4_batch(block_table, table_width, seq_lens, starts, batch, rows), as_stream(stream));
+}
+
+ql_status quantize_per_row_block_e4m3(const void* x, ql_dtype x_dtype, int64_t M, int64_t K, uint8_t* xq,
+                                      float* x_scale, void* stream) {
+    if (x_dtype != QL_F32 && x_dtype != QL_F16)
+        return QL_ERR_DTYPE;
+    if (bad_dims(M, 1, K) || K % 16 != 0)
+        return QL_ERR_SHAPE;
+    if (M == 0)
+        return QL_OK;
+    if (!x || !xq || !x_scale)
+        return QL_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(x_scale, 4))
+        return QL_ERR_ALIGN;
+    return ql::launch_quant_rows_block_e4m3(x, x_dtype == QL_F16, M, K, xq, x_scale, as_stream(stream));
+}
+
+ql_status quantize_weight_block_e4m3(const float* w, int64_t E, int64_t K, int64_t N, uint8_t* wq,
+                                     float* w_scale, void* stream) {
+    if (bad_dims(1, N, K) || K % 16 != 0 || E < 0 || E > (1 << 20))
+        return QL_ERR_SHAPE;
+    if (N == 0 || E == 0)
+        return QL_OK;
+    if (!w || !wq || !w_scale)
+        return QL_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(wq, 16) || !aligned(w_scale, 4))
+        return QL_ERR_ALIGN;
+    return ql::launch_quant_weight_block_e4m3(w, E, N, K, wq, w_scale, as_stream(stream));
+}
+
+ql_status gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t* wq, const float* w_scale,
+                          const float* bias, ql_activation act, void* y, ql_dtype y_dtype, int64_t M,
+                          int64_t N, int64_t K, void* stream) {
+    if (y_dtype != QL_F32 && y_dtype != QL_F16)
+        return QL_ERR_DTYPE;
+    if (act != QL_ACT_NONE && act != QL_ACT_GELU && act != QL_ACT_SILU)
+        return QL_ERR_DTYPE;
+    ql_status st = check_w8a8(reinterpret_cast<const int8_t*>(xq), reinterpret_cast<const int8_t*>(wq), y, M, N, K);
+    if (st != QL_OK || M == 0 || N == 0)
+        return st;
+    if (!x_scale || !w_scale)
+        return QL_ERR_NULL;
+    if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || (bias && !aligned(bias, 4)))
+        return QL_ERR_ALIGN;
+    return ql::launch_gemm_e4m3_block(xq, x_scale, wq, w_scale, bias, (int)act, y, y_dtype == QL_F16, M, N, K,
+                                      as_stream(stream));
 }
 
 }  // extern "C"

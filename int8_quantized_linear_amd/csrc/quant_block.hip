@@ -1,0 +1,150 @@
+// quant_block.hip -- E4M3 codes with a scale for each block of 128: activations (one row's 128
+// values a block) and weights (128 x 128 a block).
+//
+//   a = max |v| over the block,  s = max(a, 1e-10) / 448,  code = e4m3(clamp(v / s, -448, 448))
+//
+// Each value is read once and its code written once; both are bound by memory.
+#include "e4m3_block.h"
+#include "quant_codes.h"
+
+namespace ql {
+namespace {
+
+constexpr int NT = 256;
+
+// Maximum over the 16 lanes of a row of lanes, in every one of them.
+__device__ inline float max16(float v) {
+    auto step = [&](auto ctrl) {
+        const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true);
+        v = fmaxf(v, __int_as_float(o));
+    };
+    step(std::integral_constant<int, 0x128>{});   // rotations by 8, 4, 2 and 1 lanes
+    step(std::integral_constant<int, 0x124>{});
+    step(std::integral_constant<int, 0x122>{});
+    step(std::integral_constant<int, 0x121>{});
+    return v;
+}
+
+template <bool F16>
+__device__ inline void load8(float (&v)[8], const void* p, int64_t i) {
+    if constexpr (F16) {
+        const f16x8 h = *reinterpret_cast<const f16x8*>(reinterpret_cast<const _Float16*>(p) + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = (float)h[j];
+    } else {
+        const f32x4* f = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = f[j / 4][j % 4];
+    }
+}
+
+__device__ inline float absmax8(const float (&v)[8]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        a = fmaxf(a, fabsf(v[j]));
+    return a;
+}
+
+// 16 lanes take a block of one row, 8 values each; a workgroup 16 rows and RB blocks of K, so that
+// the 16 scales of a block leave as one 64-byte piece.
+constexpr int RB = 4;
+template <bool F16>
+__global__ __launch_bounds__(NT) void quant_rows_block_kernel(const void* __restrict__ x, int64_t M, int64_t K,
+                                                              int nkb, int64_t first, uint8_t* __restrict__ xq,
+                                                              float* __restrict__ xs) {
+    const int kgroups = (nkb + RB - 1) / RB;
+    const int64_t wg = first + blockIdx.x;
+    const int64_t m = wg / kgroups * 16 + threadIdx.x / 16;
+    const int b0 = (int)(wg % kgroups) * RB, l = threadIdx.x % 16;
+    if (m >= M)
+        return;
+    float v[RB][8];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int64_t k = (int64_t)(b0 + b) * QB + 8 * l;
+        if (k < K) {
+            load8<F16>(v[b], x, m * K + k);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[b][j] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int64_t k = (int64_t)(b0 + b) * QB + 8 * l;
+        const float s = fmaxf(max16(absmax8(v[b])), 1e-10f) / 448.0f;
+        if (k < K)
+            store_codes_e4m3<8>(xq + m * K + k, v[b], s, 1.0f / s);
+        if (l == 0 && b0 + b < nkb)
+            xs[(b0 + b) * M + m] = s;
+    }
+}
+
+// A workgroup takes one block of 128 x 128: 16 lanes a row, eight rows a thread.
+__global__ __launch_bounds__(NT) void quant_weight_block_kernel(const float* __restrict__ w, int64_t N, int64_t K,
+                                                                int64_t nnb, int64_t nkb, int64_t first,
+                                                                uint8_t* __restrict__ wq, float* __restrict__ ws) {
+    __shared__ float red[NT / WAVE];
+    const int64_t wg = first + blockIdx.x;
+    const int64_t kb = wg % nkb, nb = wg / nkb % nnb, e = wg / nkb / nnb;
+    const int64_t k = kb * QB + 8 * (threadIdx.x % 16), n0 = nb * QB + threadIdx.x / 16;
+    w += e * N * K;
+    wq += e * N * K;
+    float v[8][8], a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (n0 + 16 * i < N && k < K) {
+            load8<false>(v[i], w, (n0 + 16 * i) * K + k);
+            a = fmaxf(a, absmax8(v[i]));
+        }
+    }
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o >>= 1)
+        a = fmaxf(a, __shfl_xor(a, o, WAVE));
+    if (threadIdx.x % WAVE == 0)
+        red[threadIdx.x / WAVE] = a;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / WAVE; ++i)
+        a = fmaxf(a, red[i]);
+    const float s = fmaxf(a, 1e-10f) / 448.0f, y = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (n0 + 16 * i < N && k < K)
+            store_codes_e4m3<8>(wq + (n0 + 16 * i) * K + k, v[i], s, y);
+    if (threadIdx.x == 0)
+        ws[wg] = s;
+}
+
+constexpr int64_t MOST = (int64_t)1 << 23;   // workgroups of a launch: its threads stay below 2^32
+
+}  // namespace
+
+ql_status launch_quant_rows_block_e4m3(const void* x, bool x_f16, int64_t M, int64_t K, uint8_t* xq, float* x_scale,
+                                       hipStream_t stream) {
+    const int nkb = (int)e4m3_blocks(K);
+    const int64_t wgs = (M + 15) / 16 * ((nkb + RB - 1) / RB);
+    for (int64_t f = 0; f < wgs; f += MOST) {
+        const dim3 grid((uint32_t)(wgs - f < MOST ? wgs - f : MOST));
+        if (x_f16)
+            quant_rows_block_kernel<true><<<grid, dim3(NT), 0, stream>>>(x, M, K, nkb, f, xq, x_scale);
+        else
+            quant_rows_block_kernel<false><<<grid, dim3(NT), 0, stream>>>(x, M, K, nkb, f, xq, x_scale);
+    }
+    return launch_status();
+}
+
+ql_status launch_quant_weight_block_e4m3(const float* w, int64_t E, int64_t N, int64_t K, uint8_t* wq, float* w_scale,
+                                         hipStream_t stream) {
+    const int64_t nnb = e4m3_blocks(N), nkb = e4m3_blocks(K), wgs = E * nnb * nkb;
+    for (int64_t f = 0; f < wgs; f += MOST)
+        quant_weight_block_kernel<<<dim3((uint32_t)(wgs - f < MOST ? wgs - f : MOST)), dim3(NT), 0, stream>>>(
+            w, N, K, nnb, nkb, f, wq, w_scale);
+    return launch_status();
+}
+
+}  // namespace ql
