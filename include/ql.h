@@ -502,6 +502,45 @@ ql_status gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t
                           const float* bias, ql_activation act, void* y, ql_dtype y_dtype, int64_t M,
                           int64_t N, int64_t K, void* stream);
 
+/*
+ * A mixture-of-experts layer for a few tokens (a decode step, drafted tokens). The router's product:
+ *   logits[t][e] = sum_k x[t,k] * w[e,k]          (fp32 sums of exact products)
+ * x [T,K] fp16 row-major, w [E][K] fp16, logits fp32 [T][E] (out); 16-byte aligned (logits 4).
+ * Requires K > 0, K % 64 == 0, K <= 131008, E <= 2^20.
+ */
+ql_status moe_router(const void* x, const void* w, float* logits, int64_t T, int64_t E, int64_t K, void* stream);
+
+/*
+ * The experts, chosen by the logits. Per token t, with p = softmax over all E logits and e_1 .. e_k
+ * the experts of the top_k largest ones (of equal ones the lower numbers):
+ *   p_j    = p[e_j], divided by p[e_1] + .. + p[e_k] if renormalize != 0
+ *   h_j    = p_j * silu(W1[e_j] x[t]) * (W3[e_j] x[t])
+ *   out[t] = sum_j W2[e_j] h_j
+ * A logit of -infinity masks its expert, which is then never chosen (a token whose logits leave fewer
+ * than top_k has fewer; one that has none gives zeros), nor is one whose logit is NaN. +infinity is
+ * not allowed.
+ * Weights are E4M3 codes with a scale for each 128 x 128 block, as quantize_weight_block_e4m3 makes
+ * them. They enter fp16 (W1, W3) or bf16 (W2) products exactly, with fp32 sums; h is kept as two bf16
+ * terms (relative error 2^-17).
+ *
+ * x       [T,K] fp16 row-major
+ * logits  fp32 [T][E]
+ * w13     codes [E][2 I][K]: rows 0 .. I-1 are W1's (gate), I .. 2 I - 1 W3's (up)
+ * s13     fp32 [E][ceil(2 I / 128)][ceil(K / 128)]
+ * w2      codes [E][K][I];  s2 fp32 [E][ceil(K / 128)][ceil(I / 128)]
+ * out     [T,K] row-major, fp32 or fp16 (out_dtype) (out)
+ * workspace, workspace_bytes  at least what moe_e4m3_block_workspace_bytes says (else QL_ERR_SHAPE),
+ *         16-byte aligned. Its contents need not be set, and are not kept.
+ * Requires 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I > 0, multiples of 64 and <= 131008.
+ * Every token's result is the same whatever the other tokens are. Weights of chosen experts are read
+ * once for each 64 tokens: longer batches run, in launches of 64.
+ */
+ql_status moe_e4m3_block(const void* x, const float* logits, const uint8_t* w13, const float* s13,
+                         const uint8_t* w2, const float* s2, void* out, ql_dtype out_dtype, int64_t T,
+                         int64_t E, int64_t top_k, int64_t K, int64_t I, int renormalize, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+ql_status moe_e4m3_block_workspace_bytes(int64_t T, int64_t top_k, int64_t I, int64_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

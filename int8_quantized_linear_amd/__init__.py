@@ -26,7 +26,7 @@ __all__ = [
     "linear_e4m3", "quantize_per_tensor_int8", "gemm_w8a8_requant",
     "rms_norm_quantize_int8", "rms_norm_quantize_e4m3", "kv4_page_bytes", "kv4_append", "kv4_read",
     "attention_kv4", "quantize_per_row_block_e4m3", "quantize_weight_block_e4m3", "gemm_e4m3_block",
-    "linear_e4m3_block",
+    "linear_e4m3_block", "moe_router", "moe_e4m3_block",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +78,9 @@ _SIGS = {
     "quantize_per_row_block_e4m3": [_P, _I, _I64, _I64, _P, _P, _P],
     "quantize_weight_block_e4m3": [_P, _I64, _I64, _I64, _P, _P, _P],
     "gemm_e4m3_block": [_P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P],
+    "moe_router": [_P, _P, _P, _I64, _I64, _I64, _P],
+    "moe_e4m3_block": [_P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P],
+    "moe_e4m3_block_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(_I64)],
     "attention_kv4_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
 }
 for _name, _args in _SIGS.items():
@@ -698,6 +701,71 @@ def linear_e4m3_block(x, wq, w_scale, bias=None, act: str = "none", out_dtype=No
     """The block-scaled fp8 layer: quantize_per_row_block_e4m3 of x, then gemm_e4m3_block."""
     xq, xs = quantize_per_row_block_e4m3(x)
     return gemm_e4m3_block(xq, xs, wq, w_scale, bias, act, out_dtype or x.dtype)
+
+
+def moe_router(x, w, logits=None):
+    """A router's logits: x fp16 [T, K] @ w fp16 [E, K]^T as fp32 [T, E]."""
+    index = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be 2-D [T, K]")
+    T, K = x.shape
+    xp = _same(x, "x", torch.float16, (T, K), index)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be 2-D [E, K]")
+    E = w.shape[0]
+    wp = _same(w, "w", torch.float16, (E, K), index)
+    if logits is None:
+        logits = x.new_empty((T, E), dtype=torch.float32)
+        lp = logits.data_ptr()
+    else:
+        lp = _same(logits, "logits", torch.float32, (T, E), index)
+    _status("moe_router", lib.moe_router(xp, wp, lp, T, E, K, _raw_stream(index)))
+    return logits
+
+
+@functools.lru_cache(maxsize=1024)
+def _moe_workspace(T, top_k, I):
+    need = _I64(0)
+    _call("moe_e4m3_block_workspace_bytes", T, top_k, I, ctypes.byref(need))
+    return need.value
+
+
+def moe_e4m3_block(x, logits, w13, s13, w2, s2, top_k: int, renormalize: bool = True, out_dtype=torch.float16,
+                   out=None):
+    """A mixture-of-experts layer for a few tokens. x fp16 [T, K], logits fp32 [T, E] (moe_router's;
+    -inf masks an expert). Per token the top_k experts e_j of the largest logits, weighted by the
+    softmax over all experts (over the chosen ones, if renormalize):
+    out [T, K] = sum_j p_j W2[e_j] (silu(W1[e_j] x) * (W3[e_j] x)), fp16 or fp32. w13 are codes
+    (float8_e4m3fn or uint8) [E, 2 I, K], W1's rows before W3's, w2 codes [E, K, I], both with a
+    scale for each 128 x 128 block, as quantize_weight_block_e4m3 returns them. Meant for up to 64
+    tokens; longer batches run in launches of 64."""
+    wp, vp = _codes_e4m3(w13, "w13", 3), _codes_e4m3(w2, "w2", 3)
+    E, I2, K = w13.shape
+    I = I2 // 2
+    index = w13.get_device()
+    if I2 % 2 or w2.shape != (E, K, I) or w2.get_device() != index:
+        raise ValueError("w13 %s and w2 %s on %s and %s: expected [E, 2 I, K] and [E, K, I] on one device"
+                         % (tuple(w13.shape), tuple(w2.shape), w13.device, w2.device))
+    sp = _same(s13, "s13", torch.float32, (E, _blocks(I2), _blocks(K)), index)
+    tp = _same(s2, "s2", torch.float32, (E, _blocks(K), _blocks(I)), index)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be 2-D [T, K]")
+    T = x.shape[0]
+    xp = _same(x, "x", torch.float16, (T, K), index)
+    lp = _same(logits, "logits", torch.float32, (T, E), index)
+    if out_dtype not in _FLOATS:
+        raise TypeError("out_dtype must be float16 or float32")
+    if out is None:
+        out = x.new_empty((T, K), dtype=out_dtype)
+        op = out.data_ptr()
+    else:
+        op = _same(out, "out", out_dtype, (T, K), index)
+    need = _moe_workspace(T, top_k, I)
+    ws = w13.new_empty((need,), dtype=torch.uint8)   # of the current stream, as the kernels are
+    _status("moe_e4m3_block", lib.moe_e4m3_block(
+        xp, lp, wp, sp, vp, tp, op, QL_F16 if out_dtype is torch.float16 else QL_F32, T, E, top_k, K, I,
+        1 if renormalize else 0, ws.data_ptr(), need, _raw_stream(index)))
+    return out
 
 
 def linear_w8a8_asym(x, wq, w_scale, w_colsum, bias=None, act: str = "none", out_dtype=None):

@@ -25,7 +25,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["capi.cpp", "quant.hip", "gemm_w8a8.hip", "gemm_w8a8_small.hip", "gemm_w8a8_mid.hip", "wonly.hip",
-           "norm.hip", "kv4.hip", "attention_kv4.hip", "quant_block.hip", "gemm_e4m3_block.hip"]
+           "norm.hip", "kv4.hip", "attention_kv4.hip", "quant_block.hip", "gemm_e4m3_block.hip",
+           "moe.hip"]
 PROBE_SOURCES = ["probes.hip"]
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",

@@ -582,4 +582,65 @@ ql_status gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t
                                       as_stream(stream));
 }
 
+ql_status moe_router(const void* x, const void* w, float* logits, int64_t T, int64_t E, int64_t K, void* stream) {
+    if (bad_dims(T, E, K) || K % 64 != 0 || K > kMaxKw8a8 || E > (1 << 20))
+        return QL_ERR_SHAPE;
+    if (T == 0 || E == 0)
+        return QL_OK;
+    if (!x || !w || !logits)
+        return QL_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(logits, 4))
+        return QL_ERR_ALIGN;
+    return ql::launch_moe_router(x, w, logits, T, E, K, as_stream(stream));
+}
+
+static bool bad_moe(int64_t T, int64_t top_k, int64_t I) {
+    return T < 0 || T >= kMaxDim || top_k < 1 || top_k > ql::MOE_TOP_K || I < 1 || I % 64 != 0 || I > kMaxKw8a8;
+}
+
+ql_status moe_e4m3_block_workspace_bytes(int64_t T, int64_t top_k, int64_t I, int64_t* bytes) {
+    if (bad_moe(T, top_k, I))
+        return QL_ERR_SHAPE;
+    if (!bytes)
+        return QL_ERR_NULL;
+    *bytes = T == 0 ? 0 : ql::moe_workspace(T, (int)top_k, (int)I);
+    return QL_OK;
+}
+
+ql_status moe_e4m3_block(const void* x, const float* logits, const uint8_t* w13, const float* s13,
+                         const uint8_t* w2, const float* s2, void* out, ql_dtype out_dtype, int64_t T,
+                         int64_t E, int64_t top_k, int64_t K, int64_t I, int renormalize, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+    if (out_dtype != QL_F32 && out_dtype != QL_F16)
+        return QL_ERR_DTYPE;
+    if (bad_moe(T, top_k, I) || E < top_k || E > ql::MOE_EXPERTS || K < 1 || K % 64 != 0 || K > kMaxKw8a8)
+        return QL_ERR_SHAPE;
+    if (T == 0)
+        return QL_OK;
+    if (workspace_bytes < ql::moe_workspace(T, (int)top_k, (int)I))
+        return QL_ERR_SHAPE;
+    if (!x || !logits || !w13 || !s13 || !w2 || !s2 || !out || !workspace)
+        return QL_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(w13, 16) || !aligned(s13, 4) || !aligned(w2, 16) ||
+        !aligned(s2, 4) || !aligned(out, 16) || !aligned(workspace, 16))
+        return QL_ERR_ALIGN;
+    ql::MoeLayer l = {};
+    l.x = reinterpret_cast<const _Float16*>(x);
+    l.logits = logits;
+    l.w13 = w13;
+    l.s13 = s13;
+    l.w2 = w2;
+    l.s2 = s2;
+    l.out = out;
+    l.ws = reinterpret_cast<int8_t*>(workspace);
+    l.T = T;
+    l.E = (int)E;
+    l.top_k = (int)top_k;
+    l.K = (int)K;
+    l.I = (int)I;
+    l.renormalize = renormalize != 0;
+    l.out_f16 = out_dtype == QL_F16;
+    return ql::launch_moe_e4m3_block(l, as_stream(stream));
+}
+
 }  // extern "C"

@@ -60,4 +60,26 @@ ql_status launch_gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const 
                                  const float* bias, int act, void* y, bool y_f16, int64_t M, int64_t N, int64_t K,
                                  hipStream_t stream);
 
+// A mixture-of-experts layer; see moe_e4m3_block in ql.h.
+struct MoeLayer {
+    const _Float16* x;      // [T][K]
+    const float* logits;    // [T][E]
+    const uint8_t* w13;     // [E][2 I][K]
+    const float* s13;
+    const uint8_t* w2;      // [E][K][I]
+    const float* s2;
+    void* out;              // [T][K]
+    int8_t* ws;
+    int64_t T;
+    int E, top_k, K, I;
+    bool renormalize, out_f16;
+};
+constexpr int MOE_TOKENS = 64;     // of a launch
+constexpr int MOE_EXPERTS = 512;   // at most
+constexpr int MOE_TOP_K = 16;      // at most
+int64_t moe_workspace(int64_t T, int top_k, int I);
+ql_status launch_moe_router(const void* x, const void* w, float* logits, int64_t T, int64_t E, int64_t K,
+                            hipStream_t stream);
+ql_status launch_moe_e4m3_block(const MoeLayer& l, hipStream_t stream);
+
 }  // namespace ql

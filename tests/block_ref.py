@@ -106,3 +106,57 @@ def gemm_tolerance(pre, err, bias, act, f16):
         err = 1.1 * err + (np.abs(v) + 4) * 2.0 ** -23 * np.abs(y) + 1e-30
     half = 2.0 ** -11 if f16 else 2.0 ** -24
     return y, err * (1 + half) + half * np.abs(y) + (2.0 ** -25 if f16 else 1e-37)
+
+
+def routes(logits, k, renorm):
+    """Per token the chosen experts (fewer than k where -inf or NaN leave fewer), their weights in 64
+    bits, and a bound on the relative error of the kernel's fp32 weights."""
+    out = []
+    for row in logits:
+        ok = [e for e in range(row.size) if row[e] > -np.inf]
+        ids = sorted(ok, key=lambda e: (-row[e], e))[:k]
+        if not ids:
+            out.append(([], np.zeros(0), np.zeros(0)))
+            continue
+        d = row.astype(np.float64) - float(row[ids[0]])
+        w = np.where(np.isnan(d), 0, np.exp(np.where(np.isnan(d), 0, d)))
+        among = np.array(ids) if renorm else np.array(ok)
+        total = w[among].sum()
+        # an exponential of d: |d| + 4 units of 2^-23; up to 48 additions of positive terms; division
+        one = lambda e: (np.abs(d[e]) + 4) * 2.0 ** -23  # noqa: E731
+        rel = one(ids) + (w[among] * one(among)).sum() / total + 50 * 2.0 ** -24
+        out.append((ids, w[ids] / total, rel))
+    return out
+
+
+def moe64(x, logits, w13, s13, w2, s2, k, renorm):
+    """The layer in 64 bits, and a bound on the kernel's error before the output's rounding, both
+    [T, K]. fp16 (bf16) products with codes are exact in fp32; a sum of n products in any order, each
+    addition at most one unit off, has an error of n 2^-23 of the sum of magnitudes: 128 and 4 more
+    in a block, one a block, 8 at the join."""
+    T, K = x.shape
+    E, I2, _ = w13.shape
+    I = I2 // 2
+    x = x.astype(np.float64)
+    y, err = np.zeros((T, K)), np.zeros((T, K))
+    up = (132 + blocks(K) + 8) * 2.0 ** -23
+    route = routes(logits, k, renorm)
+    down = (132 + blocks(I) * k + k + 8) * 2.0 ** -23
+    for e in range(E):
+        rows = [t for t in range(T) if e in route[t][0]]
+        if not rows:
+            continue
+        a, b = weight64(w13[e], s13[e]), weight64(w2[e], s2[e])
+        p = np.array([route[t][1][route[t][0].index(e)] for t in rows])[:, None]
+        prel = np.array([route[t][2][route[t][0].index(e)] for t in rows])[:, None]
+        gu, mag = x[rows] @ a.T, np.abs(x[rows]) @ np.abs(a).T
+        g, u, eg, eu = gu[:, :I], gu[:, I:], up * mag[:, :I], up * mag[:, I:]
+        with np.errstate(over="ignore"):
+            s = g / (1 + np.exp(-g))
+        es = 1.1 * eg + (np.abs(g) + 4) * 2.0 ** -23 * np.abs(s) + 1e-30
+        h = p * s * u
+        # both factors' errors, the weight's, three roundings, two bf16 terms
+        eh = p * (es * (np.abs(u) + eu) + np.abs(s) * eu) + np.abs(h) * (prel + 3 * 2.0 ** -24 + 2.0 ** -17)
+        y[rows] += h @ b.T
+        err[rows] += eh @ np.abs(b).T + down * (np.abs(h) + eh) @ np.abs(b).T
+    return y, err

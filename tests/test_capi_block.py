@@ -21,6 +21,9 @@ def lib():
     L.quantize_per_row_block_e4m3.argtypes = [P, I, I64, I64, P, P, P]
     L.quantize_weight_block_e4m3.argtypes = [P, I64, I64, I64, P, P, P]
     L.gemm_e4m3_block.argtypes = [P, P, P, P, P, I, P, I, I64, I64, I64, P]
+    L.moe_router.argtypes = [P, P, P, I64, I64, I64, P]
+    L.moe_e4m3_block.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, I, P, I64, P]
+    L.moe_e4m3_block_workspace_bytes.argtypes = [I64, I64, I64, ctypes.POINTER(I64)]
     return L
 
 
@@ -65,3 +68,45 @@ def test_gemm(lib):
     for kw in (dict(dt=2), dict(act=3), dict(act=-1)):
         assert f(**kw) == DTYPE
     assert f(M=0, x=None) == OK and f(N=0, w=None) == OK
+
+
+def test_router(lib):
+    def f(x=A, w=A, out=A, T=4, E=8, K=256):
+        return lib.moe_router(x, w, out, T, E, K, None)
+
+    for kw in (dict(x=None), dict(w=None), dict(out=None)):
+        assert f(**kw) == NULL
+    for kw in (dict(x=A + 8), dict(w=A + 2), dict(out=A + 2)):
+        assert f(**kw) == ALIGN
+    for kw in (dict(T=-1), dict(E=-1), dict(E=(1 << 20) + 1), dict(K=0), dict(K=96), dict(K=131072)):
+        assert f(**kw) == SHAPE, kw
+    assert f(T=0, x=None) == OK and f(E=0, w=None) == OK
+
+
+def test_experts(lib):
+    def need(T=4, k=2, I=128):
+        n = ctypes.c_int64(-1)
+        assert lib.moe_e4m3_block_workspace_bytes(T, k, I, ctypes.byref(n)) == OK
+        return n.value
+
+    def f(x=A, lg=A, w13=A, s13=A, w2=A, s2=A, out=A, dt=F16, T=4, E=8, k=2, K=256, I=128, ws=A, size=None):
+        return lib.moe_e4m3_block(x, lg, w13, s13, w2, s2, out, dt, T, E, k, K, I, 1, ws,
+                                  need() if size is None else size, None)
+
+    for name in ("x", "lg", "w13", "s13", "w2", "s2", "out", "ws"):
+        assert f(**{name: None}) == NULL
+    for kw in (dict(x=A + 8), dict(lg=A + 2), dict(w13=A + 4), dict(s13=A + 1), dict(w2=MIS), dict(s2=A + 2), dict(out=A + 8),
+               dict(ws=A + 8)):
+        assert f(**kw) == ALIGN, kw
+    for kw in (dict(T=-1), dict(T=1 << 31), dict(E=0), dict(E=513), dict(k=0), dict(k=9), dict(k=17, E=32), dict(E=1), dict(K=0),
+               dict(K=32), dict(K=131072), dict(I=0), dict(I=96), dict(I=131072), dict(size=need() - 1), dict(size=0),
+               dict(T=5)):
+        assert f(**kw) == SHAPE, kw
+    assert f(dt=2) == DTYPE
+    assert f(T=0, x=None, size=0) == OK
+
+    n = ctypes.c_int64(7)
+    for bad in ((-1, 2, 128), (4, 0, 128), (4, 17, 128), (4, 2, 0), (4, 2, 100)):
+        assert lib.moe_e4m3_block_workspace_bytes(*bad, ctypes.byref(n)) == SHAPE
+    assert n.value == 7 and lib.moe_e4m3_block_workspace_bytes(4, 2, 128, None) == NULL
+    assert need(T=0) == 0 and need(T=1000) == need(T=64) > need(T=63)
