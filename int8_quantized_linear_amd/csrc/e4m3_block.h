@@ -60,6 +60,9 @@ ql_status launch_gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const 
                                  const float* bias, int act, void* y, bool y_f16, int64_t M, int64_t N, int64_t K,
                                  hipStream_t stream);
 
+// Kernel of launch_gemm_e4m3_block for these sizes, by its number there. For tests; not part of the interface.
+extern "C" int ql_gemm_e4m3_block_kernel(int64_t M, int64_t N, int64_t K);
+
 // A mixture-of-experts layer; see moe_e4m3_block in ql.h.
 struct MoeLayer {
     const _Float16* x;      // [T][K]

@@ -5,13 +5,10 @@
 // The inner sums run on the fp8 matrix cores, from zero for each block; the block's sum is then
 // added to the output's fp32 sum with its scales, one multiply-add an output and block.
 #include "e4m3_block.h"
+#include "gemm_w8a8_tile.h"
 
 namespace ql {
 namespace {
-
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-
-__device__ inline i32x8 cat(i32x4 lo, i32x4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 
 struct BlockGemm {
     const uint8_t* xq;
@@ -35,18 +32,18 @@ __device__ inline float activated(float v, int act) {
 // in LDS, S - 1 blocks ahead, and needs no barrier until its sums are joined with the others'.
 // W is the first operand, so a lane's sums belong to one row m (lane & 15) and four columns
 // (4 (lane >> 4) + i): one scale of X a lane, one of W for all.
-template <int MB, int SW, int S, bool YF16>
+template <int NB, int MB, int SW, int S, bool YF16>
 __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
-    constexpr int W_BYTES = 16 * QB, X_BYTES = MB * 16 * QB, SLOT = W_BYTES + X_BYTES + 256;
-    constexpr int COPIES = 2 + 2 * MB + 1;
+    constexpr int W_BYTES = NB * 16 * QB, X_BYTES = MB * 16 * QB, SLOT = W_BYTES + X_BYTES + 256;
+    constexpr int COPIES = 2 * NB + 2 * MB + 1;
     __shared__ __attribute__((aligned(1024))) int8_t smem[SW * S * SLOT];
-    static_assert(SW * MB * 1024 <= SW * S * SLOT, "the joined sums fit the ring");
+    static_assert(SW * NB * MB * 1024 <= SW * S * SLOT, "the joined sums fit the ring");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MB;
+    const int n0 = blockIdx.x * 16 * NB, m0 = blockIdx.y * 16 * MB;
     const int nkb = (g.K + QB - 1) / QB;
     int8_t* ring = smem + wave * S * SLOT;
 
-    const __amdgpu_buffer_rsrc_t rw = buffer_of(g.wq + (int64_t)n0 * g.K, min(g.N - n0, 16) * g.K);
+    const __amdgpu_buffer_rsrc_t rw = buffer_of(g.wq + (int64_t)n0 * g.K, min(g.N - n0, 16 * NB) * g.K);
     const __amdgpu_buffer_rsrc_t rx = buffer_of(g.xq + (int64_t)m0 * g.K, min(g.rows - m0, 16 * MB) * g.K);
     const int row = lane >> 3, c0 = copy_chunk128(lane, 0), c1 = copy_chunk128(lane, 1);
     const int far = 0x40000000;
@@ -57,8 +54,11 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
         const int left = g.K - b * QB;   // of this block
         const int cut0 = 16 * c0 < left ? 0 : far, cut1 = 16 * c1 < left ? 0 : far;
         const int o0 = row * g.K + 16 * c0 + b * QB, o1 = row * g.K + 16 * c1 + b * QB;
-        buffer_to_lds16<2>(rw, o0 | cut0, 0, to);
-        buffer_to_lds16<2>(rw, (o1 + 8 * g.K) | cut1, 0, to + 1024);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            buffer_to_lds16<2>(rw, (o0 + 16 * i * g.K) | cut0, 0, to + 2048 * i);
+            buffer_to_lds16<2>(rw, (o1 + (16 * i + 8) * g.K) | cut1, 0, to + 2048 * i + 1024);
+        }
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             buffer_to_lds16(rx, (o0 + 16 * i * g.K) | cut0, 0, to + W_BYTES + 2048 * i);
@@ -67,10 +67,12 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
         global_to_lds4(g.xs + (int64_t)min(b, nkb - 1) * g.M + min(m0 + lane, g.rows - 1), to + W_BYTES + X_BYTES);
     };
 
-    f32x4 acc[MB];
+    f32x4 acc[NB][MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-        acc[i] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            acc[j][i] = f32x4{0, 0, 0, 0};
     // W's scales of this wave's blocks, 64 of them at a time, one a lane
     const float* wrow = g.ws + (int64_t)(n0 / QB) * nkb;
     auto scales_from = [&](int j) { return wrow[min(wave + SW * (j + lane), nkb - 1)]; };
@@ -94,23 +96,28 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
         __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * COPIES));
         __builtin_amdgcn_sched_barrier(0);
         const float w1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wsc), j & 63));
-        const i32x8 a = cat(*reinterpret_cast<const i32x4*>(at + f0), *reinterpret_cast<const i32x4*>(at + f1));
-        i32x8 x[MB];
+        i32x8 a[NB], x[MB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            a[i] = cat8(*reinterpret_cast<const i32x4*>(at + 2048 * i + f0), *reinterpret_cast<const i32x4*>(at + 2048 * i + f1));
         float sc[MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             const int8_t* p = at + W_BYTES + 2048 * i;
-            x[i] = cat(*reinterpret_cast<const i32x4*>(p + f0), *reinterpret_cast<const i32x4*>(p + f1));
+            x[i] = cat8(*reinterpret_cast<const i32x4*>(p + f0), *reinterpret_cast<const i32x4*>(p + f1));
             sc[i] = *reinterpret_cast<const float*>(at + W_BYTES + X_BYTES + 4 * (16 * i + r));
         }
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            const f32x4 zero{0, 0, 0, 0};
-            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x[i], zero, 0, 0, 0, 0, 0, 0);
             const float s = sc[i] * w1;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][e] = fmaf(s, p[e], acc[i][e]);
+            for (int n = 0; n < NB; ++n) {
+                const f32x4 zero{0, 0, 0, 0};
+                const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[n], x[i], zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[n][i][e] = fmaf(s, p[e], acc[n][i][e]);
+            }
         }
         // the slot's reads are done before it is filled again
         __builtin_amdgcn_s_waitcnt(WAIT_LDS);
@@ -121,17 +128,19 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
     __syncthreads();
     f32x4* red = reinterpret_cast<f32x4*>(smem);
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-        red[(wave * MB + i) * 64 + lane] = acc[i];
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            red[(wave * NB * MB + j * MB + i) * 64 + lane] = acc[j][i];
     __syncthreads();
     using OutT = typename std::conditional<YF16, _Float16, float>::type;
     using Out4 = OutT __attribute__((ext_vector_type(4)));
-    for (int i = wave; i < MB; i += SW) {
-        f32x4 t = red[i * 64 + lane];
+    for (int b = wave; b < NB * MB; b += SW) {
+        f32x4 t = red[b * 64 + lane];
 #pragma unroll
         for (int w = 1; w < SW; ++w)
-            t += red[(w * MB + i) * 64 + lane];
-        const int m = m0 + 16 * i + r, n = n0 + 4 * q;
+            t += red[(w * NB * MB + b) * 64 + lane];
+        const int m = m0 + 16 * (b % MB) + r, n = n0 + 16 * (b / MB) + 4 * q;
         if (m >= g.rows)
             continue;
         Out4 o;
@@ -151,37 +160,152 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
     }
 }
 
+// Many rows: the tiles of gemm_w8a8_tile.h with block scales, 256 x 192 first and then, on the columns
+// they leave, 128 x BNS. Workgroup b takes big tile b and then small tile b.
+struct BlockPlan {
+    int tiles_m_big, nbig, tiles_m_small, nsmall, n_small0;
+};
+
+template <int YMODE, int BNS>
+__global__ __launch_bounds__(64 * NWAVES, 1) void gemm_block_tile_kernel(BlockGemm g, BlockPlan plan) {
+    __shared__ __attribute__((aligned(1024))) int8_t smem[RING_BYTES + SCALE_BYTES];
+    const int bid = blockIdx.x, M = (int)g.M;
+    const int8_t* A = reinterpret_cast<const int8_t*>(g.xq);
+    const int8_t* B = reinterpret_cast<const int8_t*>(g.wq);
+    const EpiArgs none{nullptr, nullptr, nullptr, 0};
+    if (bid < plan.nbig) {
+        const int tile = xcd_remap(bid, plan.nbig);
+        const int tn = tile / plan.tiles_m_big, tm = tile - tn * plan.tiles_m_big;
+        gemm_tile_pp<256, 192, YMODE, EL_E4M3_BLOCK>(A, g.xs, B, g.ws, g.bias, g.y, M, g.N, g.K, tm * 256, tn * 192, g.act,
+                                                     none, smem);
+        if (bid >= plan.nsmall)
+            return;
+        __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the epilogue has read all it needs from LDS
+        barrier_no_fence();
+    }
+    if (bid < plan.nsmall) {
+        const int tile = xcd_remap(bid, plan.nsmall);
+        const int tn = tile / plan.tiles_m_small, tm = tile - tn * plan.tiles_m_small;
+        gemm_tile_ks<BNS, YMODE, EL_E4M3_BLOCK>(A, g.xs, B, g.ws, g.bias, g.y, M, g.N, g.K, tm * 128,
+                                                plan.n_small0 + tn * BNS, g.act, none, smem);
+    }
+}
+
+// The kernels to choose from: few-row kernels with NB x 16 columns and MB x 16 rows a workgroup, and
+// tiles. A call takes rounds of as many workgroups as the chip holds at once, each about a + b * blocks
+// of K us long; the least product is chosen. a and b are fits to warm times on MI355X of 60 shapes
+// (M 64-1024, N 1024-14336, K 1024-11008) and of M 1-64 from cold memory; the choices among them are within 5%
+// of the best. Some of both sides, us (chosen first):
+//   1 x 11008 x 4096     2x1 12.0, 1x1 14.1 (cold)     64 x 4096 x 4096    2x2 8.0, 1x2 11.3, 128x128 18.3
+//   32 x 11008 x 4096    4x2 12.7, 1x2 15.8            128 x 4096 x 4096   2x4 10.4, 4x4 15.3, 128x128 18.2
+//   96 x 11008 x 4096    128x128 19.1, 2x4 28.0        256 x 4096 x 4096   4x4 15.0, 128x128 18.3
+//   333 x 11008 x 4096   128x192 27.4, 128x128 37.9    1024 x 11008 x 4096 256x192 45, 128x192 57, 128x128 63
+struct Choice {
+    int nb, mb, waves, slots;   // few-row kernels; 0: tiles
+    int rows, cols;             // of a workgroup
+    int per_cu;
+    float a, b;
+};
+constexpr Choice CHOICES[] = {
+    {1, 1, 8, 2, 16, 16, 2, 1.4f, 0.13f},  {2, 1, 4, 3, 16, 32, 2, 2.0f, 0.20f},   {1, 2, 8, 2, 32, 16, 1, 1.8f, 0.12f},
+    {2, 2, 8, 2, 32, 32, 1, 3.1f, 0.152f}, {4, 2, 4, 3, 32, 64, 1, 3.8f, 0.224f},  {2, 4, 4, 2, 64, 32, 1, 3.45f, 0.217f},
+    {4, 4, 4, 2, 64, 64, 1, 5.0f, 0.311f}, {0, 0, 0, 0, 128, 128, 1, 5.0f, 0.56f}, {0, 0, 0, 0, 128, 192, 1, 7.4f, 0.65f},
+    {0, 0, 0, 0, 256, 192, 1, 7.0f, 1.0f},
+};
+constexpr int FEW = 7, SMALL128 = 7, SMALL192 = 8, BIG = 9, MIXED = 10;
+
+struct Chosen {
+    int kernel;       // index into CHOICES; MIXED: whole rounds of big tiles, then 128 x 192
+    int big_panels;   // columns of big tiles
+};
+
+Chosen choose(int64_t M, int64_t N, int64_t K) {
+    const int64_t kb = e4m3_blocks(K);
+    const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const auto tiles = [&](const Choice& c, int64_t n) { return cdiv(M, c.rows) * cdiv(n, c.cols); };
+    const auto cost = [&](const Choice& c, int64_t wgs) { return (float)cdiv(wgs, c.per_cu * cu_count()) * (c.a + c.b * kb); };
+    Chosen best{0, 0};
+    float least = cost(CHOICES[0], tiles(CHOICES[0], N));
+    for (int i = 1; i <= BIG; ++i) {
+        if (i < FEW && CHOICES[i].rows > 16 && CHOICES[i].rows >= 2 * cdiv(M, 16) * 16)
+            continue;   // half of its rows or more would be empty
+        const float t = cost(CHOICES[i], tiles(CHOICES[i], N));
+        if (t < least) {
+            least = t;
+            best.kernel = i;
+        }
+    }
+    // whole rounds of big tiles, and small ones for the columns that would make a last, short round
+    const int64_t big = tiles(CHOICES[BIG], N), panels = big / cu_count() * cu_count() / cdiv(M, 256);
+    if (best.kernel == BIG && panels > 0 && panels < cdiv(N, 192)) {
+        const float t = cost(CHOICES[BIG], panels * cdiv(M, 256)) + cost(CHOICES[SMALL192], tiles(CHOICES[SMALL192], N - panels * 192));
+        if (t < least)
+            best = {MIXED, (int)panels};
+    }
+    if (best.kernel == BIG)
+        best.big_panels = (int)cdiv(N, 192);
+    return best;
+}
+
 template <bool YF16>
-void launch_few(const BlockGemm& g, hipStream_t stream) {
-    const uint32_t nx = (uint32_t)((g.N + 15) / 16);
-    // rows in launches whose grid stays within 65535 in y
-    auto go = [&](auto kernel, int sw, int rows) {
-        const int64_t most = (int64_t)rows * 65535;
+void launch_few(const BlockGemm& g, int c, hipStream_t stream) {
+    auto go = [&](auto kernel) {
+        const Choice& k = CHOICES[c];
+        // rows in launches whose grid stays within 65535 in y
+        const int64_t most = (int64_t)k.rows * 65535;
         for (int64_t m = 0; m < g.M; m += most) {
             BlockGemm p = g;
             p.xq += m * g.K;
             p.xs += m;
             p.y = reinterpret_cast<int8_t*>(g.y) + m * g.N * (YF16 ? 2 : 4);
             p.rows = (int)(g.M - m < most ? g.M - m : most);
-            kernel<<<dim3(nx, (uint32_t)((p.rows + rows - 1) / rows)), dim3(64 * sw), 0, stream>>>(p);
+            kernel<<<dim3((uint32_t)((g.N + k.cols - 1) / k.cols), (uint32_t)((p.rows + k.rows - 1) / k.rows)),
+                     dim3(64 * k.waves), 0, stream>>>(p);
         }
     };
-    if (g.M <= 16)
-        go(gemm_block_few_kernel<1, 8, 4, YF16>, 8, 16);
+    auto of = [&](auto i) {
+        constexpr Choice k = CHOICES[decltype(i)::value];
+        if (c == decltype(i)::value)
+            go(gemm_block_few_kernel<k.nb, k.mb, k.waves, k.slots, YF16>);
+    };
+    of(std::integral_constant<int, 0>{});
+    of(std::integral_constant<int, 1>{});
+    of(std::integral_constant<int, 2>{});
+    of(std::integral_constant<int, 3>{});
+    of(std::integral_constant<int, 4>{});
+    of(std::integral_constant<int, 5>{});
+    of(std::integral_constant<int, 6>{});
+}
+
+template <int YMODE>
+void launch_tiles(const BlockGemm& g, const Chosen& c, hipStream_t stream) {
+    const int64_t small = c.kernel == SMALL128 ? 128 : 192;
+    BlockPlan p{};
+    p.tiles_m_big = (int)((g.M + 255) / 256);
+    p.tiles_m_small = (int)((g.M + 127) / 128);
+    p.nbig = p.tiles_m_big * c.big_panels;
+    p.n_small0 = c.big_panels * 192;
+    p.nsmall = g.N <= p.n_small0 ? 0 : (int)(p.tiles_m_small * ((g.N - p.n_small0 + small - 1) / small));
+    const dim3 grid((uint32_t)(p.nbig > p.nsmall ? p.nbig : p.nsmall)), nt(64 * NWAVES);
+    if (small == 128)
+        gemm_block_tile_kernel<YMODE, 128><<<grid, nt, 0, stream>>>(g, p);
     else
-        go(gemm_block_few_kernel<2, 8, 3, YF16>, 8, 32);
+        gemm_block_tile_kernel<YMODE, 192><<<grid, nt, 0, stream>>>(g, p);
 }
 
 }  // namespace
+
+extern "C" int ql_gemm_e4m3_block_kernel(int64_t M, int64_t N, int64_t K) { return choose(M, N, K).kernel; }
 
 ql_status launch_gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t* wq, const float* w_scale,
                                  const float* bias, int act, void* y, bool y_f16, int64_t M, int64_t N, int64_t K,
                                  hipStream_t stream) {
     const BlockGemm g{xq, x_scale, wq, w_scale, bias, y, 0, (int)N, (int)K, act, M};
-    if (y_f16)
-        launch_few<true>(g, stream);
+    const Chosen c = choose(M, N, K);
+    if (c.kernel < FEW)
+        (y_f16 ? launch_few<true> : launch_few<false>)(g, c.kernel, stream);
     else
-        launch_few<false>(g, stream);
+        (y_f16 ? launch_tiles<Y_F16> : launch_tiles<Y_F32>)(g, c, stream);
     return launch_status();
 }
 

@@ -1,0 +1,38 @@
+"""Which kernel gemm_e4m3_block takes for the sizes of the GPU tests: every one is reached, at full and at
+ragged tiles (the library's own rule is asked; no compute call is made here)."""
+import ctypes
+import os
+
+import pytest
+
+from block_shapes import LARGE, SHAPES
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "int8_quantized_linear_amd", "libql.so")
+# rows and columns of a workgroup of each kernel, the last one a mix of the two before
+TILES = [(16, 16), (16, 32), (32, 16), (32, 32), (32, 64), (64, 32), (64, 64), (128, 128), (128, 192), (256, 192), (256, 192)]
+
+
+@pytest.fixture(scope="module")
+def kernel():
+    if not os.path.exists(LIB):
+        pytest.skip("libql.so not built")
+    f = ctypes.CDLL(LIB).ql_gemm_e4m3_block_kernel
+    f.argtypes = [ctypes.c_int64] * 3
+    return f
+
+
+def test_every_kernel_is_reached(kernel):
+    seen = {}
+    for M, N, K in SHAPES + LARGE:
+        k = kernel(M, N, K)
+        r, c = TILES[k]
+        seen.setdefault(k, set()).add((M % r != 0, N % c != 0, K % 128 != 0))
+    assert sorted(seen) == list(range(len(TILES)))
+    for k, kinds in seen.items():
+        assert any(a for a, _, _ in kinds) and any(b for _, b, _ in kinds) and any(c for _, _, c in kinds), (k, kinds)
+
+
+def test_largest_sizes(kernel):
+    for s in ((1, 1, 64), ((1 << 31) - 1, 1, 64), (1, 1 << 23, 64), (2 ** 14, 1 << 23, 131008), ((1 << 31) - 1, 64, 64)):
+        assert 0 <= kernel(*s) < len(TILES)

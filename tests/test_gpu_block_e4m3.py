@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import block_ref as ref
+from block_shapes import LARGE, SHAPES
 from gpu_util import Guarded, dev, host
 
 pytestmark = pytest.mark.gpu
@@ -98,11 +99,6 @@ def _check(ql, ops, act, f16, with_bias, sample=None):
     assert (diff <= tol).all(), "%d outside, worst %g of its tolerance" % ((diff > tol).sum(), (diff / tol).max())
 
 
-SHAPES = [(1, 16, 64), (1, 64, 128), (2, 33, 192), (5, 130, 4096), (16, 256, 2112), (17, 129, 640), (33, 272, 1088),
-          (64, 144, 832), (65, 384, 320), (100, 1001, 256), (129, 300, 448), (200, 260, 1024), (257, 513, 576),
-          (300, 70, 2176)]
-
-
 @pytest.mark.parametrize("f16", [True, False])
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_gemm(ql, M, N, K, f16):
@@ -117,9 +113,7 @@ def test_gemm_activation(ql, M, N, K, act, f16):
     _check(ql, _operands(7, M, N, K, 2.0 ** -16), act, f16, True)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 11008, 4096), (32, 4096, 11008), (8, 12345, 2048), (130, 14336, 1024),
-                                   (333, 4001, 2112), (512, 4096, 4096), (700, 6000, 1024), (1111, 11008, 512),
-                                   (2048, 4096, 1024), (2048, 11008, 640), (4100, 2111, 256)])
+@pytest.mark.parametrize("M,N,K", LARGE)
 def test_gemm_sampled(ql, M, N, K):
     """Large products on a sample of rows and columns, the edges of every tile size among them."""
     rng = np.random.default_rng(M)
