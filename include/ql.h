@@ -539,7 +539,7 @@ ql_status moe_e4m3_block(const void* x, const float* logits, const uint8_t* w13,
                          const uint8_t* w2, const float* s2, void* out, ql_dtype out_dtype, int64_t T,
                          int64_t E, int64_t top_k, int64_t K, int64_t I, int renormalize, void* workspace,
                          int64_t workspace_bytes, void* stream);
-ql_status moe_e4m3_block_workspace_bytes(int64_t T, int64_t top_k, int64_t I, int64_t* bytes);
+ql_status moe_e4m3_block_workspace_bytes(int64_t T, int64_t top_k, int64_t K, int64_t I, int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -80,7 +80,7 @@ _SIGS = {
     "gemm_e4m3_block": [_P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P],
     "moe_router": [_P, _P, _P, _I64, _I64, _I64, _P],
     "moe_e4m3_block": [_P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P],
-    "moe_e4m3_block_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(_I64)],
+    "moe_e4m3_block_workspace_bytes": [_I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
     "attention_kv4_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
 }
 for _name, _args in _SIGS.items():
@@ -724,9 +724,9 @@ def moe_router(x, w, logits=None):
 
 
 @functools.lru_cache(maxsize=1024)
-def _moe_workspace(T, top_k, I):
+def _moe_workspace(T, top_k, K, I):
     need = _I64(0)
-    _call("moe_e4m3_block_workspace_bytes", T, top_k, I, ctypes.byref(need))
+    _call("moe_e4m3_block_workspace_bytes", T, top_k, K, I, ctypes.byref(need))
     return need.value
 
 
@@ -760,7 +760,7 @@ def moe_e4m3_block(x, logits, w13, s13, w2, s2, top_k: int, renormalize: bool = 
         op = out.data_ptr()
     else:
         op = _same(out, "out", out_dtype, (T, K), index)
-    need = _moe_workspace(T, top_k, I)
+    need = _moe_workspace(T, top_k, K, I)
     ws = w13.new_empty((need,), dtype=torch.uint8)   # of the current stream, as the kernels are
     _status("moe_e4m3_block", lib.moe_e4m3_block(
         xp, lp, wp, sp, vp, tp, op, QL_F16 if out_dtype is torch.float16 else QL_F32, T, E, top_k, K, I,

@@ -594,16 +594,17 @@ ql_status moe_router(const void* x, const void* w, float* logits, int64_t T, int
     return ql::launch_moe_router(x, w, logits, T, E, K, as_stream(stream));
 }
 
-static bool bad_moe(int64_t T, int64_t top_k, int64_t I) {
-    return T < 0 || T >= kMaxDim || top_k < 1 || top_k > ql::MOE_TOP_K || I < 1 || I % 64 != 0 || I > kMaxKw8a8;
+static bool bad_moe(int64_t T, int64_t top_k, int64_t K, int64_t I) {
+    return T < 0 || T >= kMaxDim || top_k < 1 || top_k > ql::MOE_TOP_K || K < 1 || K % 64 != 0 || K > kMaxKw8a8 || I < 1 ||
+           I % 64 != 0 || I > kMaxKw8a8;
 }
 
-ql_status moe_e4m3_block_workspace_bytes(int64_t T, int64_t top_k, int64_t I, int64_t* bytes) {
-    if (bad_moe(T, top_k, I))
+ql_status moe_e4m3_block_workspace_bytes(int64_t T, int64_t top_k, int64_t K, int64_t I, int64_t* bytes) {
+    if (bad_moe(T, top_k, K, I))
         return QL_ERR_SHAPE;
     if (!bytes)
         return QL_ERR_NULL;
-    *bytes = T == 0 ? 0 : ql::moe_workspace(T, (int)top_k, (int)I);
+    *bytes = T == 0 ? 0 : ql::moe_workspace(T, (int)top_k, (int)K, (int)I);
     return QL_OK;
 }
 
@@ -613,11 +614,11 @@ ql_status moe_e4m3_block(const void* x, const float* logits, const uint8_t* w13,
                          int64_t workspace_bytes, void* stream) {
     if (out_dtype != QL_F32 && out_dtype != QL_F16)
         return QL_ERR_DTYPE;
-    if (bad_moe(T, top_k, I) || E < top_k || E > ql::MOE_EXPERTS || K < 1 || K % 64 != 0 || K > kMaxKw8a8)
+    if (bad_moe(T, top_k, K, I) || E < top_k || E > ql::MOE_EXPERTS)
         return QL_ERR_SHAPE;
     if (T == 0)
         return QL_OK;
-    if (workspace_bytes < ql::moe_workspace(T, (int)top_k, (int)I))
+    if (workspace_bytes < ql::moe_workspace(T, (int)top_k, (int)K, (int)I))
         return QL_ERR_SHAPE;
     if (!x || !logits || !w13 || !s13 || !w2 || !s2 || !out || !workspace)
         return QL_ERR_NULL;

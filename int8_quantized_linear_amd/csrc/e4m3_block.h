@@ -80,7 +80,7 @@ struct MoeLayer {
 constexpr int MOE_TOKENS = 64;     // of a launch
 constexpr int MOE_EXPERTS = 512;   // at most
 constexpr int MOE_TOP_K = 16;      // at most
-int64_t moe_workspace(int64_t T, int top_k, int I);
+int64_t moe_workspace(int64_t T, int top_k, int K, int I);
 ql_status launch_moe_router(const void* x, const void* w, float* logits, int64_t T, int64_t E, int64_t K,
                             hipStream_t stream);
 ql_status launch_moe_e4m3_block(const MoeLayer& l, hipStream_t stream);

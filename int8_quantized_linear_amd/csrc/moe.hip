@@ -12,9 +12,9 @@
 // scale is applied in fp32. h is kept as two bf16 terms (16 bits of significand, fp32's range): one
 // rounding of relative size 2^-17 that its products see.
 //
-// A wave reads codes through its own ring in LDS, copied there directly and several blocks ahead;
-// the other operand's few rows come from L2 into registers, as far ahead. The order of every sum is
-// fixed, whatever the other tokens are.
+// A wave copies the blocks of 128 that it takes, codes and the other operand's rows, straight into its
+// own ring in LDS, one block ahead, and needs no barrier until the waves' sums are joined. The order of
+// every sum is fixed, whatever the other tokens are.
 #include "e4m3_block.h"
 
 namespace ql {
@@ -85,35 +85,48 @@ __global__ __launch_bounds__(RW* WAVE) void moe_router_kernel(const _Float16* __
 //
 // Every workgroup of the first kernel works the routes out for itself from the logits (it would
 // wait as long for another to do it). Pairs (expert, token) are numbered expert by expert, tokens
-// in order.
+// in order, and cut into units of one expert and up to 16 pairs, the columns of a matrix instruction.
 
-struct Routes {
-    unsigned long long tokens[MOE_EXPERTS];   // bit t: token t takes the expert
-    uint16_t base[MOE_EXPERTS];               // first pair of an expert
-    uint16_t act[MOE_EXPERTS];                // experts that some token takes
-    uint16_t id[MOE_TOKENS][MOE_TOP_K];       // of a token, MOE_EXPERTS for none
-    float p[MOE_TOKENS][MOE_TOP_K];
-    float pair_p[MOE_TOKENS * MOE_TOP_K];
-    uint16_t pair_token[MOE_TOKENS * MOE_TOP_K];
-    uint32_t part[NW];
-    int nact;
+constexpr int MOE_PAIRS = MOE_TOKENS * MOE_TOP_K;
+constexpr int MOE_UNITS = MOE_EXPERTS + MOE_PAIRS / 16;   // at most: all experts, each with a last, short unit
+
+struct alignas(8) MoeUnit {
+    uint16_t expert, base, count, pad;   // its first pair, its pairs
 };
 
-// The workspace: the routes as the second kernel needs them, then h's two terms, [pairs][I] each.
+struct Routes {
+    MoeUnit units[MOE_UNITS];
+    float pair_p[MOE_PAIRS];
+    uint8_t pair_token[MOE_PAIRS];
+    int nunits;
+};
+// what only make_routes needs
+struct RouteScratch {
+    unsigned long long tokens[MOE_EXPERTS];   // bit t: token t takes the expert
+    uint16_t base[MOE_EXPERTS];               // first pair of an expert
+    uint16_t id[MOE_TOKENS][MOE_TOP_K];       // of a token, MOE_EXPERTS for none
+    float p[MOE_TOKENS][MOE_TOP_K];
+    uint32_t part[8];
+};
+
+// The workspace: the routes as the second kernel needs them, arrivals at each slice of output columns,
+// h's terms ([pairs][I] each), and the parts' sums of the output.
+constexpr int MOE_SLICES = 131072 / 32;
 struct MoeSpace {
-    int nact;
+    int nunits;
     int pad[3];
-    struct {
-        uint16_t expert, base, count, pad;
-    } act[MOE_EXPERTS];
-    uint16_t pair_token[MOE_TOKENS * MOE_TOP_K];
+    MoeUnit units[MOE_UNITS];
+    uint8_t pair_token[MOE_PAIRS];
+    uint32_t arrived[MOE_SLICES];
 };
 
 struct Moe {
     MoeLayer l;
     int T;           // tokens of this launch
+    int parts;       // workgroups that share a slice of output columns in the second kernel
     MoeSpace* space;
-    __bf16 *hi, *lo;
+    __bf16* h;       // TERMS planes
+    float* sums;     // [parts][T][K]
 };
 
 template <class F>
@@ -142,10 +155,9 @@ __device__ inline int row16_min(int v) {
 // 16 lanes a token, R logits a lane: top_k rounds of the largest that is left. NaN is never taken,
 // nor is -infinity.
 template <int R>
-__device__ inline void make_routes(Routes& rt, const Moe& g) {
+__device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
     const int tid = threadIdx.x, E = g.l.E, k = g.l.top_k;
-    for (int e = tid; e < MOE_EXPERTS; e += NT)
-        rt.tokens[e] = 0;
+    rs.tokens[tid] = 0;
     __syncthreads();
     const int l = tid & 15;
     for (int t0 = 0; t0 < g.T; t0 += NT / 16) {
@@ -161,10 +173,12 @@ __device__ inline void make_routes(Routes& rt, const Moe& g) {
         top = row16(top, [](float a, float b) { return fmaxf(a, b); });
         const float from = top == -INFINITY ? 0.0f : top;
         float all = 0.0f;
+        if (!g.l.renormalize) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            all += v[r] == v[r] ? __expf(v[r] - from) : 0.0f;
-        all = row16(all, [](float a, float b) { return a + b; });
+            for (int r = 0; r < R; ++r)
+                all += v[r] == v[r] ? __expf(v[r] - from) : 0.0f;
+            all = row16(all, [](float a, float b) { return a + b; });
+        }
         float chosen = 0.0f, mine = 0.0f;
         int my_id = MOE_EXPERTS;
         for (int j = 0; j < k; ++j) {
@@ -190,17 +204,18 @@ __device__ inline void make_routes(Routes& rt, const Moe& g) {
                 v[r] = 16 * r + l == at ? -INFINITY : v[r];
         }
         if (t < g.T && l < k) {
-            rt.id[t][l] = (uint16_t)my_id;
-            rt.p[t][l] = mine / (g.l.renormalize ? chosen : all);
+            rs.id[t][l] = (uint16_t)my_id;
+            rs.p[t][l] = mine / (g.l.renormalize ? chosen : all);
             if (my_id < MOE_EXPERTS)
-                atomicOr(&rt.tokens[my_id], 1ull << t);
+                atomicOr(&rs.tokens[my_id], 1ull << t);
         }
     }
     __syncthreads();
-    // experts in use, and their first pairs: a running sum over the experts, one a thread
+    // the experts' first pairs and units: a running sum over the experts, one a thread
     static_assert(NT == MOE_EXPERTS, "one expert a thread");
-    const unsigned long long m = rt.tokens[tid];
-    const uint32_t own = (uint32_t)__popcll(m) << 16 | (m != 0);
+    const unsigned long long m = rs.tokens[tid];
+    const int pairs = __popcll(m);
+    const uint32_t own = (uint32_t)pairs << 16 | (uint32_t)((pairs + 15) / 16);
     uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < WAVE; o <<= 1) {
@@ -208,26 +223,26 @@ __device__ inline void make_routes(Routes& rt, const Moe& g) {
         sum += (tid & 63) >= o ? up : 0;
     }
     if ((tid & 63) == 63)
-        rt.part[tid >> 6] = sum;
+        rs.part[tid >> 6] = sum;
     __syncthreads();
     sum -= own;
     uint32_t total = 0;
     for (int w = 0; w < NW; ++w) {
-        total += rt.part[w];
-        sum += w < tid >> 6 ? rt.part[w] : 0;
+        total += rs.part[w];
+        sum += w < tid >> 6 ? rs.part[w] : 0;
     }
-    rt.base[tid] = (uint16_t)(sum >> 16);
-    if (m != 0)
-        rt.act[sum & 0xFFFF] = (uint16_t)tid;
+    rs.base[tid] = (uint16_t)(sum >> 16);
+    for (int i = 0; 16 * i < pairs; ++i)
+        rt.units[(sum & 0xFFFF) + i] = {(uint16_t)tid, (uint16_t)((sum >> 16) + 16 * i), (uint16_t)min(16, pairs - 16 * i), 0};
     if (tid == 0)
-        rt.nact = (int)(total & 0xFFFF);
+        rt.nunits = (int)(total & 0xFFFF);
     __syncthreads();
     for (int i = tid; i < g.T * k; i += NT) {
-        const int t = i / k, e = rt.id[t][i % k];
+        const int t = i / k, e = rs.id[t][i % k];
         if (e < MOE_EXPERTS) {
-            const int at = rt.base[e] + __popcll(rt.tokens[e] & ((1ull << t) - 1));
-            rt.pair_token[at] = (uint16_t)t;
-            rt.pair_p[at] = rt.p[t][i % k];
+            const int at = rs.base[e] + __popcll(rs.tokens[e] & ((1ull << t) - 1));
+            rt.pair_token[at] = (uint8_t)t;
+            rt.pair_p[at] = rs.p[t][i % k];
         }
     }
     __syncthreads();
@@ -250,46 +265,70 @@ __device__ inline bf16x8 codes_bf16(int w0, int w1) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Copies of 16 rows of 256 bytes (128 values of 16 bits) into LDS, four rows each: chunk c (16 bytes)
+// of row r lies at chunk position c ^ r, so that the 16 rows of a fragment read fall into distinct
+// banks. rows[i] is the byte offset of the lane's row in copy i, or out of range; `left` values are
+// left of K at this block, the rest comes as zeros.
+__device__ inline void copy_rows16(__amdgpu_buffer_rsrc_t from, const int (&rows)[4], int at, int left, int lane, int8_t* to) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = (lane & 15) ^ (4 * i + (lane >> 4));
+        buffer_to_lds16(from, (rows[i] + at + 16 * c) | (8 * c < left ? 0 : 0x40000000), 0, to + 1024 * i);
+    }
+}
+
+// Fragment f of four of such rows, with the k order in which codes_* takes a row of codes.
+template <class V>
+__device__ inline V rows16_fragment(const int8_t* from, int r, int q, int f) {
+    const int c = ((f >> 1) * 4 + q) * 2 + (f & 1);
+    return *reinterpret_cast<const V*>(from + r * 256 + ((c ^ r) << 4));
+}
+
 // ------------------------------------------------------------------------ the gated products
 //
-// A task is an expert in use and 16 columns of h: 16 rows of W1 and 16 of W3 against the expert's
-// tokens (TILES tiles of 16). A workgroup takes every gridDim-th task; its waves split K, wave w
-// taking the blocks w, w + 8, ... of every task. The wave's items (task, block) make one sequence, so
-// the next task's first copies are in flight while a task's sums are joined. W is the first
-// operand: a lane's sums belong to one token (lane & 15) and four columns of h.
+// A task is a unit and 16 columns of h: 16 rows of W1 and 16 of W3 against the unit's tokens. A
+// workgroup takes every gridDim-th task; its waves split K, wave w taking the blocks w, w + 8, ... of
+// every task. The wave's items (task, block) make one sequence, so the next task's first copies are in
+// flight while a task's sums are joined. W is the first operand: a lane's sums belong to one token
+// (lane & 15) and four columns of h.
 
-template <int TILES>
-constexpr int UP_DEPTH = TILES == 4 ? 2 : 3;
+constexpr int UP_SLOT = 4096 + 4096 + 256, UP_COPIES = 4 + 4 + 1;
 
-template <int TILES, int R>
+// (One LDS variable a kernel: with several the compiler tells the copies into them apart and waits for
+// those into the rings, all of them, before any read of a ring.)
+struct UpShared {
+    int8_t rings[NW * 2 * UP_SLOT];   // RouteScratch before the copies start
+    f32x4 red[NW][2][WAVE];
+    Routes rt;
+};
+
+template <int R, int TERMS>
 __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
-    constexpr int S = UP_DEPTH<TILES>, SLOT = 4096 + 256, BATCH = 5 + 4 * TILES;
-    __shared__ Routes rt;
-    __shared__ __attribute__((aligned(1024))) int8_t rings[NW * S * SLOT];
-    __shared__ f32x4 red[NW][TILES][2][WAVE];
-    make_routes<R>(rt, g);
+    __shared__ __attribute__((aligned(1024))) UpShared sh;
+    static_assert(sizeof(RouteScratch) <= sizeof(sh.rings), "the routes are made before the rings are used");
+    Routes& rt = sh.rt;
+    auto& red = sh.red;
+    make_routes<R>(rt, *reinterpret_cast<RouteScratch*>(sh.rings), g);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
-    const int K = g.l.K, I = g.l.I, nact = __builtin_amdgcn_readfirstlane(rt.nact);
+    const int K = g.l.K, I = g.l.I, nunits = __builtin_amdgcn_readfirstlane(rt.nunits);
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0)
-            g.space->nact = nact;
-        for (int i = threadIdx.x; i < nact; i += NT) {
-            const int e = rt.act[i];
-            g.space->act[i] = {(uint16_t)e, rt.base[e], (uint16_t)__popcll(rt.tokens[e]), 0};
-        }
+            g.space->nunits = nunits;
+        for (int i = threadIdx.x; i < nunits; i += NT)
+            g.space->units[i] = rt.units[i];
         for (int i = threadIdx.x; i < g.T * g.l.top_k; i += NT)
             g.space->pair_token[i] = rt.pair_token[i];
+        for (int i = threadIdx.x; i < K / 32; i += NT)
+            g.space->arrived[i] = 0;
     }
-    const int nkb = (K + QB - 1) / QB, cols = I / 16, tasks = nact * cols;
+    const int nkb = (K + QB - 1) / QB, cols = I / 16, tasks = nunits * cols;
     const int J = (nkb + NW - 1) / NW;                       // a wave's blocks of a task
     const int first = blockIdx.x, G = gridDim.x;
-    const int mine = first < tasks ? (tasks - first + G - 1) / G : 0;
-    const int items = mine * J;
-    if (items == 0)
+    if (first >= tasks)
         return;
 
-    int8_t* ring = rings + wave * S * SLOT;
+    int8_t* ring = sh.rings + wave * 2 * UP_SLOT;
     const int64_t blocks13 = e4m3_blocks(2 * (int64_t)I);
     const __amdgpu_buffer_rsrc_t rx = buffer_of(g.l.x, g.T * K * 2);
     const int row = lane >> 3, c0 = copy_chunk128(lane, 0), c1 = copy_chunk128(lane, 1);
@@ -300,179 +339,171 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
         int task, j;
         __amdgpu_buffer_rsrc_t gate, up;
         const float* scale;
-        int xoff[TILES];
+        int rows[4];
     } nx;
     auto enter = [&](int task) {
         nx.task = task;
         nx.j = 0;
-        const int a = min(task, tasks - 1);
-        const int e = __builtin_amdgcn_readfirstlane(rt.act[a / cols]), i0 = (a % cols) * 16;
+        const int a = min(task, tasks - 1), i0 = (a % cols) * 16;
+        const MoeUnit u = rt.units[a / cols];
+        const int e = __builtin_amdgcn_readfirstlane(u.expert);
         const int size = task < tasks ? 16 * K : 0;
         const uint8_t* w = g.l.w13 + ((int64_t)e * 2 * I + i0) * K;
         nx.gate = buffer_of(w, size);
         nx.up = buffer_of(w + (int64_t)I * K, size);
         nx.scale = g.l.s13 + (e * blocks13 + (i0 + (lane < 32 ? 0 : I)) / QB) * nkb;
-        const int base = rt.base[e], count = __popcll(rt.tokens[e]);
 #pragma unroll
-        for (int i = 0; i < TILES; ++i)   // columns past the tokens repeat the last one
-            nx.xoff[i] = (rt.pair_token[base + min(16 * i + r, count - 1)] * K + 16 * q) * 2;
+        for (int i = 0; i < 4; ++i) {
+            const int n = 4 * i + q;
+            nx.rows[i] = n < u.count ? rt.pair_token[u.base + n] * K * 2 : far;
+        }
     };
-    i32x4 xv[S][TILES][4];
-    auto fetch = [&](int slot, i32x4 (&x)[TILES][4]) {
-        int8_t* to = ring + slot * SLOT;
-        const int b = wave + NW * nx.j, left = K - b * QB;
+    auto fetch = [&](int slot) {
+        int8_t* to = ring + slot * UP_SLOT;
+        const int b = wave + NW * nx.j, left = K - b * QB;   // blocks past the end come as zeros
         const int cut0 = 16 * c0 < left ? 0 : far, cut1 = 16 * c1 < left ? 0 : far;
         const int o0 = row * K + 16 * c0 + b * QB, o1 = (row + 8) * K + 16 * c1 + b * QB;
         buffer_to_lds16<2>(nx.gate, o0 | cut0, 0, to);
         buffer_to_lds16<2>(nx.gate, o1 | cut1, 0, to + 1024);
         buffer_to_lds16<2>(nx.up, o0 | cut0, 0, to + 2048);
         buffer_to_lds16<2>(nx.up, o1 | cut1, 0, to + 3072);
-        global_to_lds4(nx.scale + min(b, nkb - 1), to + 4096);
-        // past K the codes are zeros, and x anything finite
-        const int bx = min(b, nkb - 1) * QB, half = left > 64 ? 128 : 0;
-#pragma unroll
-        for (int i = 0; i < TILES; ++i)
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-                x[i][f] = __builtin_amdgcn_raw_buffer_load_b128(rx, nx.xoff[i] + 16 * (f & 1) + (f >> 1) * half, 2 * bx, 0);
-        asm volatile("" ::: "memory");   // no load may sink past the waits that count it
+        copy_rows16(rx, nx.rows, 2 * b * QB, left, lane, to + 4096);
+        global_to_lds4(nx.scale + min(b, nkb - 1), to + 8192);
         if (++nx.j == J)
             enter(nx.task + G);
     };
 
-    f32x4 acc[TILES][2];
-    auto clear = [&]() {
-#pragma unroll
-        for (int i = 0; i < TILES; ++i)
-            acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    };
-    clear();
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
     enter(first);
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s)
-        fetch(s, xv[s]);
-    int task = first, j = 0;
+    fetch(0);
     const int f0 = r * QB + ((q ^ swizzle128(r)) << 4), f1 = r * QB + (((q + 4) ^ swizzle128(r)) << 4);
-    // in rounds of S items, the last one filled up with zeros (a branch out of the middle would make
-    // the compiler wait for all loads in every round)
-    for (int it = 0; it < items; it += S) {
-#pragma unroll
-        for (int u = 0; u < S; ++u) {
-            fetch((u + S - 1) % S, xv[(u + S - 1) % S]);
+    int slot = 0;
+    for (int task = first; task < tasks; task += G) {
+        for (int j = 0; j < J; ++j) {
+            fetch(slot ^ 1);
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * BATCH));
+            __builtin_amdgcn_s_waitcnt(wait_vm(UP_COPIES));
             __builtin_amdgcn_sched_barrier(0);
-            const int8_t* at = ring + u * SLOT;
+            const int8_t* at = ring + slot * UP_SLOT;
             const i32x4 g0 = *reinterpret_cast<const i32x4*>(at + f0), g1 = *reinterpret_cast<const i32x4*>(at + f1);
             const i32x4 u0 = *reinterpret_cast<const i32x4*>(at + 2048 + f0);
             const i32x4 u1 = *reinterpret_cast<const i32x4*>(at + 2048 + f1);
-            const float sg = *reinterpret_cast<const float*>(at + 4096);
-            const float su = *reinterpret_cast<const float*>(at + 4096 + 128);
+            const float sg = *reinterpret_cast<const float*>(at + 8192);
+            const float su = *reinterpret_cast<const float*>(at + 8192 + 128);
+            f16x8 x[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                x[f] = rows16_fragment<f16x8>(at + 4096, r, q, f);
             const f16x8 ga[4] = {codes_f16(g0[0], g0[1]), codes_f16(g0[2], g0[3]), codes_f16(g1[0], g1[1]), codes_f16(g1[2], g1[3])};
             const f16x8 ua[4] = {codes_f16(u0[0], u0[1]), codes_f16(u0[2], u0[3]), codes_f16(u1[0], u1[1]), codes_f16(u1[2], u1[3])};
+            f32x4 pg{0, 0, 0, 0}, pu{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                f32x4 pg{0, 0, 0, 0}, pu{0, 0, 0, 0};
+            for (int f = 0; f < 4; ++f) {
+                pg = __builtin_amdgcn_mfma_f32_16x16x32_f16(ga[f], x[f], pg, 0, 0, 0);
+                pu = __builtin_amdgcn_mfma_f32_16x16x32_f16(ua[f], x[f], pu, 0, 0, 0);
+            }
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const f16x8 b = __builtin_bit_cast(f16x8, xv[u][i][f]);
-                    pg = __builtin_amdgcn_mfma_f32_16x16x32_f16(ga[f], b, pg, 0, 0, 0);
-                    pu = __builtin_amdgcn_mfma_f32_16x16x32_f16(ua[f], b, pu, 0, 0, 0);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    acc[i][0][e] = fmaf(sg, pg[e], acc[i][0][e]);
-                    acc[i][1][e] = fmaf(su, pu[e], acc[i][1][e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                acc[0][e] = fmaf(sg, pg[e], acc[0][e]);
+                acc[1][e] = fmaf(su, pu[e], acc[1][e]);
             }
             __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the slot's reads are done before it is filled again
             __builtin_amdgcn_sched_barrier(0);
-            if (++j == J && task < tasks) {
-                // the task's sums of all waves, joined by one wave a tile
+            slot ^= 1;
+        }
+        // the task's sums of all waves, joined by wave 0
+        red[wave][0][lane] = acc[0];
+        red[wave][1][lane] = acc[1];
+        acc[0] = acc[1] = f32x4{0, 0, 0, 0};
+        barrier_lds();
+        if (wave == 0) {
+            const MoeUnit u = rt.units[task / cols];
+            f32x4 gs = red[0][0][lane], us = red[0][1][lane];
 #pragma unroll
-                for (int i = 0; i < TILES; ++i) {
-                    red[wave][i][0][lane] = acc[i][0];
-                    red[wave][i][1][lane] = acc[i][1];
-                }
-                clear();
-                barrier_lds();
-                const int e = rt.act[task / cols], i0 = (task % cols) * 16;
-                const int pair = 16 * wave + r, count = __popcll(rt.tokens[e]);
-                if (wave < TILES && 16 * wave < count) {
-                    f32x4 gs = red[0][wave][0][lane], us = red[0][wave][1][lane];
+            for (int w = 1; w < NW; ++w) {
+                gs += red[w][0][lane];
+                us += red[w][1][lane];
+            }
+            if (r < u.count) {
+                const float p = rt.pair_p[u.base + r];
+                const int64_t to = (int64_t)(u.base + r) * I + (task % cols) * 16 + 4 * q;
+                float h[4];
 #pragma unroll
-                    for (int w = 1; w < NW; ++w) {
-                        gs += red[w][wave][0][lane];
-                        us += red[w][wave][1][lane];
+                for (int n = 0; n < 4; ++n)
+                    h[n] = p * activation<ACT_SILU>(gs[n]) * us[n];
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k) {
+                    bf16x4 v;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        v[n] = (__bf16)h[n];
+                        h[n] -= (float)v[n];
                     }
-                    if (pair < count) {
-                        const int at_pair = rt.base[e] + pair;
-                        const float p = rt.pair_p[at_pair];
-                        bf16x4 hi, lo;
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            const float h = p * activation<ACT_SILU>(gs[n]) * us[n];
-                            hi[n] = (__bf16)h;
-                            lo[n] = (__bf16)(h - (float)hi[n]);
-                        }
-                        const int64_t to = (int64_t)at_pair * I + i0 + 4 * q;
-                        *reinterpret_cast<bf16x4*>(g.hi + to) = hi;
-                        *reinterpret_cast<bf16x4*>(g.lo + to) = lo;
-                    }
+                    *reinterpret_cast<bf16x4*>(g.h + (int64_t)k * g.T * g.l.top_k * I + to) = v;
                 }
-                barrier_lds();
-                j = 0;
-                task += G;
             }
         }
+        barrier_lds();
     }
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
 }
 
 // --------------------------------------------------------------------- the sums over experts
 //
-// A workgroup owns 16 columns of the output. Block b of expert e is wave (e * blocks + b) % 8's: a
-// wave's blocks of an expert lie 8 apart (neighbouring waves read neighbouring 128 bytes), the waves
-// have about as many blocks each, and which wave adds what to a token's sums does not depend on the
-// other tokens' experts. A wave adds an expert's products to its own sums [token][16] in LDS, and the
-// waves' sums are added at the end.
+// A workgroup owns 32 columns of the output and one of `parts` shares of I. Block b of expert e is
+// number (e * blocks + b) % (parts * 4)'s, part by part and wave by wave: neighbouring waves read
+// neighbouring 128 bytes, all have about as many blocks, and who adds what to a token's sums does not
+// depend on the other tokens' experts. A wave adds a unit's products to its own sums [token][32] in LDS;
+// the waves' sums are added at the end, and the parts' by the workgroup that comes last.
 
-template <int TILES>
-__global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
-    constexpr int S = TILES == 1 ? 4 : 3, SLOT = 2048 + 256, TOK = 16 * TILES;
-    constexpr int BATCH = 3 + 8;
-    __shared__ __attribute__((aligned(1024))) int8_t rings[NW * S * SLOT];
-    __shared__ float sums[NW][TOK][16];
-    __shared__ __attribute__((aligned(8))) uint16_t act[MOE_EXPERTS][4];   // expert, first pair, pairs
-    __shared__ __attribute__((aligned(4))) uint16_t pair_token[TOK * MOE_TOP_K];
+constexpr int DOWN_WAVES = 4, DOWN_COLS = 32;
+
+template <int TERMS, int TOKENS>
+struct DownShared {
+    static constexpr int SLOT = DOWN_COLS * QB + TERMS * 4096 + 256;
+    int8_t rings[DOWN_WAVES * 2 * SLOT];
+    float sums[DOWN_WAVES][TOKENS][DOWN_COLS];
+    MoeUnit units[MOE_UNITS];
+    uint8_t pair_token[TOKENS * MOE_TOP_K];
+    int last;
+};
+
+template <int TERMS, int TOKENS>
+__global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
+    using Shared = DownShared<TERMS, TOKENS>;
+    constexpr int SLOT = Shared::SLOT, COPIES = DOWN_COLS / 8 + TERMS * 4 + 1;
+    constexpr int NTD = 64 * DOWN_WAVES;
+    __shared__ __attribute__((aligned(1024))) Shared sh;
+    auto& sums = sh.sums;
+    auto& units = sh.units;
+    auto& pair_token = sh.pair_token;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
-    const int K = g.l.K, I = g.l.I, n0 = blockIdx.x * 16;
-    const int nact = __builtin_amdgcn_readfirstlane(g.space->nact);
-    for (int i = threadIdx.x; i < nact; i += NT)
-        *reinterpret_cast<u32x2*>(act[i]) = *reinterpret_cast<const u32x2*>(&g.space->act[i]);
-    for (int i = threadIdx.x; i < (g.T * g.l.top_k + 1) / 2; i += NT)
+    const int slices = g.l.K / DOWN_COLS, slice = blockIdx.x % slices, part = blockIdx.x / slices;
+    const int K = g.l.K, I = g.l.I, n0 = slice * DOWN_COLS;
+    const int nunits = __builtin_amdgcn_readfirstlane(g.space->nunits);
+    for (int i = threadIdx.x; i < nunits; i += NTD)
+        *reinterpret_cast<u32x2*>(&units[i]) = *reinterpret_cast<const u32x2*>(&g.space->units[i]);
+    for (int i = threadIdx.x; 4 * i < g.T * g.l.top_k; i += NTD)
         reinterpret_cast<uint32_t*>(pair_token)[i] = reinterpret_cast<const uint32_t*>(g.space->pair_token)[i];
-    for (int i = threadIdx.x; i < NW * TOK * 4; i += NT)
+    for (int i = threadIdx.x; i < DOWN_WAVES * TOKENS * DOWN_COLS / 4; i += NTD)
         reinterpret_cast<f32x4*>(sums)[i] = f32x4{0, 0, 0, 0};
     __syncthreads();
-    const int nib = (I + QB - 1) / QB;
+    const int nib = (I + QB - 1) / QB, share = part * DOWN_WAVES + wave, shares = g.parts * DOWN_WAVES;
 
-    int8_t* ring = rings + wave * S * SLOT;
+    int8_t* ring = sh.rings + wave * 2 * SLOT;
     const int64_t blocks2 = e4m3_blocks(K);
-    const int pairs = g.T * g.l.top_k;
-    const __amdgpu_buffer_rsrc_t rh = buffer_of(g.hi, pairs * I * 2), rl = buffer_of(g.lo, pairs * I * 2);
+    const int plane = g.T * g.l.top_k * I * 2;
+    __amdgpu_buffer_rsrc_t rh[TERMS];
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k)
+        rh[k] = buffer_of(reinterpret_cast<const int8_t*>(g.h) + (int64_t)k * plane, plane);
     const int row = lane >> 3, c0 = copy_chunk128(lane, 0), c1 = copy_chunk128(lane, 1);
     const int far = 0x40000000;
-    auto pair_offset = [&](int s, int tile) {   // columns past the pairs repeat the last one
-        const int base = act[s][1], count = act[s][2];
-        return ((base + min(16 * tile + r, count - 1)) * I + 16 * q) * 2;
-    };
-    // the wave's first block of the next expert in use, from number s on, that has one; s == nact
-    // at the end
+    // the wave's first block of the next unit, from number s on, that has one; s == nunits at the end
     auto next = [&](int& s, int& b) {
-        for (; s < nact; ++s) {
-            b = (wave - __builtin_amdgcn_readfirstlane(act[s][0]) * nib) & (NW - 1);
+        for (; s < nunits; ++s) {
+            b = (share - __builtin_amdgcn_readfirstlane(units[s].expert) * nib) & (shares - 1);
             if (b < nib)
                 return;
         }
@@ -482,142 +513,198 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
         int s, b;   // what is fetched next
         __amdgpu_buffer_rsrc_t w;
         const float* scale;
-        int hoff;
+        int rows[4];
     } nx;
     auto enter = [&]() {
         next(nx.s, nx.b);
-        const int a = min(nx.s, nact - 1);
-        const int e = __builtin_amdgcn_readfirstlane(act[a][0]);
-        nx.w = buffer_of(g.l.w2 + ((int64_t)e * K + n0) * I, nx.s < nact ? 16 * I : 0);
+        const MoeUnit u = units[min(nx.s, nunits - 1)];
+        const int e = __builtin_amdgcn_readfirstlane(u.expert);
+        nx.w = buffer_of(g.l.w2 + ((int64_t)e * K + n0) * I, nx.s < nunits ? DOWN_COLS * I : 0);
         nx.scale = g.l.s2 + (e * blocks2 + n0 / QB) * nib;
-        nx.hoff = pair_offset(a, 0);
-    };
-    i32x4 hv[S][2][4];
-    auto load_h = [&](i32x4 (&h)[2][4], int off, int b) {
-        const int half = I - b * QB > 64 ? 128 : 0;   // past I the codes are zeros, and h anything finite
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            h[0][f] = __builtin_amdgcn_raw_buffer_load_b128(rh, off + 16 * (f & 1) + (f >> 1) * half, 2 * b * QB, 0);
-            h[1][f] = __builtin_amdgcn_raw_buffer_load_b128(rl, off + 16 * (f & 1) + (f >> 1) * half, 2 * b * QB, 0);
-        }
+        for (int i = 0; i < 4; ++i)
+            nx.rows[i] = 4 * i + q < u.count ? (u.base + 4 * i + q) * I * 2 : far;
     };
-    auto fetch = [&](int slot, i32x4 (&h)[2][4]) {
+    auto fetch = [&](int slot) {
         int8_t* to = ring + slot * SLOT;
         const int left = I - nx.b * QB;
         const int cut0 = 16 * c0 < left ? 0 : far, cut1 = 16 * c1 < left ? 0 : far;
         const int o0 = row * I + 16 * c0 + nx.b * QB, o1 = (row + 8) * I + 16 * c1 + nx.b * QB;
-        buffer_to_lds16<2>(nx.w, o0 | cut0, 0, to);
-        buffer_to_lds16<2>(nx.w, o1 | cut1, 0, to + 1024);
-        global_to_lds4(nx.scale + nx.b, to + 2048);
-        load_h(h, nx.hoff, nx.b);
-        asm volatile("" ::: "memory");   // no load may sink past the waits that count it
-        nx.b += NW;
+#pragma unroll
+        for (int i = 0; i < DOWN_COLS / 16; ++i) {
+            buffer_to_lds16<2>(nx.w, (o0 + 16 * i * I) | cut0, 0, to + 2048 * i);
+            buffer_to_lds16<2>(nx.w, (o1 + 16 * i * I) | cut1, 0, to + 2048 * i + 1024);
+        }
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+            copy_rows16(rh[k], nx.rows, 2 * nx.b * QB, left, lane, to + DOWN_COLS * QB + 4096 * k);
+        global_to_lds4(nx.scale + nx.b, to + DOWN_COLS * QB + 4096 * TERMS);
+        nx.b += shares;
         if (nx.b >= nib) {
             ++nx.s;
             enter();
         }
     };
 
-    f32x4 acc[TILES];
+    f32x4 acc[DOWN_COLS / 16];
 #pragma unroll
-    for (int i = 0; i < TILES; ++i)
+    for (int i = 0; i < DOWN_COLS / 16; ++i)
         acc[i] = f32x4{0, 0, 0, 0};
-    int s = 0, b = 0;
-    if (nact > 0)
-        next(s, b);
-    if (s < nact) {
+    int s = 0, b = 0, slot = 0;
+    next(s, b);
+    if (s < nunits) {
         nx.s = 0;
         enter();
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i)
-            fetch(i, hv[i]);
+        fetch(0);
         const int f0 = r * QB + ((q ^ swizzle128(r)) << 4), f1 = r * QB + (((q + 4) ^ swizzle128(r)) << 4);
-        while (s < nact) {   // in rounds, as in the first kernel
+        while (s < nunits) {
+            fetch(slot ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(wait_vm(COPIES));
+            __builtin_amdgcn_sched_barrier(0);
+            const int8_t* at = ring + slot * SLOT;
+            const float sc = *reinterpret_cast<const float*>(at + DOWN_COLS * QB + 4096 * TERMS);
+            bf16x8 h[TERMS][4];
 #pragma unroll
-            for (int u = 0; u < S; ++u) {
-                fetch((u + S - 1) % S, hv[(u + S - 1) % S]);
-                __builtin_amdgcn_sched_barrier(0);
-                __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * BATCH));
-                __builtin_amdgcn_sched_barrier(0);
-                const int8_t* at = ring + u * SLOT;
-                const i32x4 w0 = *reinterpret_cast<const i32x4*>(at + f0), w1 = *reinterpret_cast<const i32x4*>(at + f1);
-                const float sc = *reinterpret_cast<const float*>(at + 2048);
+            for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    h[k][f] = rows16_fragment<bf16x8>(at + DOWN_COLS * QB + 4096 * k, r, q, f);
+#pragma unroll
+            for (int i = 0; i < DOWN_COLS / 16; ++i) {
+                const i32x4 w0 = *reinterpret_cast<const i32x4*>(at + 2048 * i + f0);
+                const i32x4 w1 = *reinterpret_cast<const i32x4*>(at + 2048 * i + f1);
                 const bf16x8 a[4] = {codes_bf16(w0[0], w0[1]), codes_bf16(w0[2], w0[3]), codes_bf16(w1[0], w1[1]),
                                      codes_bf16(w1[2], w1[3])};
-                auto product = [&](const i32x4 (&h)[2][4], f32x4& to) {
-                    f32x4 ph{0, 0, 0, 0}, pl{0, 0, 0, 0};
+                f32x4 p[TERMS];
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        ph = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[f], __builtin_bit_cast(bf16x8, h[0][f]), ph, 0, 0, 0);
-                        pl = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[f], __builtin_bit_cast(bf16x8, h[1][f]), pl, 0, 0, 0);
-                    }
+                for (int k = 0; k < TERMS; ++k) {
+                    p[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        to[e] = fmaf(sc, ph[e] + pl[e], to[e]);
-                };
-                product(hv[u], acc[0]);
-                const int count = __builtin_amdgcn_readfirstlane(act[min(s, nact - 1)][2]);
-#pragma unroll
-                for (int i = 1; i < TILES; ++i) {
-                    if (16 * i < count) {
-                        i32x4 more[2][4];
-                        load_h(more, pair_offset(min(s, nact - 1), i), b);
-                        product(more, acc[i]);
-                    }
+                    for (int f = 0; f < 4; ++f)
+                        p[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[f], h[k][f], p[k], 0, 0, 0);
                 }
-                __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the slot's reads are done before it is filled again
-                __builtin_amdgcn_sched_barrier(0);
-                b += NW;
-                if (b >= nib && s < nact) {
-                    // leave the expert: a token's four sums lie together, and no two pairs of an
-                    // expert share a token
-                    const int base = act[s][1];
 #pragma unroll
-                    for (int i = 0; i < TILES; ++i) {
-                        if (16 * i + r < count) {
-                            f32x4* to = reinterpret_cast<f32x4*>(&sums[wave][pair_token[base + 16 * i + r]][4 * q]);
-                            *to += acc[i];
-                        }
-                        acc[i] = f32x4{0, 0, 0, 0};
-                    }
-                    ++s;
-                    next(s, b);
+                for (int e = 0; e < 4; ++e) {
+                    float v = p[TERMS - 1][e];
+#pragma unroll
+                    for (int k = TERMS - 2; k >= 0; --k)
+                        v += p[k][e];
+                    acc[i][e] = fmaf(sc, v, acc[i][e]);
                 }
+            }
+            __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the slot's reads are done before it is filled again
+            __builtin_amdgcn_sched_barrier(0);
+            slot ^= 1;
+            b += shares;
+            if (b >= nib) {
+                // leave the unit: a token's four sums lie together, and no two pairs of a unit share a
+                // token
+                const MoeUnit u = units[s];
+                if (r < u.count) {
+                    float* to = sums[wave][pair_token[u.base + r]] + 4 * q;
+#pragma unroll
+                    for (int i = 0; i < DOWN_COLS / 16; ++i)
+                        *reinterpret_cast<f32x4*>(to + 16 * i) += acc[i];
+                }
+#pragma unroll
+                for (int i = 0; i < DOWN_COLS / 16; ++i)
+                    acc[i] = f32x4{0, 0, 0, 0};
+                ++s;
+                next(s, b);
             }
         }
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < g.T * 16; i += NT) {
-        const int t = i / 16, n = i % 16;
-        float v = sums[0][t][n];
+    // four columns of a token a thread
+    constexpr int C4 = DOWN_COLS / 4;
+    auto put = [&](int i, f32x4 v) {
+        const int64_t at = (int64_t)(i / C4) * K + n0 + i % C4 * 4;
+        if (g.l.out_f16) {
+            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(g.l.out) + at) =
+                f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+        } else {
+            *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(g.l.out) + at) = v;
+        }
+    };
+    auto joined = [&](int i) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][i / C4][i % C4 * 4]);
 #pragma unroll
-        for (int w = 1; w < NW; ++w)
-            v += sums[w][t][n];
-        const int64_t at = (int64_t)t * K + n0 + n;
-        if (g.l.out_f16)
-            reinterpret_cast<_Float16*>(g.l.out)[at] = (_Float16)v;
-        else
-            reinterpret_cast<float*>(g.l.out)[at] = v;
+        for (int w = 1; w < DOWN_WAVES; ++w)
+            v += *reinterpret_cast<const f32x4*>(&sums[w][i / C4][i % C4 * 4]);
+        return v;
+    };
+    if (g.parts == 1) {
+        for (int i = threadIdx.x; i < g.T * C4; i += NTD)
+            put(i, joined(i));
+        return;
+    }
+    // The parts' sums go past the XCDs' caches, as the parts may be on different ones: stores and loads
+    // of device scope, the stores done before the arrival is counted. Whoever counts the last arrival
+    // adds the parts in order. Nobody waits for another.
+    constexpr int DEVICE = 16;   // sc1
+    const int psize = g.T * K * 4;
+    const __amdgpu_buffer_rsrc_t mine = buffer_of(g.sums + (int64_t)part * g.T * K, psize);
+    for (int i = threadIdx.x; i < g.T * C4; i += NTD)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, joined(i)), mine,
+                                               ((i / C4) * K + n0 + i % C4 * 4) * 4, 0, DEVICE);
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    __syncthreads();
+    if (threadIdx.x == 0)
+        sh.last = __hip_atomic_fetch_add(&g.space->arrived[slice], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (uint32_t)g.parts - 1;
+    __syncthreads();
+    if (!sh.last)
+        return;
+    for (int i = threadIdx.x; i < g.T * C4; i += NTD) {
+        f32x4 v{0, 0, 0, 0};
+        for (int p = 0; p < g.parts; ++p) {
+            const __amdgpu_buffer_rsrc_t from = buffer_of(g.sums + (int64_t)p * g.T * K, psize);
+            v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               from, ((i / C4) * K + n0 + i % C4 * 4) * 4, 0, DEVICE));
+        }
+        put(i, v);
     }
 }
 
-template <int TILES>
-void launch_up(const Moe& g, uint32_t grid, hipStream_t stream) {
-    const dim3 wgs(grid), nt(NT);
+template <int TERMS>
+void launch_experts(const Moe& g, hipStream_t stream) {
+    const int64_t most = (int64_t)(g.T * g.l.top_k < MOE_UNITS ? g.T * g.l.top_k : MOE_UNITS) * (g.l.I / 16);
+    const dim3 up((uint32_t)(most < cu_count() ? most : cu_count())), nt(NT);
     if (g.l.E <= 64)
-        moe_up_kernel<TILES, 4><<<wgs, nt, 0, stream>>>(g);
+        moe_up_kernel<4, TERMS><<<up, nt, 0, stream>>>(g);
     else if (g.l.E <= 128)
-        moe_up_kernel<TILES, 8><<<wgs, nt, 0, stream>>>(g);
+        moe_up_kernel<8, TERMS><<<up, nt, 0, stream>>>(g);
     else
-        moe_up_kernel<TILES, 32><<<wgs, nt, 0, stream>>>(g);
+        moe_up_kernel<32, TERMS><<<up, nt, 0, stream>>>(g);
+    const dim3 down((uint32_t)(g.l.K / DOWN_COLS * g.parts)), ntd(64 * DOWN_WAVES);
+    if (g.T <= 16)
+        moe_down_kernel<TERMS, 16><<<down, ntd, 0, stream>>>(g);
+    else if constexpr (TERMS == 2)
+        moe_down_kernel<TERMS, 64><<<down, ntd, 0, stream>>>(g);
+    else
+        moe_down_kernel<TERMS, 32><<<down, ntd, 0, stream>>>(g);
+}
+
+// Tokens of a launch: three terms leave LDS for the sums of 32.
+int tokens_of_launch(bool out_f16) { return out_f16 ? MOE_TOKENS : 32; }
+
+// Workgroups that share a slice of output columns, so that the slices of narrow layers fill the chip's
+// 256 CUs.
+int parts_of(int K) {
+    int p = 1;
+    while (p < 8 && 2 * p * (K / DOWN_COLS) <= 256)
+        p *= 2;
+    return p;
 }
 
 }  // namespace
 
-int64_t moe_workspace(int64_t T, int top_k, int I) {
-    const int64_t t = T < MOE_TOKENS ? T : MOE_TOKENS;
-    return (int64_t)sizeof(MoeSpace) + t * top_k * I * 4;
+int64_t moe_workspace(int64_t T, int top_k, int K, int I) {
+    const int64_t t = T < MOE_TOKENS ? T : MOE_TOKENS;   // (32 of three terms take less)
+    return (int64_t)sizeof(MoeSpace) + t * K * 4 * parts_of(K) + t * top_k * I * 6;
 }
 
 ql_status launch_moe_router(const void* x, const void* w, float* logits, int64_t T, int64_t E, int64_t K,
@@ -633,29 +720,22 @@ ql_status launch_moe_router(const void* x, const void* w, float* logits, int64_t
 }
 
 ql_status launch_moe_e4m3_block(const MoeLayer& l, hipStream_t stream) {
-    for (int64_t t = 0; t < l.T; t += MOE_TOKENS) {
+    const int tokens = tokens_of_launch(l.out_f16);
+    for (int64_t t = 0; t < l.T; t += tokens) {
         Moe g{};
         g.l = l;
-        g.T = (int)(l.T - t < MOE_TOKENS ? l.T - t : MOE_TOKENS);
+        g.T = (int)(l.T - t < tokens ? l.T - t : tokens);
+        g.parts = parts_of(l.K);
         g.l.x += t * l.K;
         g.l.logits += t * l.E;
         g.l.out = reinterpret_cast<int8_t*>(l.out) + t * l.K * (l.out_f16 ? 2 : 4);
         g.space = reinterpret_cast<MoeSpace*>(l.ws);
-        g.hi = reinterpret_cast<__bf16*>(l.ws + sizeof(MoeSpace));
-        g.lo = g.hi + (int64_t)g.T * l.top_k * l.I;
-        const int64_t most = (int64_t)(l.E < g.T * l.top_k ? l.E : g.T * l.top_k) * (l.I / 16);
-        const uint32_t grid = (uint32_t)(most < cu_count() ? most : cu_count());
-        const dim3 down((uint32_t)(l.K / 16)), nt(NT);
-        if (g.T <= 16) {
-            launch_up<1>(g, grid, stream);
-            moe_down_kernel<1><<<down, nt, 0, stream>>>(g);
-        } else if (g.T <= 32) {
-            launch_up<2>(g, grid, stream);
-            moe_down_kernel<2><<<down, nt, 0, stream>>>(g);
-        } else {
-            launch_up<4>(g, grid, stream);
-            moe_down_kernel<4><<<down, nt, 0, stream>>>(g);
-        }
+        g.sums = reinterpret_cast<float*>(l.ws + sizeof(MoeSpace));
+        g.h = reinterpret_cast<__bf16*>(g.sums + (int64_t)g.parts * g.T * l.K);
+        if (l.out_f16)
+            launch_experts<2>(g, stream);
+        else
+            launch_experts<3>(g, stream);
     }
     return launch_status();
 }

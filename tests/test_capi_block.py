@@ -23,7 +23,7 @@ def lib():
     L.gemm_e4m3_block.argtypes = [P, P, P, P, P, I, P, I, I64, I64, I64, P]
     L.moe_router.argtypes = [P, P, P, I64, I64, I64, P]
     L.moe_e4m3_block.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, I, P, I64, P]
-    L.moe_e4m3_block_workspace_bytes.argtypes = [I64, I64, I64, ctypes.POINTER(I64)]
+    L.moe_e4m3_block_workspace_bytes.argtypes = [I64, I64, I64, I64, ctypes.POINTER(I64)]
     return L
 
 
@@ -84,9 +84,9 @@ def test_router(lib):
 
 
 def test_experts(lib):
-    def need(T=4, k=2, I=128):
+    def need(T=4, k=2, K=256, I=128):
         n = ctypes.c_int64(-1)
-        assert lib.moe_e4m3_block_workspace_bytes(T, k, I, ctypes.byref(n)) == OK
+        assert lib.moe_e4m3_block_workspace_bytes(T, k, K, I, ctypes.byref(n)) == OK
         return n.value
 
     def f(x=A, lg=A, w13=A, s13=A, w2=A, s2=A, out=A, dt=F16, T=4, E=8, k=2, K=256, I=128, ws=A, size=None):
@@ -106,7 +106,7 @@ def test_experts(lib):
     assert f(T=0, x=None, size=0) == OK
 
     n = ctypes.c_int64(7)
-    for bad in ((-1, 2, 128), (4, 0, 128), (4, 17, 128), (4, 2, 0), (4, 2, 100)):
+    for bad in ((-1, 2, 64, 128), (4, 0, 64, 128), (4, 17, 64, 128), (4, 2, 64, 0), (4, 2, 64, 100), (4, 2, 0, 64), (4, 2, 32, 64)):
         assert lib.moe_e4m3_block_workspace_bytes(*bad, ctypes.byref(n)) == SHAPE
-    assert n.value == 7 and lib.moe_e4m3_block_workspace_bytes(4, 2, 128, None) == NULL
+    assert n.value == 7 and lib.moe_e4m3_block_workspace_bytes(4, 2, 64, 128, None) == NULL
     assert need(T=0) == 0 and need(T=1000) == need(T=64) > need(T=63)
