@@ -451,47 +451,44 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
 // --------------------------------------------------------------------- the sums over experts
 //
 // A workgroup owns 32 columns of the output and one of `parts` shares of I. Block b of expert e is
-// number (e * blocks + b) % (parts * 4)'s, part by part and wave by wave: neighbouring waves read
+// number (e * blocks + b) % (parts * 8)'s, part by part and wave by wave: neighbouring waves read
 // neighbouring 128 bytes, all have about as many blocks, and who adds what to a token's sums does not
-// depend on the other tokens' experts. A wave adds a unit's products to its own sums [token][32] in LDS;
-// the waves' sums are added at the end, and the parts' by the workgroup that comes last.
+// depend on the other tokens' experts. A wave's blocks of all units make one sequence. Codes go through
+// its ring of S slots in LDS; h's few rows come from L2 into registers, as far ahead (in LDS they would
+// take twice the codes' space). A wave adds a unit's products to its own sums [token][32] in LDS; the
+// waves' sums are added at the end, and the parts' by the workgroup that comes last.
 
-constexpr int DOWN_WAVES = 4, DOWN_COLS = 32;
+constexpr int DOWN_COLS = 32, DOWN_SLOT = DOWN_COLS * QB + 256;
 
-template <int TERMS, int TOKENS>
+template <int TOKENS, int S>
 struct DownShared {
-    static constexpr int SLOT = DOWN_COLS * QB + TERMS * 4096 + 256;
-    int8_t rings[DOWN_WAVES * 2 * SLOT];
-    float sums[DOWN_WAVES][TOKENS][DOWN_COLS];
+    int8_t rings[NW * S * DOWN_SLOT];
+    float sums[NW][TOKENS][DOWN_COLS];
     MoeUnit units[MOE_UNITS];
     uint8_t pair_token[TOKENS * MOE_TOP_K];
     int last;
 };
 
-template <int TERMS, int TOKENS>
-__global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
-    using Shared = DownShared<TERMS, TOKENS>;
-    constexpr int SLOT = Shared::SLOT, COPIES = DOWN_COLS / 8 + TERMS * 4 + 1;
-    constexpr int NTD = 64 * DOWN_WAVES;
-    __shared__ __attribute__((aligned(1024))) Shared sh;
+template <int TERMS, int TOKENS, int S>
+__global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
+    constexpr int COPIES = DOWN_COLS / 8 + 1 + TERMS * 4;
+    __shared__ __attribute__((aligned(1024))) DownShared<TOKENS, S> sh;
     auto& sums = sh.sums;
-    auto& units = sh.units;
-    auto& pair_token = sh.pair_token;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int slices = g.l.K / DOWN_COLS, slice = blockIdx.x % slices, part = blockIdx.x / slices;
     const int K = g.l.K, I = g.l.I, n0 = slice * DOWN_COLS;
     const int nunits = __builtin_amdgcn_readfirstlane(g.space->nunits);
-    for (int i = threadIdx.x; i < nunits; i += NTD)
-        *reinterpret_cast<u32x2*>(&units[i]) = *reinterpret_cast<const u32x2*>(&g.space->units[i]);
-    for (int i = threadIdx.x; 4 * i < g.T * g.l.top_k; i += NTD)
-        reinterpret_cast<uint32_t*>(pair_token)[i] = reinterpret_cast<const uint32_t*>(g.space->pair_token)[i];
-    for (int i = threadIdx.x; i < DOWN_WAVES * TOKENS * DOWN_COLS / 4; i += NTD)
+    for (int i = threadIdx.x; i < nunits; i += NT)
+        *reinterpret_cast<u32x2*>(&sh.units[i]) = *reinterpret_cast<const u32x2*>(&g.space->units[i]);
+    for (int i = threadIdx.x; 4 * i < g.T * g.l.top_k; i += NT)
+        reinterpret_cast<uint32_t*>(sh.pair_token)[i] = reinterpret_cast<const uint32_t*>(g.space->pair_token)[i];
+    for (int i = threadIdx.x; i < NW * TOKENS * DOWN_COLS / 4; i += NT)
         reinterpret_cast<f32x4*>(sums)[i] = f32x4{0, 0, 0, 0};
     __syncthreads();
-    const int nib = (I + QB - 1) / QB, share = part * DOWN_WAVES + wave, shares = g.parts * DOWN_WAVES;
+    const int nib = (I + QB - 1) / QB, share = part * NW + wave, shares = g.parts * NW;
 
-    int8_t* ring = sh.rings + wave * 2 * SLOT;
+    int8_t* ring = sh.rings + wave * S * DOWN_SLOT;
     const int64_t blocks2 = e4m3_blocks(K);
     const int plane = g.T * g.l.top_k * I * 2;
     __amdgpu_buffer_rsrc_t rh[TERMS];
@@ -500,33 +497,46 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
         rh[k] = buffer_of(reinterpret_cast<const int8_t*>(g.h) + (int64_t)k * plane, plane);
     const int row = lane >> 3, c0 = copy_chunk128(lane, 0), c1 = copy_chunk128(lane, 1);
     const int far = 0x40000000;
-    // the wave's first block of the next unit, from number s on, that has one; s == nunits at the end
-    auto next = [&](int& s, int& b) {
-        for (; s < nunits; ++s) {
-            b = (share - __builtin_amdgcn_readfirstlane(units[s].expert) * nib) & (shares - 1);
-            if (b < nib)
-                return;
-        }
-        b = 0;
-    };
+
+    // What is fetched next: block b of the unit that lane `at` of the window holds. A window is 64
+    // units, one a lane, and `have` says in which of them the wave has a block.
     struct {
-        int s, b;   // what is fetched next
+        int window, at, b, hoff;
+        unsigned long long have;
+        int expert, pairs, first;   // of the lane's unit: base and count << 16, the wave's first block
         __amdgpu_buffer_rsrc_t w;
         const float* scale;
-        int rows[4];
     } nx;
-    auto enter = [&]() {
-        next(nx.s, nx.b);
-        const MoeUnit u = units[min(nx.s, nunits - 1)];
-        const int e = __builtin_amdgcn_readfirstlane(u.expert);
-        nx.w = buffer_of(g.l.w2 + ((int64_t)e * K + n0) * I, nx.s < nunits ? DOWN_COLS * I : 0);
-        nx.scale = g.l.s2 + (e * blocks2 + n0 / QB) * nib;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            nx.rows[i] = 4 * i + q < u.count ? (u.base + 4 * i + q) * I * 2 : far;
+    auto open_window = [&](int w) {
+        nx.window = w;
+        const int n = min(w + lane, nunits - 1);
+        const MoeUnit u = sh.units[n];
+        nx.expert = u.expert;
+        nx.pairs = u.base | u.count << 16;
+        nx.first = (share - u.expert * nib) & (shares - 1);
+        nx.have = __ballot(w + lane < nunits && nx.first < nib);
     };
-    auto fetch = [&](int slot) {
-        int8_t* to = ring + slot * SLOT;
+    auto enter = [&]() {   // the next unit that has a block, if any is left
+        while (nx.have == 0 && nx.window + 64 < nunits)
+            open_window(nx.window + 64);
+        if (nx.have == 0) {
+            nx.at = -1;
+            nx.w = buffer_of(g.l.w2, 0);
+            return;
+        }
+        nx.at = __builtin_ctzll(nx.have);
+        nx.have &= nx.have - 1;
+        nx.b = __builtin_amdgcn_readlane(nx.first, nx.at);
+        const int e = __builtin_amdgcn_readlane(nx.expert, nx.at), pairs = __builtin_amdgcn_readlane(nx.pairs, nx.at);
+        nx.w = buffer_of(g.l.w2 + ((int64_t)e * K + n0) * I, DOWN_COLS * I);
+        nx.scale = g.l.s2 + (e * blocks2 + n0 / QB) * nib;
+        // columns past the unit's pairs repeat the last one
+        nx.hoff = (((pairs & 0xFFFF) + min(r, (pairs >> 16) - 1)) * I + 16 * q) * 2;
+    };
+    // an item's unit as pairs above, with bit 31 where it is the wave's last block of the unit; -1 past
+    // the end
+    auto fetch = [&](int slot, i32x4 (&h)[TERMS][4]) {
+        int8_t* to = ring + slot * DOWN_SLOT;
         const int left = I - nx.b * QB;
         const int cut0 = 16 * c0 < left ? 0 : far, cut1 = 16 * c1 < left ? 0 : far;
         const int o0 = row * I + 16 * c0 + nx.b * QB, o1 = (row + 8) * I + 16 * c1 + nx.b * QB;
@@ -535,83 +545,91 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
             buffer_to_lds16<2>(nx.w, (o0 + 16 * i * I) | cut0, 0, to + 2048 * i);
             buffer_to_lds16<2>(nx.w, (o1 + 16 * i * I) | cut1, 0, to + 2048 * i + 1024);
         }
+        global_to_lds4(nx.scale + nx.b, to + DOWN_COLS * QB);
+        const int half = left > 64 ? 128 : 0;   // past I the codes are zeros, and h anything finite
 #pragma unroll
         for (int k = 0; k < TERMS; ++k)
-            copy_rows16(rh[k], nx.rows, 2 * nx.b * QB, left, lane, to + DOWN_COLS * QB + 4096 * k);
-        global_to_lds4(nx.scale + nx.b, to + DOWN_COLS * QB + 4096 * TERMS);
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                h[k][f] = __builtin_amdgcn_raw_buffer_load_b128(rh[k], nx.hoff + 16 * (f & 1) + (f >> 1) * half, 2 * nx.b * QB, 0);
+        asm volatile("" ::: "memory");   // no load may sink past the waits that count it
+        if (nx.at < 0)
+            return -1;
+        int info = __builtin_amdgcn_readlane(nx.pairs, nx.at);
         nx.b += shares;
         if (nx.b >= nib) {
-            ++nx.s;
+            info |= (int)0x80000000;
+            nx.b = 0;
             enter();
         }
+        return info;
     };
 
     f32x4 acc[DOWN_COLS / 16];
 #pragma unroll
     for (int i = 0; i < DOWN_COLS / 16; ++i)
         acc[i] = f32x4{0, 0, 0, 0};
-    int s = 0, b = 0, slot = 0;
-    next(s, b);
-    if (s < nunits) {
-        nx.s = 0;
+    if (nunits > 0) {
+        i32x4 hv[S][TERMS][4];
+        int info[S];
+        nx.scale = g.l.s2;
+        nx.b = nx.hoff = 0;
+        open_window(0);
         enter();
-        fetch(0);
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i)
+            info[i] = fetch(i, hv[i]);
         const int f0 = r * QB + ((q ^ swizzle128(r)) << 4), f1 = r * QB + (((q + 4) ^ swizzle128(r)) << 4);
-        while (s < nunits) {
-            fetch(slot ^ 1);
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(wait_vm(COPIES));
-            __builtin_amdgcn_sched_barrier(0);
-            const int8_t* at = ring + slot * SLOT;
-            const float sc = *reinterpret_cast<const float*>(at + DOWN_COLS * QB + 4096 * TERMS);
-            bf16x8 h[TERMS][4];
+        // in rounds of S items, the last one filled up with zeros
+        while (info[0] != -1) {
 #pragma unroll
-            for (int k = 0; k < TERMS; ++k)
+            for (int u = 0; u < S; ++u) {
+                info[(u + S - 1) % S] = fetch((u + S - 1) % S, hv[(u + S - 1) % S]);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * COPIES));
+                __builtin_amdgcn_sched_barrier(0);
+                const int8_t* at = ring + u * DOWN_SLOT;
+                const float sc = *reinterpret_cast<const float*>(at + DOWN_COLS * QB);
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    h[k][f] = rows16_fragment<bf16x8>(at + DOWN_COLS * QB + 4096 * k, r, q, f);
+                for (int i = 0; i < DOWN_COLS / 16; ++i) {
+                    const i32x4 w0 = *reinterpret_cast<const i32x4*>(at + 2048 * i + f0);
+                    const i32x4 w1 = *reinterpret_cast<const i32x4*>(at + 2048 * i + f1);
+                    const bf16x8 a[4] = {codes_bf16(w0[0], w0[1]), codes_bf16(w0[2], w0[3]), codes_bf16(w1[0], w1[1]),
+                                         codes_bf16(w1[2], w1[3])};
+                    f32x4 p[TERMS];
 #pragma unroll
-            for (int i = 0; i < DOWN_COLS / 16; ++i) {
-                const i32x4 w0 = *reinterpret_cast<const i32x4*>(at + 2048 * i + f0);
-                const i32x4 w1 = *reinterpret_cast<const i32x4*>(at + 2048 * i + f1);
-                const bf16x8 a[4] = {codes_bf16(w0[0], w0[1]), codes_bf16(w0[2], w0[3]), codes_bf16(w1[0], w1[1]),
-                                     codes_bf16(w1[2], w1[3])};
-                f32x4 p[TERMS];
+                    for (int k = 0; k < TERMS; ++k) {
+                        p[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < TERMS; ++k) {
-                    p[k] = f32x4{0, 0, 0, 0};
+                        for (int f = 0; f < 4; ++f)
+                            p[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[f], __builtin_bit_cast(bf16x8, hv[u][k][f]), p[k],
+                                                                           0, 0, 0);
+                    }
 #pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        p[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[f], h[k][f], p[k], 0, 0, 0);
+                    for (int e = 0; e < 4; ++e) {
+                        float v = p[TERMS - 1][e];
+#pragma unroll
+                        for (int k = TERMS - 2; k >= 0; --k)
+                            v += p[k][e];
+                        acc[i][e] = fmaf(sc, v, acc[i][e]);
+                    }
                 }
+                __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the slot's reads are done before it is filled again
+                __builtin_amdgcn_sched_barrier(0);
+                if (info[u] < -1) {
+                    // leave the unit: a token's four sums lie together, and no two pairs of a unit share a
+                    // token
+                    const int base = info[u] & 0xFFFF, count = info[u] >> 16 & 0x7FFF;
+                    if (r < count) {
+                        float* to = sums[wave][sh.pair_token[base + r]] + 4 * q;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = p[TERMS - 1][e];
-#pragma unroll
-                    for (int k = TERMS - 2; k >= 0; --k)
-                        v += p[k][e];
-                    acc[i][e] = fmaf(sc, v, acc[i][e]);
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the slot's reads are done before it is filled again
-            __builtin_amdgcn_sched_barrier(0);
-            slot ^= 1;
-            b += shares;
-            if (b >= nib) {
-                // leave the unit: a token's four sums lie together, and no two pairs of a unit share a
-                // token
-                const MoeUnit u = units[s];
-                if (r < u.count) {
-                    float* to = sums[wave][pair_token[u.base + r]] + 4 * q;
+                        for (int i = 0; i < DOWN_COLS / 16; ++i)
+                            *reinterpret_cast<f32x4*>(to + 16 * i) += acc[i];
+                    }
 #pragma unroll
                     for (int i = 0; i < DOWN_COLS / 16; ++i)
-                        *reinterpret_cast<f32x4*>(to + 16 * i) += acc[i];
+                        acc[i] = f32x4{0, 0, 0, 0};
                 }
-#pragma unroll
-                for (int i = 0; i < DOWN_COLS / 16; ++i)
-                    acc[i] = f32x4{0, 0, 0, 0};
-                ++s;
-                next(s, b);
             }
         }
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
@@ -632,12 +650,12 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
     auto joined = [&](int i) {
         f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][i / C4][i % C4 * 4]);
 #pragma unroll
-        for (int w = 1; w < DOWN_WAVES; ++w)
+        for (int w = 1; w < NW; ++w)
             v += *reinterpret_cast<const f32x4*>(&sums[w][i / C4][i % C4 * 4]);
         return v;
     };
     if (g.parts == 1) {
-        for (int i = threadIdx.x; i < g.T * C4; i += NTD)
+        for (int i = threadIdx.x; i < g.T * C4; i += NT)
             put(i, joined(i));
         return;
     }
@@ -647,7 +665,7 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
     constexpr int DEVICE = 16;   // sc1
     const int psize = g.T * K * 4;
     const __amdgpu_buffer_rsrc_t mine = buffer_of(g.sums + (int64_t)part * g.T * K, psize);
-    for (int i = threadIdx.x; i < g.T * C4; i += NTD)
+    for (int i = threadIdx.x; i < g.T * C4; i += NT)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, joined(i)), mine,
                                                ((i / C4) * K + n0 + i % C4 * 4) * 4, 0, DEVICE);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
@@ -658,7 +676,7 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe g) {
     __syncthreads();
     if (!sh.last)
         return;
-    for (int i = threadIdx.x; i < g.T * C4; i += NTD) {
+    for (int i = threadIdx.x; i < g.T * C4; i += NT) {
         f32x4 v{0, 0, 0, 0};
         for (int p = 0; p < g.parts; ++p) {
             const __amdgpu_buffer_rsrc_t from = buffer_of(g.sums + (int64_t)p * g.T * K, psize);
@@ -679,17 +697,14 @@ void launch_experts(const Moe& g, hipStream_t stream) {
         moe_up_kernel<8, TERMS><<<up, nt, 0, stream>>>(g);
     else
         moe_up_kernel<32, TERMS><<<up, nt, 0, stream>>>(g);
-    const dim3 down((uint32_t)(g.l.K / DOWN_COLS * g.parts)), ntd(64 * DOWN_WAVES);
+    const dim3 down((uint32_t)(g.l.K / DOWN_COLS * g.parts));
     if (g.T <= 16)
-        moe_down_kernel<TERMS, 16><<<down, ntd, 0, stream>>>(g);
-    else if constexpr (TERMS == 2)
-        moe_down_kernel<TERMS, 64><<<down, ntd, 0, stream>>>(g);
+        moe_down_kernel<TERMS, 16, 3><<<down, nt, 0, stream>>>(g);
+    else if (g.T <= 32)
+        moe_down_kernel<TERMS, 32, 3><<<down, nt, 0, stream>>>(g);
     else
-        moe_down_kernel<TERMS, 32><<<down, ntd, 0, stream>>>(g);
+        moe_down_kernel<TERMS, 64, 2><<<down, nt, 0, stream>>>(g);
 }
-
-// Tokens of a launch: three terms leave LDS for the sums of 32.
-int tokens_of_launch(bool out_f16) { return out_f16 ? MOE_TOKENS : 32; }
 
 // Workgroups that share a slice of output columns, so that the slices of narrow layers fill the chip's
 // 256 CUs.
@@ -703,7 +718,7 @@ int parts_of(int K) {
 }  // namespace
 
 int64_t moe_workspace(int64_t T, int top_k, int K, int I) {
-    const int64_t t = T < MOE_TOKENS ? T : MOE_TOKENS;   // (32 of three terms take less)
+    const int64_t t = T < MOE_TOKENS ? T : MOE_TOKENS;
     return (int64_t)sizeof(MoeSpace) + t * K * 4 * parts_of(K) + t * top_k * I * 6;
 }
 
@@ -720,11 +735,10 @@ ql_status launch_moe_router(const void* x, const void* w, float* logits, int64_t
 }
 
 ql_status launch_moe_e4m3_block(const MoeLayer& l, hipStream_t stream) {
-    const int tokens = tokens_of_launch(l.out_f16);
-    for (int64_t t = 0; t < l.T; t += tokens) {
+    for (int64_t t = 0; t < l.T; t += MOE_TOKENS) {
         Moe g{};
         g.l = l;
-        g.T = (int)(l.T - t < tokens ? l.T - t : tokens);
+        g.T = (int)(l.T - t < MOE_TOKENS ? l.T - t : MOE_TOKENS);
         g.parts = parts_of(l.K);
         g.l.x += t * l.K;
         g.l.logits += t * l.E;
