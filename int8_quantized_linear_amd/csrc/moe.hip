@@ -85,8 +85,10 @@ __global__ __launch_bounds__(RW* WAVE) void moe_router_kernel(const _Float16* __
 //
 // Every workgroup of the first kernel works the routes out for itself from the logits (it would
 // wait as long for another to do it). Pairs (expert, token) are numbered expert by expert, tokens
-// in order, and cut into units of one expert and up to 16 pairs, the columns of a matrix instruction.
+// in order, and cut into units of one expert and up to 16 pairs, the columns of a matrix instruction
+// (up to 32 in the first kernel where experts have many).
 
+constexpr int DOWN_COLS = 32;   // output columns of a workgroup of the second kernel
 constexpr int MOE_PAIRS = MOE_TOKENS * MOE_TOP_K;
 constexpr int MOE_UNITS = MOE_EXPERTS + MOE_PAIRS / 16;   // at most: all experts, each with a last, short unit
 
@@ -111,7 +113,7 @@ struct RouteScratch {
 
 // The workspace: the routes as the second kernel needs them, arrivals at each slice of output columns,
 // h's terms ([pairs][I] each), and the parts' sums of the output.
-constexpr int MOE_SLICES = 131072 / 32;
+constexpr int MOE_SLICES = 131072 / DOWN_COLS;
 struct MoeSpace {
     int nunits;
     int pad[3];
@@ -154,7 +156,7 @@ __device__ inline int row16_min(int v) {
 
 // 16 lanes a token, R logits a lane: top_k rounds of the largest that is left. NaN is never taken,
 // nor is -infinity.
-template <int R>
+template <int R, int UNIT>
 __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
     const int tid = threadIdx.x, E = g.l.E, k = g.l.top_k;
     rs.tokens[tid] = 0;
@@ -215,7 +217,8 @@ __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
     static_assert(NT == MOE_EXPERTS, "one expert a thread");
     const unsigned long long m = rs.tokens[tid];
     const int pairs = __popcll(m);
-    const uint32_t own = (uint32_t)pairs << 16 | (uint32_t)((pairs + 15) / 16);
+    // pairs, units of 16 and units of UNIT in one number
+    const uint32_t own = (uint32_t)pairs << 20 | (uint32_t)((pairs + 15) / 16) << 10 | (uint32_t)((pairs + UNIT - 1) / UNIT);
     uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < WAVE; o <<= 1) {
@@ -231,11 +234,18 @@ __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
         total += rs.part[w];
         sum += w < tid >> 6 ? rs.part[w] : 0;
     }
-    rs.base[tid] = (uint16_t)(sum >> 16);
-    for (int i = 0; 16 * i < pairs; ++i)
-        rt.units[(sum & 0xFFFF) + i] = {(uint16_t)tid, (uint16_t)((sum >> 16) + 16 * i), (uint16_t)min(16, pairs - 16 * i), 0};
+    const int base = (int)(sum >> 20);
+    rs.base[tid] = (uint16_t)base;
+    for (int i = 0; UNIT * i < pairs; ++i)
+        rt.units[(sum & 1023) + i] = {(uint16_t)tid, (uint16_t)(base + UNIT * i), (uint16_t)min(UNIT, pairs - UNIT * i), 0};
     if (tid == 0)
-        rt.nunits = (int)(total & 0xFFFF);
+        rt.nunits = (int)(total & 1023);
+    if (blockIdx.x == 0) {
+        for (int i = 0; 16 * i < pairs; ++i)
+            g.space->units[(sum >> 10 & 1023) + i] = {(uint16_t)tid, (uint16_t)(base + 16 * i), (uint16_t)min(16, pairs - 16 * i), 0};
+        if (tid == 0)
+            g.space->nunits = (int)(total >> 10 & 1023);
+    }
     __syncthreads();
     for (int i = tid; i < g.T * k; i += NT) {
         const int t = i / k, e = rs.id[t][i % k];
@@ -265,61 +275,41 @@ __device__ inline bf16x8 codes_bf16(int w0, int w1) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Copies of 16 rows of 256 bytes (128 values of 16 bits) into LDS, four rows each: chunk c (16 bytes)
-// of row r lies at chunk position c ^ r, so that the 16 rows of a fragment read fall into distinct
-// banks. rows[i] is the byte offset of the lane's row in copy i, or out of range; `left` values are
-// left of K at this block, the rest comes as zeros.
-__device__ inline void copy_rows16(__amdgpu_buffer_rsrc_t from, const int (&rows)[4], int at, int left, int lane, int8_t* to) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = (lane & 15) ^ (4 * i + (lane >> 4));
-        buffer_to_lds16(from, (rows[i] + at + 16 * c) | (8 * c < left ? 0 : 0x40000000), 0, to + 1024 * i);
-    }
-}
-
-// Fragment f of four of such rows, with the k order in which codes_* takes a row of codes.
-template <class V>
-__device__ inline V rows16_fragment(const int8_t* from, int r, int q, int f) {
-    const int c = ((f >> 1) * 4 + q) * 2 + (f & 1);
-    return *reinterpret_cast<const V*>(from + r * 256 + ((c ^ r) << 4));
-}
-
 // ------------------------------------------------------------------------ the gated products
 //
-// A task is a unit and 16 columns of h: 16 rows of W1 and 16 of W3 against the unit's tokens. A
-// workgroup takes every gridDim-th task; its waves split K, wave w taking the blocks w, w + 8, ... of
-// every task. The wave's items (task, block) make one sequence, so the next task's first copies are in
-// flight while a task's sums are joined. W is the first operand: a lane's sums belong to one token
-// (lane & 15) and four columns of h.
+// A task is a unit and 16 columns of h: 16 rows of W1 and 16 of W3 against the unit's tokens, TILES x 16
+// of them at most. A workgroup takes every gridDim-th task; its waves split K, wave w taking the blocks
+// w, w + 8, ... of every task. The wave's items (task, block) make one sequence, so the next task's first
+// loads are in flight while a task's sums are joined. Codes go through the wave's ring of S slots in LDS;
+// the tokens' rows of x come from L2 into registers, as far ahead. W is the first operand: a lane's sums
+// belong to one token (lane & 15) and four columns of h.
 
-constexpr int UP_SLOT = 4096 + 4096 + 256, UP_COPIES = 4 + 4 + 1;
+constexpr int UP_S = 3, UP_SLOT = 4096 + 256;
 
 // (One LDS variable a kernel: with several the compiler tells the copies into them apart and waits for
 // those into the rings, all of them, before any read of a ring.)
+template <int TILES>
 struct UpShared {
-    int8_t rings[NW * 2 * UP_SLOT];   // RouteScratch before the copies start
-    f32x4 red[NW][2][WAVE];
+    int8_t rings[NW * UP_S * UP_SLOT];   // RouteScratch before the copies start
+    f32x4 red[NW][TILES][2][WAVE];
     Routes rt;
 };
 
-template <int R, int TERMS>
+template <int TILES, int R, int TERMS>
 __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
-    __shared__ __attribute__((aligned(1024))) UpShared sh;
+    constexpr int S = UP_S, COPIES = 5 + 4 * TILES;
+    __shared__ __attribute__((aligned(1024))) UpShared<TILES> sh;
     static_assert(sizeof(RouteScratch) <= sizeof(sh.rings), "the routes are made before the rings are used");
     Routes& rt = sh.rt;
     auto& red = sh.red;
-    make_routes<R>(rt, *reinterpret_cast<RouteScratch*>(sh.rings), g);
+    make_routes<R, 16 * TILES>(rt, *reinterpret_cast<RouteScratch*>(sh.rings), g);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int K = g.l.K, I = g.l.I, nunits = __builtin_amdgcn_readfirstlane(rt.nunits);
     if (blockIdx.x == 0) {
-        if (threadIdx.x == 0)
-            g.space->nunits = nunits;
-        for (int i = threadIdx.x; i < nunits; i += NT)
-            g.space->units[i] = rt.units[i];
         for (int i = threadIdx.x; i < g.T * g.l.top_k; i += NT)
             g.space->pair_token[i] = rt.pair_token[i];
-        for (int i = threadIdx.x; i < K / 32; i += NT)
+        for (int i = threadIdx.x; i < K / DOWN_COLS; i += NT)
             g.space->arrived[i] = 0;
     }
     const int nkb = (K + QB - 1) / QB, cols = I / 16, tasks = nunits * cols;
@@ -328,7 +318,7 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
     if (first >= tasks)
         return;
 
-    int8_t* ring = sh.rings + wave * 2 * UP_SLOT;
+    int8_t* ring = sh.rings + wave * S * UP_SLOT;
     const int64_t blocks13 = e4m3_blocks(2 * (int64_t)I);
     const __amdgpu_buffer_rsrc_t rx = buffer_of(g.l.x, g.T * K * 2);
     const int row = lane >> 3, c0 = copy_chunk128(lane, 0), c1 = copy_chunk128(lane, 1);
@@ -339,7 +329,7 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
         int task, j;
         __amdgpu_buffer_rsrc_t gate, up;
         const float* scale;
-        int rows[4];
+        int xoff[TILES];
     } nx;
     auto enter = [&](int task) {
         nx.task = task;
@@ -353,12 +343,10 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
         nx.up = buffer_of(w + (int64_t)I * K, size);
         nx.scale = g.l.s13 + (e * blocks13 + (i0 + (lane < 32 ? 0 : I)) / QB) * nkb;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 4 * i + q;
-            nx.rows[i] = n < u.count ? rt.pair_token[u.base + n] * K * 2 : far;
-        }
+        for (int i = 0; i < TILES; ++i)   // columns past the tokens repeat the last one
+            nx.xoff[i] = (rt.pair_token[u.base + min(16 * i + r, u.count - 1)] * K + 16 * q) * 2;
     };
-    auto fetch = [&](int slot) {
+    auto fetch = [&](int slot, i32x4 (&x)[TILES][4]) {
         int8_t* to = ring + slot * UP_SLOT;
         const int b = wave + NW * nx.j, left = K - b * QB;   // blocks past the end come as zeros
         const int cut0 = 16 * c0 < left ? 0 : far, cut1 = 16 * c1 < left ? 0 : far;
@@ -367,83 +355,109 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
         buffer_to_lds16<2>(nx.gate, o1 | cut1, 0, to + 1024);
         buffer_to_lds16<2>(nx.up, o0 | cut0, 0, to + 2048);
         buffer_to_lds16<2>(nx.up, o1 | cut1, 0, to + 3072);
-        copy_rows16(rx, nx.rows, 2 * b * QB, left, lane, to + 4096);
-        global_to_lds4(nx.scale + min(b, nkb - 1), to + 8192);
+        global_to_lds4(nx.scale + min(b, nkb - 1), to + 4096);
+        // past K the codes are zeros, and x anything finite
+        const int bx = min(b, nkb - 1) * QB, half = left > 64 ? 128 : 0;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                x[i][f] = __builtin_amdgcn_raw_buffer_load_b128(rx, nx.xoff[i] + 16 * (f & 1) + (f >> 1) * half, 2 * bx, 0);
+        asm volatile("" ::: "memory");   // no load may sink past the waits that count it
         if (++nx.j == J)
             enter(nx.task + G);
     };
 
-    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+    f32x4 acc[TILES][2];
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+            acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+    };
+    clear();
+    i32x4 xv[S][TILES][4];
     enter(first);
-    fetch(0);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s, xv[s]);
     const int f0 = r * QB + ((q ^ swizzle128(r)) << 4), f1 = r * QB + (((q + 4) ^ swizzle128(r)) << 4);
-    int slot = 0;
-    for (int task = first; task < tasks; task += G) {
-        for (int j = 0; j < J; ++j) {
-            fetch(slot ^ 1);
+    const int items = ((tasks - first + G - 1) / G) * J;
+    int task = first, j = 0;
+    // in rounds of S items, the last one filled up with zeros
+    for (int it = 0; it < items; it += S) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            fetch((s + S - 1) % S, xv[(s + S - 1) % S]);
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(wait_vm(UP_COPIES));
+            __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * COPIES));
             __builtin_amdgcn_sched_barrier(0);
-            const int8_t* at = ring + slot * UP_SLOT;
+            const int8_t* at = ring + s * UP_SLOT;
             const i32x4 g0 = *reinterpret_cast<const i32x4*>(at + f0), g1 = *reinterpret_cast<const i32x4*>(at + f1);
             const i32x4 u0 = *reinterpret_cast<const i32x4*>(at + 2048 + f0);
             const i32x4 u1 = *reinterpret_cast<const i32x4*>(at + 2048 + f1);
-            const float sg = *reinterpret_cast<const float*>(at + 8192);
-            const float su = *reinterpret_cast<const float*>(at + 8192 + 128);
-            f16x8 x[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-                x[f] = rows16_fragment<f16x8>(at + 4096, r, q, f);
+            const float sg = *reinterpret_cast<const float*>(at + 4096);
+            const float su = *reinterpret_cast<const float*>(at + 4096 + 128);
             const f16x8 ga[4] = {codes_f16(g0[0], g0[1]), codes_f16(g0[2], g0[3]), codes_f16(g1[0], g1[1]), codes_f16(g1[2], g1[3])};
             const f16x8 ua[4] = {codes_f16(u0[0], u0[1]), codes_f16(u0[2], u0[3]), codes_f16(u1[0], u1[1]), codes_f16(u1[2], u1[3])};
-            f32x4 pg{0, 0, 0, 0}, pu{0, 0, 0, 0};
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                pg = __builtin_amdgcn_mfma_f32_16x16x32_f16(ga[f], x[f], pg, 0, 0, 0);
-                pu = __builtin_amdgcn_mfma_f32_16x16x32_f16(ua[f], x[f], pu, 0, 0, 0);
-            }
+            for (int i = 0; i < TILES; ++i) {
+                f32x4 pg{0, 0, 0, 0}, pu{0, 0, 0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc[0][e] = fmaf(sg, pg[e], acc[0][e]);
-                acc[1][e] = fmaf(su, pu[e], acc[1][e]);
+                for (int f = 0; f < 4; ++f) {
+                    const f16x8 x = __builtin_bit_cast(f16x8, xv[s][i][f]);
+                    pg = __builtin_amdgcn_mfma_f32_16x16x32_f16(ga[f], x, pg, 0, 0, 0);
+                    pu = __builtin_amdgcn_mfma_f32_16x16x32_f16(ua[f], x, pu, 0, 0, 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[i][0][e] = fmaf(sg, pg[e], acc[i][0][e]);
+                    acc[i][1][e] = fmaf(su, pu[e], acc[i][1][e]);
+                }
             }
             __builtin_amdgcn_s_waitcnt(WAIT_LDS);   // the slot's reads are done before it is filled again
             __builtin_amdgcn_sched_barrier(0);
-            slot ^= 1;
-        }
-        // the task's sums of all waves, joined by wave 0
-        red[wave][0][lane] = acc[0];
-        red[wave][1][lane] = acc[1];
-        acc[0] = acc[1] = f32x4{0, 0, 0, 0};
-        barrier_lds();
-        if (wave == 0) {
-            const MoeUnit u = rt.units[task / cols];
-            f32x4 gs = red[0][0][lane], us = red[0][1][lane];
+            if (++j == J && task < tasks) {
+                // the task's sums of all waves, joined by one wave a tile
 #pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                gs += red[w][0][lane];
-                us += red[w][1][lane];
-            }
-            if (r < u.count) {
-                const float p = rt.pair_p[u.base + r];
-                const int64_t to = (int64_t)(u.base + r) * I + (task % cols) * 16 + 4 * q;
-                float h[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    h[n] = p * activation<ACT_SILU>(gs[n]) * us[n];
-#pragma unroll
-                for (int k = 0; k < TERMS; ++k) {
-                    bf16x4 v;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        v[n] = (__bf16)h[n];
-                        h[n] -= (float)v[n];
-                    }
-                    *reinterpret_cast<bf16x4*>(g.h + (int64_t)k * g.T * g.l.top_k * I + to) = v;
+                for (int i = 0; i < TILES; ++i) {
+                    red[wave][i][0][lane] = acc[i][0];
+                    red[wave][i][1][lane] = acc[i][1];
                 }
+                clear();
+                barrier_lds();
+                if (wave < TILES) {
+                    const MoeUnit u = rt.units[task / cols];
+                    f32x4 gs = red[0][wave][0][lane], us = red[0][wave][1][lane];
+#pragma unroll
+                    for (int w = 1; w < NW; ++w) {
+                        gs += red[w][wave][0][lane];
+                        us += red[w][wave][1][lane];
+                    }
+                    const int n = 16 * wave + r;
+                    if (n < u.count) {
+                        const float p = rt.pair_p[u.base + n];
+                        const int64_t to = (int64_t)(u.base + n) * I + (task % cols) * 16 + 4 * q;
+                        float h[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            h[c] = p * activation<ACT_SILU>(gs[c]) * us[c];
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k) {
+                            bf16x4 v;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                v[c] = (__bf16)h[c];
+                                h[c] -= (float)v[c];
+                            }
+                            *reinterpret_cast<bf16x4*>(g.h + (int64_t)k * g.T * g.l.top_k * I + to) = v;
+                        }
+                    }
+                }
+                barrier_lds();
+                j = 0;
+                task += G;
             }
         }
-        barrier_lds();
     }
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
 }
@@ -458,7 +472,7 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
 // take twice the codes' space). A wave adds a unit's products to its own sums [token][32] in LDS; the
 // waves' sums are added at the end, and the parts' by the workgroup that comes last.
 
-constexpr int DOWN_COLS = 32, DOWN_SLOT = DOWN_COLS * QB + 256;
+constexpr int DOWN_SLOT = DOWN_COLS * QB + 256;
 
 template <int TOKENS, int S>
 struct DownShared {
@@ -691,12 +705,20 @@ template <int TERMS>
 void launch_experts(const Moe& g, hipStream_t stream) {
     const int64_t most = (int64_t)(g.T * g.l.top_k < MOE_UNITS ? g.T * g.l.top_k : MOE_UNITS) * (g.l.I / 16);
     const dim3 up((uint32_t)(most < cu_count() ? most : cu_count())), nt(NT);
-    if (g.l.E <= 64)
-        moe_up_kernel<4, TERMS><<<up, nt, 0, stream>>>(g);
-    else if (g.l.E <= 128)
-        moe_up_kernel<8, TERMS><<<up, nt, 0, stream>>>(g);
+    auto go = [&](auto tiles) {
+        constexpr int TILES = decltype(tiles)::value;
+        if (g.l.E <= 64)
+            moe_up_kernel<TILES, 4, TERMS><<<up, nt, 0, stream>>>(g);
+        else if (g.l.E <= 128)
+            moe_up_kernel<TILES, 8, TERMS><<<up, nt, 0, stream>>>(g);
+        else
+            moe_up_kernel<TILES, 32, TERMS><<<up, nt, 0, stream>>>(g);
+    };
+    // Units of 32 where an expert has more than 8 tokens on average: its codes are then rarely read twice.
+    if (g.T > 16 && g.T * g.l.top_k > 8 * g.l.E)
+        go(std::integral_constant<int, 2>{});
     else
-        moe_up_kernel<32, TERMS><<<up, nt, 0, stream>>>(g);
+        go(std::integral_constant<int, 1>{});
     const dim3 down((uint32_t)(g.l.K / DOWN_COLS * g.parts));
     if (g.T <= 16)
         moe_down_kernel<TERMS, 16, 3><<<down, nt, 0, stream>>>(g);
