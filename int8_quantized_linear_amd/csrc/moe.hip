@@ -284,7 +284,7 @@ __device__ inline bf16x8 codes_bf16(int w0, int w1) {
 // the tokens' rows of x come from L2 into registers, as far ahead. W is the first operand: a lane's sums
 // belong to one token (lane & 15) and four columns of h.
 
-constexpr int UP_S = 3, UP_SLOT = 4096 + 256;
+constexpr int UP_S = 2, UP_SLOT = 4096 + 256;
 
 // (One LDS variable a kernel: with several the compiler tells the copies into them apart and waits for
 // those into the rings, all of them, before any read of a ring.)
@@ -492,13 +492,16 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
     const int r = lane & 15, q = lane >> 4;
     const int slices = g.l.K / DOWN_COLS, slice = blockIdx.x % slices, part = blockIdx.x / slices;
     const int K = g.l.K, I = g.l.I, n0 = slice * DOWN_COLS;
-    const int nunits = __builtin_amdgcn_readfirstlane(g.space->nunits);
-    for (int i = threadIdx.x; i < nunits; i += NT)
+    const int units_load = g.space->nunits;
+    // (as many units as there can be, so that the loads do not wait for the number)
+    const int most = g.T * g.l.top_k < MOE_UNITS ? g.T * g.l.top_k : MOE_UNITS;
+    for (int i = threadIdx.x; i < most; i += NT)
         *reinterpret_cast<u32x2*>(&sh.units[i]) = *reinterpret_cast<const u32x2*>(&g.space->units[i]);
     for (int i = threadIdx.x; 4 * i < g.T * g.l.top_k; i += NT)
         reinterpret_cast<uint32_t*>(sh.pair_token)[i] = reinterpret_cast<const uint32_t*>(g.space->pair_token)[i];
     for (int i = threadIdx.x; i < NW * TOKENS * DOWN_COLS / 4; i += NT)
         reinterpret_cast<f32x4*>(sums)[i] = f32x4{0, 0, 0, 0};
+    const int nunits = __builtin_amdgcn_readfirstlane(units_load);
     __syncthreads();
     const int nib = (I + QB - 1) / QB, share = part * NW + wave, shares = g.parts * NW;
 
@@ -721,9 +724,9 @@ void launch_experts(const Moe& g, hipStream_t stream) {
         go(std::integral_constant<int, 1>{});
     const dim3 down((uint32_t)(g.l.K / DOWN_COLS * g.parts));
     if (g.T <= 16)
-        moe_down_kernel<TERMS, 16, 3><<<down, nt, 0, stream>>>(g);
+        moe_down_kernel<TERMS, 16, 2><<<down, nt, 0, stream>>>(g);
     else if (g.T <= 32)
-        moe_down_kernel<TERMS, 32, 3><<<down, nt, 0, stream>>>(g);
+        moe_down_kernel<TERMS, 32, 2><<<down, nt, 0, stream>>>(g);
     else
         moe_down_kernel<TERMS, 64, 2><<<down, nt, 0, stream>>>(g);
 }
