@@ -55,7 +55,7 @@ struct EpiArgs {
 // Where a tile's block scales lie in LDS (EL_E4M3_BLOCK; the rows' and columns' scales of the other
 // layers have no use there): per stage buffer the tile's rows' scales of the stage's block of K,
 // then W's for each 32 columns. The tile's bias stays where it is, between the second and first.
-constexpr int BLOCK_SCALES[3] = {0, 3072, 1280};   // past RING_BYTES; 1280 bytes, the third 768
+constexpr int BLOCK_SCALES[3] = {0, 3 * 1024, 1280};   // past RING_BYTES; 1280 bytes, the third 768
 
 // Operand element type: int8 codes (v_mfma_i32_32x32x32_i8, exact int32 sums) or OCP E4M3
 // fp8 codes (v_mfma_f32_32x32x64_f8f6f4, fp32 sums). The bytes move the same way (copies,

@@ -109,6 +109,7 @@ struct RouteScratch {
     uint16_t id[MOE_TOKENS][MOE_TOP_K];       // of a token, MOE_EXPERTS for none
     float p[MOE_TOKENS][MOE_TOP_K];
     uint32_t part[8];
+    __attribute__((aligned(16))) float row[NW][WAVE];   // a wave's token's logits
 };
 
 // The workspace: the routes as the second kernel needs them, arrivals at each slice of output columns,
@@ -131,37 +132,96 @@ struct Moe {
     float* sums;     // [parts][T][K]
 };
 
-template <class F>
-__device__ inline float row16(float v, F f) {
-    auto step = [&](auto ctrl) {
-        v = f(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true)));
+template <int CTRL, class T>
+__device__ inline T dpp(T v) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// f over the 16 lanes of a row, in every one of them (rotations by 8, 4, 2 and 1 lanes).
+template <class T, class F>
+__device__ inline T row16(T v, F f) {
+    v = f(v, dpp<0x128>(v));
+    v = f(v, dpp<0x124>(v));
+    v = f(v, dpp<0x122>(v));
+    return f(v, dpp<0x121>(v));
+}
+
+// Running sum over a wave's lanes, each lane's own included.
+__device__ inline uint32_t wave_scan(uint32_t v) {
+    auto add = [&](auto ctrl, auto rows) {
+        v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
     };
-    step(std::integral_constant<int, 0x128>{});   // rotations by 8, 4, 2 and 1 of 16 lanes
-    step(std::integral_constant<int, 0x124>{});
-    step(std::integral_constant<int, 0x122>{});
-    step(std::integral_constant<int, 0x121>{});
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // shifts by 1, 2, 4 and 8 in rows of 16
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // lane 15 and 47 to the next row
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // lane 31 to the upper rows
     return v;
 }
 
-__device__ inline int row16_min(int v) {
-    auto step = [&](auto ctrl) {
-        v = min(v, __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, 0xF, 0xF, true));
-    };
-    step(std::integral_constant<int, 0x128>{});
-    step(std::integral_constant<int, 0x124>{});
-    step(std::integral_constant<int, 0x122>{});
-    step(std::integral_constant<int, 0x121>{});
-    return v;
+// The experts of at most NW tokens, a wave a token and an expert a lane: each logit's rank is the number
+// of logits that are larger, of equal ones the lower experts first. One round whatever top_k is: 1 token,
+// 64 experts and top_k 8 take the kernel 8.3 us, with the rounds of search_experts 9.6.
+__device__ inline void rank_experts(RouteScratch& rs, const Moe& g) {
+    const int lane = threadIdx.x & 63, t = threadIdx.x >> 6, E = g.l.E, k = g.l.top_k;
+    if (t >= g.T)
+        return;
+    float* row = rs.row[t];
+    const float x = lane < E ? g.l.logits[(int64_t)t * E + lane] : -INFINITY;
+    const float v = x == x ? x : -INFINITY;
+    row[lane] = v;
+    asm volatile("" ::: "memory");   // the wave's LDS operations complete in order
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < (E + 3) / 4; ++j) {
+        const f32x4 other = reinterpret_cast<const f32x4*>(row)[j];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            rank += other[n] > v ? 1 : 0;
+    }
+    // equal logits share a rank: told apart where it matters
+    bool equal = false;
+    for (int n = 0; n < k; ++n)
+        equal = equal || __popcll(__ballot(rank == n && v > -INFINITY)) > 1;
+    if (equal)
+        for (int j = 0; j < E; ++j)
+            rank += row[j] == v && j < lane ? 1 : 0;
+    const unsigned long long first = __ballot(rank == 0 && v > -INFINITY);
+    const float from = first != 0 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), __builtin_ctzll(first))) : 0.0f;
+    const float p = __expf(v - from);
+    const bool chosen = rank < k && v > -INFINITY;
+    // added in search_experts' order: a token's result is the same among few tokens and among many
+    float sum = 0.0f;
+    if (g.l.renormalize) {
+        for (int n = 0; n < k; ++n) {
+            const unsigned long long at = __ballot(rank == n && chosen);
+            sum += at != 0 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), __builtin_ctzll(at))) : 0.0f;
+        }
+    } else {
+        row[lane] = p;
+        asm volatile("" ::: "memory");
+        for (int n = 0; n < WAVE; n += 16)
+            sum += row[n + (lane & 15)];
+        sum = row16(sum, [](float a, float b) { return a + b; });
+    }
+    if (chosen) {
+        rs.id[t][rank] = (uint16_t)lane;
+        rs.p[t][rank] = p / sum;
+        atomicOr(&rs.tokens[lane], 1ull << t);
+    }
+    const int taken = __popcll(__ballot(chosen));
+    if (lane >= taken && lane < k)
+        rs.id[t][lane] = MOE_EXPERTS;
 }
 
-// 16 lanes a token, R logits a lane: top_k rounds of the largest that is left. NaN is never taken,
-// nor is -infinity.
-template <int R, int UNIT>
-__device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
-    const int tid = threadIdx.x, E = g.l.E, k = g.l.top_k;
-    rs.tokens[tid] = 0;
-    __syncthreads();
-    const int l = tid & 15;
+// The same for any number of tokens: 16 lanes a token, R logits a lane, and top_k rounds of the largest that is
+// left. NaN is never taken, nor is -infinity.
+template <int R>
+__device__ inline void search_experts(RouteScratch& rs, const Moe& g) {
+    const int tid = threadIdx.x, E = g.l.E, k = g.l.top_k, l = tid & 15;
+    const auto larger = [](float a, float b) { return fmaxf(a, b); };
     for (int t0 = 0; t0 < g.T; t0 += NT / 16) {
         const int t = t0 + tid / 16;
         const float* row = g.l.logits + (int64_t)min(t, g.T - 1) * E;
@@ -172,7 +232,7 @@ __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
             v[r] = 16 * r + l < E ? row[16 * r + l] : -INFINITY;
             top = fmaxf(top, v[r]);
         }
-        top = row16(top, [](float a, float b) { return fmaxf(a, b); });
+        top = row16(top, larger);
         const float from = top == -INFINITY ? 0.0f : top;
         float all = 0.0f;
         if (!g.l.renormalize) {
@@ -188,12 +248,12 @@ __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 best = fmaxf(best, v[r]);
-            best = row16(best, [](float a, float b) { return fmaxf(a, b); });
+            best = row16(best, larger);
             int at = MOE_EXPERTS;
 #pragma unroll
             for (int r = R - 1; r >= 0; --r)
                 at = v[r] == best ? 16 * r + l : at;
-            at = row16_min(at);
+            at = row16(at, [](int a, int b) { return min(a, b); });
             at = best == -INFINITY ? MOE_EXPERTS : at;
             const float p = best == -INFINITY ? 0.0f : __expf(best - from);
             chosen += p;
@@ -212,6 +272,18 @@ __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
                 atomicOr(&rs.tokens[my_id], 1ull << t);
         }
     }
+}
+
+// At most 16 R experts.
+template <int R, int UNIT>
+__device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
+    const int tid = threadIdx.x, k = g.l.top_k;
+    rs.tokens[tid] = 0;
+    __syncthreads();
+    if (R == 4 && g.T <= NW)
+        rank_experts(rs, g);
+    else
+        search_experts<R>(rs, g);
     __syncthreads();
     // the experts' first pairs and units: a running sum over the experts, one a thread
     static_assert(NT == MOE_EXPERTS, "one expert a thread");
@@ -219,12 +291,7 @@ __device__ inline void make_routes(Routes& rt, RouteScratch& rs, const Moe& g) {
     const int pairs = __popcll(m);
     // pairs, units of 16 and units of UNIT in one number
     const uint32_t own = (uint32_t)pairs << 20 | (uint32_t)((pairs + 15) / 16) << 10 | (uint32_t)((pairs + UNIT - 1) / UNIT);
-    uint32_t sum = own;
-#pragma unroll
-    for (int o = 1; o < WAVE; o <<= 1) {
-        const uint32_t up = __shfl_up(sum, o, WAVE);
-        sum += (tid & 63) >= o ? up : 0;
-    }
+    uint32_t sum = wave_scan(own);
     if ((tid & 63) == 63)
         rs.part[tid >> 6] = sum;
     __syncthreads();
@@ -354,7 +421,7 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
         buffer_to_lds16<2>(nx.gate, o0 | cut0, 0, to);
         buffer_to_lds16<2>(nx.gate, o1 | cut1, 0, to + 1024);
         buffer_to_lds16<2>(nx.up, o0 | cut0, 0, to + 2048);
-        buffer_to_lds16<2>(nx.up, o1 | cut1, 0, to + 3072);
+        buffer_to_lds16<2>(nx.up, o1 | cut1, 0, to + 3 * 1024);
         global_to_lds4(nx.scale + min(b, nkb - 1), to + 4096);
         // past K the codes are zeros, and x anything finite
         const int bx = min(b, nkb - 1) * QB, half = left > 64 ? 128 : 0;
