@@ -619,6 +619,20 @@ def linear_e4m3(x, wq, w_scale, bias=None, act: str = "none", out_dtype=None):
 
 # ------------------------------------------- E4M3 codes with a scale for each block of 128
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call_on(index: int, fn: str, *args):
+    """The call with the tensors' device current: stream 0 names every device's default stream."""
+    if _current_device() == index:
+        st = getattr(lib, fn)(*args)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(lib, fn)(*args)
+    if st != 0:
+        raise QLError(fn, st)
+
+
 def _blocks(n: int) -> int:
     """Blocks of 128 that n values make, the last one possibly shorter."""
     return -(-n // 128)
@@ -649,8 +663,7 @@ def quantize_per_row_block_e4m3(x: torch.Tensor, xq: Optional[torch.Tensor] = No
     if x_scale is None:
         x_scale = x.new_empty((_blocks(K), M), dtype=torch.float32)
     sp = _same(x_scale, "x_scale", torch.float32, (_blocks(K), M), index)
-    _status("quantize_per_row_block_e4m3", lib.quantize_per_row_block_e4m3(
-        xp, dt, M, K, xq.data_ptr(), sp, _raw_stream(index)))
+    _call_on(index, "quantize_per_row_block_e4m3", xp, dt, M, K, xq.data_ptr(), sp, _raw_stream(index))
     return xq, x_scale
 
 
@@ -665,7 +678,9 @@ def quantize_weight_block_e4m3(w_nk: torch.Tensor):
     E = w_nk.shape[0] if w_nk.dim() == 3 else 1
     wq = torch.empty(w_nk.shape, dtype=torch.float8_e4m3fn, device=w_nk.device)
     ws = torch.empty((*w_nk.shape[:-2], _blocks(N), _blocks(K)), dtype=torch.float32, device=w_nk.device)
-    _call("quantize_weight_block_e4m3", _ptr(w_nk), E, K, N, _ptr(wq), _ptr(ws), _stream(w_nk))
+    index = w_nk.get_device()
+    _call_on(index, "quantize_weight_block_e4m3", w_nk.data_ptr(), E, K, N, wq.data_ptr(), ws.data_ptr(),
+             _raw_stream(index))
     return wq, ws
 
 
@@ -691,9 +706,8 @@ def gemm_e4m3_block(xq, x_scale, wq, w_scale, bias=None, act: str = "none", out_
         yp = y.data_ptr()
     else:
         yp = _same(y, "y", out_dtype, (M, N), index)
-    _status("gemm_e4m3_block", lib.gemm_e4m3_block(
-        xp, sp, wp, tp, bp, _act_code(act), yp, QL_F16 if out_dtype is torch.float16 else QL_F32, M, N, K,
-        _raw_stream(index)))
+    _call_on(index, "gemm_e4m3_block", xp, sp, wp, tp, bp, _act_code(act), yp,
+             QL_F16 if out_dtype is torch.float16 else QL_F32, M, N, K, _raw_stream(index))
     return y
 
 
@@ -719,7 +733,7 @@ def moe_router(x, w, logits=None):
         lp = logits.data_ptr()
     else:
         lp = _same(logits, "logits", torch.float32, (T, E), index)
-    _status("moe_router", lib.moe_router(xp, wp, lp, T, E, K, _raw_stream(index)))
+    _call_on(index, "moe_router", xp, wp, lp, T, E, K, _raw_stream(index))
     return logits
 
 
@@ -762,9 +776,9 @@ def moe_e4m3_block(x, logits, w13, s13, w2, s2, top_k: int, renormalize: bool = 
         op = _same(out, "out", out_dtype, (T, K), index)
     need = _moe_workspace(T, top_k, K, I)
     ws = w13.new_empty((need,), dtype=torch.uint8)   # of the current stream, as the kernels are
-    _status("moe_e4m3_block", lib.moe_e4m3_block(
-        xp, lp, wp, sp, vp, tp, op, QL_F16 if out_dtype is torch.float16 else QL_F32, T, E, top_k, K, I,
-        1 if renormalize else 0, ws.data_ptr(), need, _raw_stream(index)))
+    _call_on(index, "moe_e4m3_block", xp, lp, wp, sp, vp, tp, op,
+             QL_F16 if out_dtype is torch.float16 else QL_F32, T, E, top_k, K, I, 1 if renormalize else 0,
+             ws.data_ptr(), need, _raw_stream(index))
     return out
 
 
