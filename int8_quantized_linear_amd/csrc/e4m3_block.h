@@ -39,6 +39,10 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
 
+// Codes that are read once are loaded non-temporally (AUX 2) where rows are whole lines of 128 bytes.
+// Else a line holds codes of two blocks, and is worth keeping until the second is read.
+inline __host__ __device__ bool whole_lines(int row_bytes) { return row_bytes % 128 == 0; }
+
 // s_waitcnt immediates: at most n vector-memory operations pending, LDS operations left alone;
 // and no LDS operation pending, vector memory left alone.
 constexpr int wait_vm(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | (((n >> 4) & 3) << 14); }

@@ -183,3 +183,33 @@ def test_refusals(ql):
     with pytest.raises(TypeError):
         ql.moe_router(x, x.float())
     assert ql.moe_router(x[:0], x).shape == (0, 3)
+
+
+# many tokens an expert and enough codes: the kernels whose eight waves share the tokens' operand
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("T,E,k,K,I", [(33, 3, 2, 2048, 8256), (64, 6, 2, 1984, 4160), (70, 7, 7, 1600, 4096),
+                                       (20, 2, 1, 4096, 12352), (64, 65, 16, 2112, 512)])
+def test_experts_with_many_tokens(ql, T, E, k, K, I, f16):
+    """Against 64 bits, with experts that all tokens, few and none take; every token as in a call of its own."""
+    assert T * k >= 8 * E and E * K * I >= 40 << 20 and E * -(-I // 128) >= 192
+    rng = np.random.default_rng(T + K)
+    q = lambda *s: ql.quantize_weight_block_e4m3(dev(rng.standard_normal(s, dtype=np.float32) / np.float32(np.sqrt(s[-1]))))  # noqa: E731,E501
+    (w13, s13), (w2, s2) = q(E, 2 * I, K), q(E, K, I)
+    x = rng.standard_normal((T, K)).astype(np.float16)
+    lg = (rng.standard_normal((T, E)) * 2).astype(np.float32)
+    lg[:, 0] += 4
+    lg[:, E - 1] -= 5
+    lg[T // 3] = -np.inf
+    dt = torch.float16 if f16 else torch.float32
+    out = Guarded((T, K), dt)
+    args = (w13, s13, w2, s2, k, f16, dt)
+    ql.moe_e4m3_block(dev(x), dev(lg), *args, out.view)
+    out.check()
+    some = [0, 1, T // 3, T // 2, T - 1]
+    for t in some:
+        assert torch.equal(ql.moe_e4m3_block(dev(x[t:t + 1]), dev(lg[t:t + 1]), *args), out.view[t:t + 1])
+    inp = (x[some], lg[some], *(host(a.view(torch.uint8)) if a.dtype is not torch.float32 else host(a) for a in (w13, s13, w2, s2)))
+    want, err = ref.moe64(*inp, k, f16)
+    half, least = (2.0 ** -11, 2.0 ** -25) if f16 else (2.0 ** -24, 1e-37)
+    diff = np.abs(host(out.view)[some].astype(np.float64) - want)
+    assert (diff <= err * (1 + half) + half * np.abs(want) + least).all()
