@@ -59,7 +59,9 @@ __device__ inline void store_codes_e4m3(uint8_t* q, const float* v, float s, flo
         b = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], b, true);
         w[j] = (uint32_t)b;
     }
-    if constexpr (E == 8)
+    if constexpr (E == 16)
+        *reinterpret_cast<u32x4*>(q) = u32x4{w[0], w[1], w[2], w[3]};
+    else if constexpr (E == 8)
         *reinterpret_cast<u32x2*>(q) = u32x2{w[0], w[1]};
     else
         *reinterpret_cast<uint32_t*>(q) = w[0];
