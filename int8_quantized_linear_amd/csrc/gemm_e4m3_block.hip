@@ -4,6 +4,12 @@
 //
 // The inner sums run on the fp8 matrix cores, from zero for each block; the block's sum is then
 // added to the output's fp32 sum with its scales, one multiply-add an output and block.
+//
+// Few rows are bound by the read of W (1 x 11008 x 4096: 8.9 us, 5.1 TB/s), many by the matrix cores at the
+// chip's power limit and the multiply-adds beside them (2048 x 11008 x 4096: 93 us, 1990 TFLOP/s; a library
+// product of 8192 x 8192 x 8192 on such codes without block scales reaches 2910). Between, a tile's CU is
+// bound by LDS (128 x 128 tiles: 0.5 us a block of K, a fourth stage buffer gave nothing) and the chip by
+// how many tiles there are: 333 x 4096 x 2048 makes 96 of them and takes 13 us.
 #include "e4m3_block.h"
 #include "gemm_w8a8_tile.h"
 

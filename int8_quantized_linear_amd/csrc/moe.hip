@@ -9,12 +9,19 @@
 // kernels: the gated products of every (token, expert) pair into the workspace, and the sums over
 // the experts. Codes become fp16 (first kernel, beside x) or bf16 (second kernel) exactly, the
 // products run on the matrix cores with fp32 sums from zero for each block of 128, and the block's
-// scale is applied in fp32. h is kept as two bf16 terms (16 bits of significand, fp32's range): one
-// rounding of relative size 2^-17 that its products see.
+// scale is applied in fp32. h is kept as two bf16 terms for fp16 outputs (16 bits of significand with
+// fp32's range: one rounding of relative size 2^-17 that its products see), three for fp32 outputs
+// (2^-25; the outputs are then 4e-7 of their norm from 64 bits).
 //
-// A wave copies the blocks of 128 that it takes, codes and the other operand's rows, straight into its
-// own ring in LDS, one block ahead, and needs no barrier until the waves' sums are joined. The order of
-// every sum is fixed, whatever the other tokens are.
+// Two pairs of kernels. Where experts have few tokens, a wave copies the blocks of 128 that it takes
+// straight into its own ring in LDS, one block ahead, has the other operand's few rows in registers, and
+// needs no barrier until the waves' sums are joined. Where they have many, the tokens' operand goes
+// through LDS once for eight waves and the codes through registers. launch_experts has the rule. The
+// order of every sum is the same in both, whatever the other tokens are.
+//
+// 5 tokens of 8 large experts (2 of them each, K 4096, I 7168): 99 us, 5.35 TB/s of codes; 64 tokens of 64
+// experts (6 each, K 2048, I 1408): 125 us, 4.4 TB/s; one token of 64 (8, K 2048, I 1536): 27 us, of which
+// about 13 are the two kernels' fixed part: launch, the routes, a first load's latency, the join.
 #include "e4m3_block.h"
 
 namespace ql {
@@ -86,7 +93,7 @@ __global__ __launch_bounds__(RW* WAVE) void moe_router_kernel(const _Float16* __
 // Every workgroup of the first kernel works the routes out for itself from the logits (it would
 // wait as long for another to do it). Pairs (expert, token) are numbered expert by expert, tokens
 // in order, and cut into units of one expert and up to 16 pairs, the columns of a matrix instruction
-// (up to 32 in the first kernel where experts have many).
+// (all of them, and up to 32 in the second kernel, where experts have many).
 
 constexpr int DOWN_COLS = 32;   // output columns of a workgroup of the second kernel
 constexpr int DOWN_WIDE_UNIT = 32;   // pairs of a unit there where experts have many
@@ -406,13 +413,14 @@ __device__ inline f32x4 part_sums(const Moe& g, int part, int t, int col) {
 
 // ------------------------------------------------------------------------ the gated products
 //
-// A task is a unit and 16 columns of h: 16 rows of W1 and 16 of W3 against the unit's tokens, TILES x 16
-// of them at most. A workgroup takes every gridDim-th task; its waves split K, wave w taking the blocks
+// A task is a unit and 16 columns of h: 16 rows of W1 and 16 of W3 against the unit's tokens. A workgroup takes every gridDim-th task; its waves split K, wave w taking the blocks
 // w, w + 8, ... of every task. The wave's items (task, block) make one sequence, so the next task's first
 // loads are in flight while a task's sums are joined. Codes go through the wave's ring of S slots in LDS;
 // the tokens' rows of x come from L2 into registers, as far ahead. W is the first operand: a lane's sums
 // belong to one token (lane & 15) and four columns of h.
 
+// (Two slots; with three, one token of 64 experts takes 29.6 us instead of 27.3, 64 tokens 126 instead of
+// 127: eight waves have enough loads under way, and more start later.)
 constexpr int UP_S = 2, UP_SLOT = 4096 + 256;
 
 // (One LDS variable a kernel: with several the compiler tells the copies into them apart and waits for
@@ -1213,7 +1221,9 @@ void launch_experts(const Moe& g, hipStream_t stream) {
 }
 
 // Workgroups that share a slice of output columns, so that the slices of narrow layers fill the chip's
-// 256 CUs.
+// 256 CUs, once. Filling half / all of them / twice as many workgroups, the layer's us at T, E, top_k, K, I:
+// 1 64 8 2048 1536 28.2 / 27.3 / 30.5, 5 8 2 4096 7168 119 / 100 / 104, 64 64 6 2048 1408 151 / 127 / 133.
+// (A rule on K alone: the order of a token's sums must not depend on the batch, nor on the card.)
 int parts_of(int K) {
     int p = 1;
     while (p < 8 && 2 * p * (K / DOWN_COLS) <= 256)
