@@ -468,6 +468,7 @@ ql_status attention_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t k
  * nb = ceil(N / 128) blocks of N:
  *   activations  codes [M,K], scales fp32 [kb][M] (a block's scales of all rows together)
  *   weights      codes W [K,N] column-major ([N][K]), scales fp32 [nb][kb], one for 128 x 128
+ * `stream` belongs to the current device, as the arrays do.
  *
  * Activations: per row m and block b, with quantize_per_row_e4m3's arithmetic in the block:
  *   a = max_{k in b} |x[m,k]|,  x_scale[b][m] = max(a, 1e-10) / 448
@@ -521,7 +522,7 @@ ql_status moe_router(const void* x, const void* w, float* logits, int64_t T, int
  * not allowed.
  * Weights are E4M3 codes with a scale for each 128 x 128 block, as quantize_weight_block_e4m3 makes
  * them. They enter fp16 (W1, W3) or bf16 (W2) products exactly, with fp32 sums; h is kept as two bf16
- * terms (relative error 2^-17).
+ * terms for fp16 outputs (relative error 2^-17), as three for fp32 outputs (2^-25).
  *
  * x       [T,K] fp16 row-major
  * logits  fp32 [T][E]
@@ -532,8 +533,9 @@ ql_status moe_router(const void* x, const void* w, float* logits, int64_t T, int
  * workspace, workspace_bytes  at least what moe_e4m3_block_workspace_bytes says (else QL_ERR_SHAPE),
  *         16-byte aligned. Its contents need not be set, and are not kept.
  * Requires 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I > 0, multiples of 64 and <= 131008.
- * Every token's result is the same whatever the other tokens are. Weights of chosen experts are read
- * once for each 64 tokens: longer batches run, in launches of 64.
+ * Every token's result is the same, bit for bit, whatever and however many the other tokens are; a
+ * token's NaN and infinities stay in its row. Weights of experts that no token takes are not read, those
+ * of the others once for each 64 tokens or so: longer batches run, in launches of 64.
  */
 ql_status moe_e4m3_block(const void* x, const float* logits, const uint8_t* w13, const float* s13,
                          const uint8_t* w2, const float* s2, void* out, ql_dtype out_dtype, int64_t T,

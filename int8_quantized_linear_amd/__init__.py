@@ -751,8 +751,8 @@ def moe_e4m3_block(x, logits, w13, s13, w2, s2, top_k: int, renormalize: bool = 
     softmax over all experts (over the chosen ones, if renormalize):
     out [T, K] = sum_j p_j W2[e_j] (silu(W1[e_j] x) * (W3[e_j] x)), fp16 or fp32. w13 are codes
     (float8_e4m3fn or uint8) [E, 2 I, K], W1's rows before W3's, w2 codes [E, K, I], both with a
-    scale for each 128 x 128 block, as quantize_weight_block_e4m3 returns them. Meant for up to 64
-    tokens; longer batches run in launches of 64."""
+    scale for each 128 x 128 block, as quantize_weight_block_e4m3 returns them. A token's result does
+    not depend on the others. Meant for up to 64 tokens; longer batches run in launches of 64."""
     wp, vp = _codes_e4m3(w13, "w13", 3), _codes_e4m3(w2, "w2", 3)
     E, I2, K = w13.shape
     I = I2 // 2
