@@ -220,7 +220,7 @@ __device__ inline void issue_scales(const float* xs, const float* ws, const floa
     lds_copy4(ws + min(n0 + i, N - 1), sc + 1024);
     lds_copy4((bias != nullptr ? bias : ws) + min(n0 + i, N - 1), sc + 2048);
     if (epi.x_zero != nullptr) {
-        lds_copy4(epi.x_zero + min(m0 + i, M - 1), sc + 3072);
+        lds_copy4(epi.x_zero + min(m0 + i, M - 1), sc + 3 * 1024);
         lds_copy4(epi.colsum + min(n0 + i, N - 1), sc + 4096);
     }
     if (epi.out_scale != nullptr)   // int8 output (never with zero points): the same slot

@@ -213,3 +213,16 @@ def test_experts_with_many_tokens(ql, T, E, k, K, I, f16):
     half, least = (2.0 ** -11, 2.0 ** -25) if f16 else (2.0 ** -24, 1e-37)
     diff = np.abs(host(out.view)[some].astype(np.float64) - want)
     assert (diff <= err * (1 + half) + half * np.abs(want) + least).all()
+
+
+def test_many_tokens_and_no_expert(ql):
+    """The wide kernels where every logit masks its expert, and where one token has one."""
+    T, E, K, I = 32, 4, 2048, 6144
+    q = lambda *s: ql.quantize_weight_block_e4m3(torch.randn(s, device="cuda") / s[-1] ** 0.5)  # noqa: E731
+    (w13, s13), (w2, s2) = q(E, 2 * I, K), q(E, K, I)
+    x, lg = torch.randn(T, K, device="cuda").half(), torch.full((T, E), float("-inf"), device="cuda")
+    assert not host(ql.moe_e4m3_block(x, lg, w13, s13, w2, s2, 2)).any()
+    lg[9, 3] = -2
+    out = ql.moe_e4m3_block(x, lg, w13, s13, w2, s2, 2)
+    assert torch.equal(out[9:10], ql.moe_e4m3_block(x[9:10], lg[9:10], w13, s13, w2, s2, 2)) and host(out[9]).any()
+    assert not host(out[:9]).any() and not host(out[10:]).any()
