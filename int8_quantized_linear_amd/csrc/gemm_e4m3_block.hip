@@ -7,9 +7,8 @@
 //
 // Few rows are bound by the read of W (1 x 11008 x 4096: 8.9 us, 5.1 TB/s), many by the matrix cores at the
 // chip's power limit and the multiply-adds beside them (2048 x 11008 x 4096: 93 us, 1990 TFLOP/s; a library
-// product of 8192 x 8192 x 8192 on such codes without block scales reaches 2910). Between, a tile's CU is
-// bound by LDS (128 x 128 tiles: 0.5 us a block of K, a fourth stage buffer gave nothing) and the chip by
-// how many tiles there are: 333 x 4096 x 2048 makes 96 of them and takes 13 us.
+// product of 8192 x 8192 x 8192 on such codes without block scales reaches 2910). Between, by what a CU's
+// copies bring and how many CUs have a tile (333 x 4001 x 2112: 12.6 us).
 #include "e4m3_block.h"
 #include "gemm_w8a8_tile.h"
 
@@ -154,14 +153,127 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
         for (int e = 0; e < 4; ++e)
             o[e] = (OutT)activated<YF16>(t[e] + (g.bias != nullptr && n + e < g.N ? g.bias[n + e] : 0.0f), g.act);
         OutT* to = reinterpret_cast<OutT*>(g.y) + (int64_t)m * g.N + n;
-        if ((g.N & 3) == 0) {
-            if (n < g.N)
-                *reinterpret_cast<Out4*>(to) = o;
+        if (n + 4 <= g.N) {
+            typedef Out4 __attribute__((aligned(2))) Piece;   // rows start at any element
+            *reinterpret_cast<Piece*>(to) = o;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (n + e < g.N)
                     to[e] = o[e];
+        }
+    }
+}
+
+// Rows between: tiles of 64 x 64 on four waves, 32 x 32 each, up to three workgroups a CU. A stage is a block
+// of K, copied straight into a ring of S stages that the waves share; one barrier a stage shows that all
+// copies of it have landed and that all waves have read the one before, whose place is then filled. X's
+// scales come into registers, one a lane. Outputs leave through LDS in whole 16-byte pieces of a row.
+//
+// A CU takes 40 to 55 GB/s of such copies here (whatever the tile, and with three stages or four), so small
+// tiles on many CUs win: us for 64 x 64, 64 x 128, 128 x 64 of this kernel and 128 x 128 below
+//   333 x 4001 x 2112  12.6 14.6 13.8 14.8      512 x 4096 x 4096   18.8 22.0 21.0 20.3
+//   256 x 4096 x 4096  14.6 21.0 20.1 19.7      1024 x 4096 x 4096  33.7 30.7 30.5 24.3
+// Reading the next stage's operands from LDS under this one's products changed nothing.
+template <bool YF16>
+__global__ __launch_bounds__(256) void gemm_block_mid_kernel(BlockGemm g) {
+    constexpr int S = 3, TILE = 64, X_BYTES = TILE * QB, STAGE = 2 * TILE * QB;
+    constexpr int NC = 2 * TILE / 32, COPIES = NC + 1;   // of a wave
+    using OutT = typename std::conditional<YF16, _Float16, float>::type;
+    using Out4 = OutT __attribute__((ext_vector_type(4)));
+    constexpr int PITCH = TILE * (int)sizeof(OutT) + 16;
+    static_assert(TILE * PITCH <= S * STAGE, "the outputs fit the ring");
+    __shared__ __attribute__((aligned(1024))) int8_t smem[S * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 1, wn = wave >> 1, lr = lane & 31, lh = lane >> 5;
+    // tiles of the same columns of W one after another on one XCD
+    const int tiles_m = (g.rows + TILE - 1) / TILE, tile = xcd_remap(blockIdx.x, gridDim.x);
+    const int m0 = tile % tiles_m * TILE, n0 = tile / tiles_m * TILE;
+    const int K = g.K, nkb = (K + QB - 1) / QB, far = 0x40000000;
+
+    const __amdgpu_buffer_rsrc_t rw = buffer_of(g.wq + (int64_t)n0 * K, min(g.N - n0, TILE) * K);
+    const __amdgpu_buffer_rsrc_t rx = buffer_of(g.xq + (int64_t)m0 * K, min(g.rows - m0, TILE) * K);
+    // wave w copies the groups of 8 rows w, w + 4, ... of X's rows and then W's
+    const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+    auto fetch = [&](int b, int slot, float& xs) {
+        int8_t* to = smem + slot * STAGE + 1024 * wave;
+        const int at = row * K + 16 * chunk + b * QB, cut = 16 * chunk < K - b * QB ? 0 : far;   // past K: zeros
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            buffer_to_lds16(i < 2 ? rx : rw, (at + 32 * (i & 1) * K) | cut, 0, to + 4096 * i);
+        xs = g.xs[(int64_t)min(b, nkb - 1) * g.M + min(m0 + 32 * wm + lr, g.rows - 1)];
+        asm volatile("" ::: "memory");   // no load may sink past the waits that count it
+    };
+    const float* wrow = g.ws + (int64_t)(n0 / QB) * nkb;
+    auto scales_from = [&](int b) { return wrow[min(b + lane, nkb - 1)]; };
+    float wsc = scales_from(0);
+    asm volatile("" : "+v"(wsc));
+
+    f32x16 acc{};
+    float xs[S];
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s, s, xs[s]);
+    int at[4];   // of 16 bytes k in a fragment's row
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        at[k] = lr * QB + (((2 * k + lh) ^ swizzle128(lr)) << 4);
+    // in rounds of S stages, the last one filled up with zeros
+    for (int b0 = 0; b0 < nkb; b0 += S) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int b = b0 + s;
+            __builtin_amdgcn_s_waitcnt(wait_vm((S - 2) * COPIES) & WAIT_LDS);
+            barrier_no_fence();
+            if (b > 0 && (b & 63) == 0) {
+                wsc = scales_from(b);
+                asm volatile("" : "+v"(wsc));
+            }
+            fetch(b + S - 1, (s + S - 1) % S, xs[(s + S - 1) % S]);
+            __builtin_amdgcn_sched_barrier(0);
+            const int8_t *xp = smem + s * STAGE + 32 * wm * QB, *wp = smem + s * STAGE + X_BYTES + 32 * wn * QB;
+            i32x8 x[2], w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                w[k] = cat8(*reinterpret_cast<const i32x4*>(wp + at[2 * k]), *reinterpret_cast<const i32x4*>(wp + at[2 * k + 1]));
+                x[k] = cat8(*reinterpret_cast<const i32x4*>(xp + at[2 * k]), *reinterpret_cast<const i32x4*>(xp + at[2 * k + 1]));
+            }
+            f32x16 p{};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[k], x[k], p, 0, 0, 0, 0, 0, 0);
+            const float sc = xs[s] * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wsc), b & 63));
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[e] = fmaf(sc, p[e], acc[e]);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm(0) & WAIT_LDS);
+    barrier_no_fence();
+    // element e of a lane is row lr, column 8 (e / 4) + 4 lh + e % 4
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int c = 32 * wn + 8 * q + 4 * lh;
+        Out4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = (OutT)activated<YF16>(acc[4 * q + e] + (g.bias != nullptr ? g.bias[min(n0 + c + e, g.N - 1)] : 0.0f), g.act);
+        *reinterpret_cast<Out4*>(smem + (32 * wm + lr) * PITCH + c * (int)sizeof(OutT)) = o;
+    }
+    __syncthreads();
+    constexpr int VEC = 16 / sizeof(OutT), PIECES = TILE / VEC;
+    for (int i = threadIdx.x; i < TILE * PIECES; i += 256) {
+        const int m = m0 + i / PIECES, n = n0 + i % PIECES * VEC;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(smem + i / PIECES * PITCH + i % PIECES * 16);
+        OutT* to = reinterpret_cast<OutT*>(g.y) + (int64_t)m * g.N + n;
+        if (m < g.rows && n + VEC <= g.N) {
+            typedef u32x4 __attribute__((aligned(2))) Piece;   // rows start at any element
+            *reinterpret_cast<Piece*>(to) = v;
+        } else if (m < g.rows) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (n + e < g.N)
+                    to[e] = reinterpret_cast<const OutT*>(&v)[e];
         }
     }
 }
@@ -197,14 +309,15 @@ __global__ __launch_bounds__(64 * NWAVES, 1) void gemm_block_tile_kernel(BlockGe
     }
 }
 
-// The kernels to choose from: few-row kernels with NB x 16 columns and MB x 16 rows a workgroup, and
-// tiles. A call takes rounds of as many workgroups as the chip holds at once, each about a + b * blocks
+// The kernels to choose from: few-row kernels with NB x 16 columns and MB x 16 rows a workgroup, tiles, and
+// the kernel between. A call takes rounds of as many workgroups as the chip holds at once, each about a + b * blocks
 // of K us long; the least product is chosen. a and b are fits to warm times on MI355X of 60 shapes
 // (M 64-1024, N 1024-14336, K 1024-11008) and of M 1-64 from cold memory; the choices among them are within 5%
 // of the best. Some of both sides, us (chosen first):
 //   1 x 11008 x 4096     2x1 12.0, 1x1 14.1 (cold)     64 x 4096 x 4096    2x2 8.0, 1x2 11.3, 128x128 18.3
-//   32 x 11008 x 4096    4x2 12.7, 1x2 15.8            128 x 4096 x 4096   2x4 10.4, 4x4 15.3, 128x128 18.2
-//   96 x 11008 x 4096    128x128 19.1, 2x4 28.0        256 x 4096 x 4096   4x4 15.0, 128x128 18.3
+//   32 x 11008 x 4096    4x2 12.7, 1x2 15.8            128 x 4096 x 4096   2x4 10.4, 128x128 18.2
+//   96 x 11008 x 4096    128x128 19.1, 2x4 28.0        256 x 4096 x 4096   64x64 14.6, 128x128 19.7
+//   from cold memory: 512 x 4096 x 4096 64x64 18.8, 128x128 20.3; 150 x 2000 x 8192 2x4 19.6, 64x64 23.8
 //   333 x 11008 x 4096   128x192 27.4, 128x128 37.9    1024 x 11008 x 4096 256x192 45, 128x192 57, 128x128 63
 struct Choice {
     int nb, mb, waves, slots;   // few-row kernels; 0: tiles
@@ -215,13 +328,14 @@ struct Choice {
 constexpr Choice CHOICES[] = {
     {1, 1, 8, 2, 16, 16, 2, 1.4f, 0.13f},  {2, 1, 4, 3, 16, 32, 2, 2.0f, 0.20f},   {1, 2, 8, 2, 32, 16, 1, 1.8f, 0.12f},
     {2, 2, 8, 2, 32, 32, 1, 3.1f, 0.152f}, {4, 2, 4, 3, 32, 64, 1, 3.8f, 0.224f},  {2, 4, 4, 2, 64, 32, 1, 3.45f, 0.217f},
-    {4, 4, 4, 2, 64, 64, 1, 5.0f, 0.311f}, {0, 0, 0, 0, 128, 128, 1, 5.0f, 0.56f}, {0, 0, 0, 0, 128, 192, 1, 7.4f, 0.65f},
-    {0, 0, 0, 0, 256, 192, 1, 7.0f, 1.0f},
+    {0, 0, 0, 0, 128, 128, 1, 5.0f, 0.56f}, {0, 0, 0, 0, 128, 192, 1, 7.4f, 0.65f}, {0, 0, 0, 0, 256, 192, 1, 7.0f, 1.0f},
 };
-constexpr int FEW = 7, SMALL128 = 7, SMALL192 = 8, BIG = 9, MIXED = 10;
+constexpr int FEW = 6, SMALL128 = 6, SMALL192 = 7, BIG = 8, MIXED = 9, MID = 10;
+// gemm_block_mid_kernel with one workgroup a CU, and with two
+constexpr Choice MID_ONE{0, 0, 0, 0, 64, 64, 1, 4.7f, 0.31f}, MID_TWO{0, 0, 0, 0, 64, 64, 2, 5.5f, 0.404f};
 
 struct Chosen {
-    int kernel;       // index into CHOICES; MIXED: whole rounds of big tiles, then 128 x 192
+    int kernel;       // index into CHOICES; MIXED: whole rounds of big tiles, then 128 x 192; or MID
     int big_panels;   // columns of big tiles
 };
 
@@ -240,6 +354,12 @@ Chosen choose(int64_t M, int64_t N, int64_t K) {
             least = t;
             best.kernel = i;
         }
+    }
+    const int64_t mid = tiles(MID_ONE, N);
+    const float mid_cost = cost(MID_ONE, mid) < cost(MID_TWO, mid) ? cost(MID_ONE, mid) : cost(MID_TWO, mid);
+    if (mid_cost < least) {
+        least = mid_cost;
+        best.kernel = MID;
     }
     // whole rounds of big tiles, and small ones for the columns that would make a last, short round
     const int64_t big = tiles(CHOICES[BIG], N), panels = big / cu_count() * cu_count() / cdiv(M, 256);
@@ -280,7 +400,14 @@ void launch_few(const BlockGemm& g, int c, hipStream_t stream) {
     of(std::integral_constant<int, 3>{});
     of(std::integral_constant<int, 4>{});
     of(std::integral_constant<int, 5>{});
-    of(std::integral_constant<int, 6>{});
+}
+
+template <bool YF16>
+void launch_mid(const BlockGemm& g, hipStream_t stream) {
+    BlockGemm p = g;
+    p.rows = (int)g.M;
+    const int64_t tiles = (g.M + 63) / 64 * ((g.N + 63) / 64);
+    gemm_block_mid_kernel<YF16><<<dim3((uint32_t)tiles), dim3(256), 0, stream>>>(p);
 }
 
 template <int YMODE>
@@ -308,7 +435,9 @@ ql_status launch_gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const 
                                  hipStream_t stream) {
     const BlockGemm g{xq, x_scale, wq, w_scale, bias, y, 0, (int)N, (int)K, act, M};
     const Chosen c = choose(M, N, K);
-    if (c.kernel < FEW)
+    if (c.kernel == MID)
+        (y_f16 ? launch_mid<true> : launch_mid<false>)(g, stream);
+    else if (c.kernel < FEW)
         (y_f16 ? launch_few<true> : launch_few<false>)(g, c.kernel, stream);
     else
         (y_f16 ? launch_tiles<Y_F16> : launch_tiles<Y_F32>)(g, c, stream);
