@@ -497,7 +497,7 @@ ql_status quantize_weight_block_e4m3(const float* w, int64_t E, int64_t K, int64
  * long as each block's product and the sum stay in fp32's range.
  * xq [M,K], x_scale fp32 [kb][M], wq [N][K], w_scale fp32 [nb][kb], bias fp32 [N] or NULL; y [M,N]
  * row-major, fp32 or fp16; act as ql_activation.
- * Requires K > 0, K % 64 == 0, K <= 131008 and N <= 2^23.
+ * Requires K > 0, K % 64 == 0, K <= 131008, M <= 2^30 and N <= 2^23.
  */
 ql_status gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t* wq, const float* w_scale,
                           const float* bias, ql_activation act, void* y, ql_dtype y_dtype, int64_t M,

@@ -571,6 +571,8 @@ ql_status gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t
         return QL_ERR_DTYPE;
     if (act != QL_ACT_NONE && act != QL_ACT_GELU && act != QL_ACT_SILU)
         return QL_ERR_DTYPE;
+    if (M > (int64_t)1 << 30)   // a launch's threads stay below 2^32
+        return QL_ERR_SHAPE;
     ql_status st = check_w8a8(reinterpret_cast<const int8_t*>(xq), reinterpret_cast<const int8_t*>(wq), y, M, N, K);
     if (st != QL_OK || M == 0 || N == 0)
         return st;

@@ -37,3 +37,16 @@ def test_every_kernel_is_reached(kernel):
 def test_largest_sizes(kernel):
     for s in ((1, 1, 64), ((1 << 31) - 1, 1, 64), (1, 1 << 23, 64), (2 ** 14, 1 << 23, 131008), ((1 << 31) - 1, 64, 64)):
         assert 0 <= kernel(*s) < len(TILES)
+
+
+def test_grids_stay_below_2_to_32_threads(kernel):
+    """At the most rows, with as many columns as 288 GB hold beside them: few-row kernels split their rows over launches."""
+    for M in (1 << 30, (1 << 30) - 77, 1 << 28, 1 << 24):
+        for K in (64, 128, 4096):
+            for N in (1, 48, 64, 130, 700, 1 << 23):
+                if M * K + M * N * 2 + N * K > 288 << 30:
+                    continue
+                k = kernel(M, N, K)
+                r, c = TILES[k]
+                threads = 256 if k == len(TILES) - 1 else 512
+                assert k < 6 or -(-M // r) * -(-N // c) * threads < 1 << 32, (M, N, K, k)

@@ -63,7 +63,7 @@ def test_gemm(lib):
     for kw in (dict(x=A + 8), dict(w=MIS), dict(y=A + 8), dict(xs=A + 2), dict(ws=A + 1), dict(bias=A + 3)):
         assert f(**kw) == ALIGN
     for kw in (dict(M=-1), dict(N=-1), dict(K=0), dict(K=32), dict(K=200), dict(K=131072), dict(N=(1 << 23) + 1),
-               dict(M=1 << 31)):
+               dict(M=1 << 31), dict(M=(1 << 30) + 1)):
         assert f(**kw) == SHAPE, kw
     for kw in (dict(dt=2), dict(act=3), dict(act=-1)):
         assert f(**kw) == DTYPE
