@@ -573,21 +573,22 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
 // take twice the codes' space). A wave adds a unit's products to its own sums [token][32] in LDS; the
 // waves' sums are added at the end, and the parts' by the workgroup that comes last.
 
-constexpr int DOWN_SLOT = DOWN_COLS * QB + 256;
+constexpr int DOWN_S = 2, DOWN_SLOT = DOWN_COLS * QB + 256;
 
-template <int TOKENS, int S>
+template <int TOKENS>
 struct DownShared {
-    int8_t rings[NW * S * DOWN_SLOT];
+    int8_t rings[NW * DOWN_S * DOWN_SLOT];
     float sums[NW][TOKENS][DOWN_COLS];
     MoeUnit units[MOE_UNITS];
     uint8_t pair_token[TOKENS * MOE_TOP_K];
     int last;
 };
 
-template <int TERMS, int TOKENS, int S = 2>
+template <int TERMS, int TOKENS>
 __global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
     constexpr int COPIES = DOWN_COLS / 8 + 1 + TERMS * 4;
-    __shared__ __attribute__((aligned(1024))) DownShared<TOKENS, S> sh;
+    constexpr int S = DOWN_S;
+    __shared__ __attribute__((aligned(1024))) DownShared<TOKENS> sh;
     auto& sums = sh.sums;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
@@ -1178,10 +1179,8 @@ void launch_wide(const Moe& g, hipStream_t stream) {
     const dim3 up((uint32_t)(most < cu_count() ? most : cu_count())), nt(NT);
     if (g.l.E <= 64)
         moe_up_wide_kernel<4, TERMS><<<up, nt, 0, stream>>>(g);
-    else if (g.l.E <= 128)
+    else   // at most 128: a launch has 1024 pairs, and an expert 8 on average
         moe_up_wide_kernel<8, TERMS><<<up, nt, 0, stream>>>(g);
-    else
-        moe_up_wide_kernel<32, TERMS><<<up, nt, 0, stream>>>(g);
     const dim3 down((uint32_t)((g.l.K + WIDE_COLS - 1) / WIDE_COLS * g.parts * WIDE_PARTS));
     moe_down_wide_kernel<TERMS><<<down, nt, 0, stream>>>(g);
 }
