@@ -719,11 +719,12 @@ def linear_e4m3_block(x, wq, w_scale, bias=None, act: str = "none", out_dtype=No
 
 def moe_router(x, w, logits=None):
     """A router's logits: x fp16 [T, K] @ w fp16 [E, K]^T as fp32 [T, E]."""
-    index = x.get_device() if isinstance(x, torch.Tensor) else -1
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is torch.float16 and x.is_contiguous()):
+        _check(x, "x", (torch.float16,))
+    if x.dim() != 2:
         raise ValueError("x must be 2-D [T, K]")
     T, K = x.shape
-    xp = _same(x, "x", torch.float16, (T, K), index)
+    xp, index = x.data_ptr(), x.get_device()
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be 2-D [E, K]")
     E = w.shape[0]
