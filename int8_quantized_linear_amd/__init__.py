@@ -658,12 +658,15 @@ def quantize_per_row_block_e4m3(x: torch.Tensor, xq: Optional[torch.Tensor] = No
     index = x.get_device()
     if xq is None:
         xq = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    elif _codes_e4m3(xq, "xq", 2) and (xq.shape != x.shape or xq.device != x.device):
-        raise ValueError("xq has shape %s on %s, expected %s on %s" % (tuple(xq.shape), xq.device, (M, K), x.device))
+        qp = xq.data_ptr()
+    else:
+        qp = _codes_e4m3(xq, "xq", 2)
+        if xq.shape != x.shape or xq.device != x.device:
+            raise ValueError("xq has shape %s on %s, expected %s on %s" % (tuple(xq.shape), xq.device, (M, K), x.device))
     if x_scale is None:
         x_scale = x.new_empty((_blocks(K), M), dtype=torch.float32)
     sp = _same(x_scale, "x_scale", torch.float32, (_blocks(K), M), index)
-    _call_on(index, "quantize_per_row_block_e4m3", xp, dt, M, K, xq.data_ptr(), sp, _raw_stream(index))
+    _call_on(index, "quantize_per_row_block_e4m3", xp, dt, M, K, qp, sp, _raw_stream(index))
     return xq, x_scale
 
 

@@ -51,3 +51,14 @@ def test_the_others(ql):
                  lambda: ql.moe_e4m3_block(_half(3, 64), f(3, 4), _codes(4, 128, 64), f(4, 1, 1), _codes(4, 64, 64), f(4, 1, 1), 2)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_codes_of_another_shape(ql, monkeypatch):
+    """The output for the codes has x's shape, also where one of the two holds nothing (its pointer is null). CPU
+    tensors stand for the GPU's here."""
+    monkeypatch.setattr(ql, "_check", lambda t, *args: t)
+    monkeypatch.setattr(ql, "_current_device", lambda: -1)
+    for x, xq in ((_half(0, 64), _codes(0, 32)), (_half(5, 64), _codes(0, 64)), (_half(5, 64), _codes(4, 64)),
+                  (_half(0, 64), _codes(5, 64))):
+        with pytest.raises(ValueError, match="xq has shape"):
+            ql.quantize_per_row_block_e4m3(x, xq)
