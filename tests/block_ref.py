@@ -129,9 +129,21 @@ def routes(logits, k, renorm):
     return out
 
 
-def moe64(x, logits, w13, s13, w2, s2, k, renorm):
+def bf16_terms(h, terms):
+    """h rounded to fp32, as the sum of so many bf16 terms, each the nearest to what those before leave."""
+    rest = torch.from_numpy(np.ascontiguousarray(h, F32))
+    out = torch.zeros(rest.shape, dtype=torch.float64)
+    for _ in range(terms):
+        t = rest.bfloat16().float()
+        out += t.double()
+        rest = rest - t
+    return out.numpy()
+
+
+def moe64(x, logits, w13, s13, w2, s2, k, renorm, h_error=2.0 ** -17, terms=None):
     """The layer in 64 bits, and a bound on the kernel's error before the output's rounding, both
-    [T, K]. fp16 (bf16) products with codes are exact in fp32; a sum of n products in any order, each
+    [T, K]. h_error: of h's terms, 2^-17 for two (fp16 outputs), 2^-25 for three (fp32). With `terms`, the result is that
+    of h cut to so many terms, for tests of what a comparison tells apart. fp16 (bf16) products with codes are exact in fp32; a sum of n products in any order, each
     addition at most one unit off, has an error of n 2^-23 of the sum of magnitudes: 128 and 4 more
     in a block, one a block, 8 at the join."""
     T, K = x.shape
@@ -155,8 +167,10 @@ def moe64(x, logits, w13, s13, w2, s2, k, renorm):
             s = g / (1 + np.exp(-g))
         es = 1.1 * eg + (np.abs(g) + 4) * 2.0 ** -23 * np.abs(s) + 1e-30
         h = p * s * u
-        # both factors' errors, the weight's, three roundings, two bf16 terms
-        eh = p * (es * (np.abs(u) + eu) + np.abs(s) * eu) + np.abs(h) * (prel + 3 * 2.0 ** -24 + 2.0 ** -17)
+        # both factors' errors, the weight's, three roundings, the bf16 terms
+        eh = p * (es * (np.abs(u) + eu) + np.abs(s) * eu) + np.abs(h) * (prel + 3 * 2.0 ** -24 + h_error)
+        if terms is not None:
+            h = bf16_terms(h, terms)
         y[rows] += h @ b.T
         err[rows] += eh @ np.abs(b).T + down * (np.abs(h) + eh) @ np.abs(b).T
     return y, err
