@@ -37,7 +37,12 @@ __device__ inline float activated(float v, int act) {
 // in LDS, S - 1 blocks ahead, and needs no barrier until its sums are joined with the others'.
 // W is the first operand, so a lane's sums belong to one row m (lane & 15) and four columns
 // (4 (lane >> 4) + i): one scale of X a lane, one of W for all.
-template <int NB, int MB, int SW, int S, bool YF16>
+// ONCE: one group of rows, so that W is read once and loaded non-temporally, also where K is no multiple of 128
+// and a line holds codes of two blocks; several groups read W again, and keep it. us from cold memory,
+// non-temporal / kept: 1 x 11008 x 4096 12.1 / 13.0, 1 x 11008 x 4160 12.4 / 12.9, 32 x 11008 x 2112 10.7 / 11.0,
+// 1 x 4096 x 2112 4.5 / 4.5 (one group); 64 x 4096 x 4096 8.7 / 7.3, 64 x 4096 x 2112 8.5 / 6.7, 300 x 70 x 2176
+// 5.9 / 4.2, 150 x 2000 x 8192 19.6 / 17.4, 600 x 700 x 1024 6.9 / 6.2 (2 to 19 groups).
+template <int NB, int MB, int SW, int S, bool YF16, bool ONCE>
 __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
     constexpr int W_BYTES = NB * 16 * QB, X_BYTES = MB * 16 * QB, SLOT = W_BYTES + X_BYTES + 256;
     constexpr int COPIES = 2 * NB + 2 * MB + 1;
@@ -61,8 +66,8 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
         const int o0 = row * g.K + 16 * c0 + b * QB, o1 = row * g.K + 16 * c1 + b * QB;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            buffer_to_lds16<2>(rw, (o0 + 16 * i * g.K) | cut0, 0, to + 2048 * i);
-            buffer_to_lds16<2>(rw, (o1 + (16 * i + 8) * g.K) | cut1, 0, to + 2048 * i + 1024);
+            buffer_to_lds16<ONCE ? 2 : 0>(rw, (o0 + 16 * i * g.K) | cut0, 0, to + 2048 * i);
+            buffer_to_lds16<ONCE ? 2 : 0>(rw, (o1 + (16 * i + 8) * g.K) | cut1, 0, to + 2048 * i + 1024);
         }
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
@@ -375,7 +380,7 @@ Chosen choose(int64_t M, int64_t N, int64_t K) {
 
 template <bool YF16>
 void launch_few(const BlockGemm& g, int c, hipStream_t stream) {
-    auto go = [&](auto kernel) {
+    auto go = [&](auto kernel, auto several) {
         const Choice& k = CHOICES[c];
         // rows in launches whose grid stays within 65535 in y
         const int64_t most = (int64_t)k.rows * 65535;
@@ -385,14 +390,15 @@ void launch_few(const BlockGemm& g, int c, hipStream_t stream) {
             p.xs += m;
             p.y = reinterpret_cast<int8_t*>(g.y) + m * g.N * (YF16 ? 2 : 4);
             p.rows = (int)(g.M - m < most ? g.M - m : most);
-            kernel<<<dim3((uint32_t)((g.N + k.cols - 1) / k.cols), (uint32_t)((p.rows + k.rows - 1) / k.rows)),
-                     dim3(64 * k.waves), 0, stream>>>(p);
+            const dim3 grid((uint32_t)((g.N + k.cols - 1) / k.cols), (uint32_t)((p.rows + k.rows - 1) / k.rows));
+            (g.M <= k.rows ? kernel : several)<<<grid, dim3(64 * k.waves), 0, stream>>>(p);
         }
     };
     auto of = [&](auto i) {
         constexpr Choice k = CHOICES[decltype(i)::value];
         if (c == decltype(i)::value)
-            go(gemm_block_few_kernel<k.nb, k.mb, k.waves, k.slots, YF16>);
+            go(gemm_block_few_kernel<k.nb, k.mb, k.waves, k.slots, YF16, true>,
+               gemm_block_few_kernel<k.nb, k.mb, k.waves, k.slots, YF16, false>);
     };
     of(std::integral_constant<int, 0>{});
     of(std::integral_constant<int, 1>{});
