@@ -39,8 +39,12 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
 
-// Codes that are read once are loaded non-temporally (AUX 2) where rows are whole lines of 128 bytes.
-// Else a line holds codes of two blocks, and is worth keeping until the second is read.
+// The experts' codes are loaded non-temporally (AUX 2) where their rows are whole lines of 128 bytes. Else a
+// line holds codes of two blocks, and is worth keeping until the second is read. The layer, us, non-temporal /
+// kept, at T, E, top_k, K, I: 64 64 6 2048 1408 120.4 / 126.7, 5 8 2 4096 7168 94.6 / 101.1 (whole lines);
+// 64 60 6 1984 1344 129.3 / 126.3, 5 8 2 4160 7232 114.7 / 112.6 (halves); 8 60 4 2048 1344 57.4 / 59.2 and with
+// each kernel by its own rows 53.4. The few-row product has another rule, stated at it; the tiles read W
+// once for every tile of rows, and keep it.
 inline __host__ __device__ bool whole_lines(int row_bytes) { return row_bytes % 128 == 0; }
 
 // s_waitcnt immediates: at most n vector-memory operations pending, LDS operations left alone;

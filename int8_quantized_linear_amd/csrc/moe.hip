@@ -432,7 +432,7 @@ struct UpShared {
     Routes rt;
 };
 
-template <int R, int TERMS>
+template <int R, int TERMS, bool WHOLE>
 __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
     constexpr int S = UP_S, COPIES = 5 + 4;
     __shared__ __attribute__((aligned(1024))) UpShared sh;
@@ -482,10 +482,10 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(Moe g) {
         const int b = wave + NW * nx.j, left = K - b * QB;   // blocks past the end come as zeros
         const int cut0 = 16 * c0 < left ? 0 : far, cut1 = 16 * c1 < left ? 0 : far;
         const int o0 = row * K + 16 * c0 + b * QB, o1 = (row + 8) * K + 16 * c1 + b * QB;
-        buffer_to_lds16<2>(nx.gate, o0 | cut0, 0, to);
-        buffer_to_lds16<2>(nx.gate, o1 | cut1, 0, to + 1024);
-        buffer_to_lds16<2>(nx.up, o0 | cut0, 0, to + 2048);
-        buffer_to_lds16<2>(nx.up, o1 | cut1, 0, to + 3 * 1024);
+        buffer_to_lds16<WHOLE ? 2 : 0>(nx.gate, o0 | cut0, 0, to);
+        buffer_to_lds16<WHOLE ? 2 : 0>(nx.gate, o1 | cut1, 0, to + 1024);
+        buffer_to_lds16<WHOLE ? 2 : 0>(nx.up, o0 | cut0, 0, to + 2048);
+        buffer_to_lds16<WHOLE ? 2 : 0>(nx.up, o1 | cut1, 0, to + 3 * 1024);
         global_to_lds4(nx.scale + min(b, nkb - 1), to + 4096);
         // past K the codes are zeros, and x anything finite
         const int bx = min(b, nkb - 1) * QB, half = left > 64 ? 128 : 0;
@@ -585,7 +585,7 @@ struct DownShared {
     int last;
 };
 
-template <int TERMS, int TOKENS>
+template <int TERMS, int TOKENS, bool WHOLE>
 __global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
     constexpr int COPIES = DOWN_COLS / 8 + 1 + TERMS * 4;
     constexpr int S = DOWN_S;
@@ -662,8 +662,8 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(Moe g) {
         const int o0 = row * I + 16 * c0 + nx.b * QB, o1 = (row + 8) * I + 16 * c1 + nx.b * QB;
 #pragma unroll
         for (int i = 0; i < DOWN_COLS / 16; ++i) {
-            buffer_to_lds16<2>(nx.w, (o0 + 16 * i * I) | cut0, 0, to + 2048 * i);
-            buffer_to_lds16<2>(nx.w, (o1 + 16 * i * I) | cut1, 0, to + 2048 * i + 1024);
+            buffer_to_lds16<WHOLE ? 2 : 0>(nx.w, (o0 + 16 * i * I) | cut0, 0, to + 2048 * i);
+            buffer_to_lds16<WHOLE ? 2 : 0>(nx.w, (o1 + 16 * i * I) | cut1, 0, to + 2048 * i + 1024);
         }
         global_to_lds4(nx.scale + nx.b, to + DOWN_COLS * QB);
         const int half = left > 64 ? 128 : 0;   // past I the codes are zeros, and h anything finite
@@ -1195,19 +1195,21 @@ template <int TERMS>
 void launch_narrow(const Moe& g, hipStream_t stream) {
     const int64_t most = (int64_t)(g.T * g.l.top_k < MOE_UNITS ? g.T * g.l.top_k : MOE_UNITS) * (g.l.I / 16);
     const dim3 up((uint32_t)(most < cu_count() ? most : cu_count())), nt(NT);
+    auto launch_up = [&](auto kernel, auto halves) { (whole_lines(g.l.K) ? kernel : halves)<<<up, nt, 0, stream>>>(g); };
     if (g.l.E <= 64)
-        moe_up_kernel<4, TERMS><<<up, nt, 0, stream>>>(g);
+        launch_up(moe_up_kernel<4, TERMS, true>, moe_up_kernel<4, TERMS, false>);
     else if (g.l.E <= 128)
-        moe_up_kernel<8, TERMS><<<up, nt, 0, stream>>>(g);
+        launch_up(moe_up_kernel<8, TERMS, true>, moe_up_kernel<8, TERMS, false>);
     else
-        moe_up_kernel<32, TERMS><<<up, nt, 0, stream>>>(g);
+        launch_up(moe_up_kernel<32, TERMS, true>, moe_up_kernel<32, TERMS, false>);
     const dim3 down((uint32_t)(g.l.K / DOWN_COLS * g.parts));
+    auto launch_down = [&](auto kernel, auto halves) { (whole_lines(g.l.I) ? kernel : halves)<<<down, nt, 0, stream>>>(g); };
     if (g.T <= 16)
-        moe_down_kernel<TERMS, 16><<<down, nt, 0, stream>>>(g);
+        launch_down(moe_down_kernel<TERMS, 16, true>, moe_down_kernel<TERMS, 16, false>);
     else if (g.T <= 32)
-        moe_down_kernel<TERMS, 32><<<down, nt, 0, stream>>>(g);
+        launch_down(moe_down_kernel<TERMS, 32, true>, moe_down_kernel<TERMS, 32, false>);
     else
-        moe_down_kernel<TERMS, 64><<<down, nt, 0, stream>>>(g);
+        launch_down(moe_down_kernel<TERMS, 64, true>, moe_down_kernel<TERMS, 64, false>);
 }
 
 template <int TERMS>
