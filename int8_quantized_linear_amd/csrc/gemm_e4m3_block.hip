@@ -184,10 +184,16 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
 // copies of it have landed and that all waves have read the one before, whose place is then filled. X's
 // scales come into registers, one a lane. Outputs leave through LDS in whole 16-byte pieces of a row.
 //
-// A CU takes 40 to 55 GB/s of such copies here (whatever the tile, and with three stages or four), so small
-// tiles on many CUs win: us for 64 x 64, 64 x 128, 128 x 64 of this kernel and 128 x 128 below
+// Bound by the copies into LDS. us from warm memory, with work left out in copies made for timing:
+//                              whole  no matrix instr.  no LDS reads  copies alone  the same from L1  no copies
+//   512 x 4096 x 4096 / 8192   18.8 / 32.7  16.2 / 28.2  17.4 / 29.3  15.6 / 27.8   16.1 / 26.4   12.7 / 19.4
+// (from L1: every stage copies the first block.) 32 stages of two workgroups a CU are 13.9 us, 75 GB/s a CU; the
+// copies alone take 12.1 of them (87 GB/s; 10.3 and 102 from L1), and 4.9 us are launch, first loads and outputs. The LDS
+// is active for 24% of the cycles (bank conflicts 2% of those), the matrix cores for 23%. So what counts is how many bytes the
+// busiest CU copies: us for 64 x 64, 64 x 128, 128 x 64 of this kernel and 128 x 128 below
 //   333 x 4001 x 2112  12.6 14.6 13.8 14.8      512 x 4096 x 4096   18.8 22.0 21.0 20.3
 //   256 x 4096 x 4096  14.6 21.0 20.1 19.7      1024 x 4096 x 4096  33.7 30.7 30.5 24.3
+// (a fourth stage changed nothing).
 // Reading the next stage's operands from LDS under this one's products changed nothing.
 template <bool YF16>
 __global__ __launch_bounds__(256) void gemm_block_mid_kernel(BlockGemm g) {
