@@ -40,9 +40,9 @@ __device__ inline float activated(float v, int act) {
     return act == ACT_GELU ? activation<ACT_GELU, F16>(v) : act == ACT_SILU ? activation<ACT_SILU, F16>(v) : v;
 }
 
-// Few rows: bound by the read of W. A workgroup owns 16 output columns and 16 MB rows; its SW waves
+// Few rows: bound by the read of W. A workgroup owns 16 NB output columns and 16 MB rows; its SW waves
 // take the blocks of K in turn (neighbouring waves read neighbouring 128 bytes of W's rows). A wave
-// copies its blocks (16 rows of W, the rows of X, X's scales) straight into its own ring of S slots
+// copies its blocks (16 NB rows of W, the rows of X, X's scales) straight into its own ring of S slots
 // in LDS, S - 1 blocks ahead, and needs no barrier until its sums are joined with the others'.
 // W is the first operand, so a lane's sums belong to one row m (lane & 15) and four columns
 // (4 (lane >> 4) + i): one scale of X a lane, one of W for all.
@@ -331,14 +331,16 @@ __global__ __launch_bounds__(64 * NWAVES, 1) void gemm_block_tile_kernel(BlockGe
 
 // The kernels to choose from: few-row kernels with NB x 16 columns and MB x 16 rows a workgroup, tiles, and
 // the kernel between. A call takes rounds of as many workgroups as the chip holds at once, each about a + b * blocks
-// of K us long; the least product is chosen. a and b are fits to warm times on MI355X of 60 shapes
-// (M 64-1024, N 1024-14336, K 1024-11008) and of M 1-64 from cold memory; the choices among them are within 5%
-// of the best. Some of both sides, us (chosen first):
-//   1 x 11008 x 4096     2x1 12.0, 1x1 14.1 (cold)     64 x 4096 x 4096    2x2 8.0, 1x2 11.3, 128x128 18.3
-//   32 x 11008 x 4096    4x2 12.7, 1x2 15.8            128 x 4096 x 4096   2x4 10.4, 128x128 18.2
-//   96 x 11008 x 4096    128x128 19.1, 2x4 28.0        256 x 4096 x 4096   64x64 14.6, 128x128 19.7
-//   from cold memory: 512 x 4096 x 4096 64x64 18.8, 128x128 20.3; 150 x 2000 x 8192 2x4 19.6, 64x64 23.8
-//   333 x 11008 x 4096   128x192 27.4, 128x128 37.9    1024 x 11008 x 4096 256x192 45, 128x192 57, 128x128 63
+// of K us long; the least product is chosen. a and b are fits to times on MI355X of 60 shapes. At 250 others (M 1-4096,
+// N 192-14336, K 256-14336, from cold memory) the choice takes 3.1% longer than the best in the geometric mean,
+// at 202 up to 5%, at 14 up to 10%, at most 48% (32 x 192 x 5120 1x2 7.6 us, 1x1 5.2). Some of both sides, us from cold
+// memory (chosen first):
+//   1 x 11008 x 4096     2x1 12.1, 1x1 12.9            64 x 4096 x 4096    2x2 7.4, 2x1 9.4, 64x64 14.5
+//   32 x 11008 x 4096    4x2 14.5, 2x2 16.6            128 x 4096 x 4096   2x4 10.2, 4x2 10.7, 64x64 14.8
+//   96 x 11008 x 4096    64x64 23.2, 128x128 25.8      256 x 4096 x 4096   64x64 15.6, 2x4 18.3, 128x128 19.3
+//   512 x 4096 x 4096    64x64 21.9, 128x128 23.5      150 x 2000 x 8192   2x4 17.1, 4x2 15.0
+//   333 x 11008 x 4096   128x192 30.5, 256x192 42.2    1024 x 11008 x 4096 256x192 48.2, 128x192 61.7
+//   1024 x 4096 x 4096   128x128 26.3, 128x192 30.0    4096 x 4096 x 4096  mixed 79.2, 256x192 82.0
 struct Choice {
     int nb, mb, waves, slots;   // few-row kernels; 0: tiles
     int rows, cols;             // of a workgroup
