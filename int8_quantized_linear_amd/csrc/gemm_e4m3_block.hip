@@ -14,10 +14,13 @@
 // (fp32 outputs; the best tiles of each). All kernels keep to one arithmetic, which gemm_e4m3_per_channel has too, so
 // that the precision does not depend on the number of rows.
 //
-// Few rows are bound by the read of W (1 x 11008 x 4096: 8.9 us, 5.1 TB/s), many by the matrix cores at the
-// chip's power limit and the multiply-adds beside them (2048 x 11008 x 4096: 93 us, 1990 TFLOP/s; a library
-// product of 8192 x 8192 x 8192 on such codes without block scales reaches 2910). Between, by what a CU's
-// copies bring and how many CUs have a tile (333 x 4001 x 2112: 12.6 us).
+// Few rows are bound by the read of W (1 x 11008 x 4096: 8.9 us, 5.1 TB/s). Between, by what a CU's copies bring and
+// how many CUs have a tile (333 x 4001 x 2112: 12.6 us). Many rows, 2048 x 11008 x 4096: 92 us, 2010 TFLOP/s, where a
+// library product of 8192 x 8192 x 8192 on such codes without block scales reaches 2910. Its 464 tiles are 1.81 of two
+// rounds, at the library's rate 70 us; the matrix cores are busy for 56% of a busy CU's cycles, at 2.1 GHz. us with work left
+// out in copies made for timing: matrix instructions, barriers and outputs alone 67, with the multiply-adds for the
+// scales 72, all but the reads of LDS 81, all but the copies 76, all but the multiply-adds 83. So the copies and reads beside
+// the matrix instructions cost more than the multiply-adds.
 #include "e4m3_block.h"
 #include "gemm_w8a8_tile.h"
 
@@ -185,11 +188,12 @@ __global__ __launch_bounds__(64 * SW) void gemm_block_few_kernel(BlockGemm g) {
 // scales come into registers, one a lane. Outputs leave through LDS in whole 16-byte pieces of a row.
 //
 // Bound by the copies into LDS. us from warm memory, with work left out in copies made for timing:
-//                              whole  no matrix instr.  no LDS reads  copies alone  the same from L1  no copies
-//   512 x 4096 x 4096 / 8192   18.8 / 32.7  16.2 / 28.2  17.4 / 29.3  15.6 / 27.8   16.1 / 26.4   12.7 / 19.4
-// (from L1: every stage copies the first block.) 32 stages of two workgroups a CU are 13.9 us, 75 GB/s a CU; the
-// copies alone take 12.1 of them (87 GB/s; 10.3 and 102 from L1), and 4.9 us are launch, first loads and outputs. The LDS
-// is active for 24% of the cycles (bank conflicts 2% of those), the matrix cores for 23%. So what counts is how many bytes the
+//                              whole        no products  no LDS reads  neither      no reads, L1  no copies
+//   512 x 4096 x 4096 / 8192   18.8 / 32.7  16.2 / 28.2  17.4 / 29.3   15.6 / 27.8  16.1 / 26.4   12.7 / 19.4
+// (L1: every stage copies the first block.) 32 stages of two workgroups a CU are 13.9 us, 75 GB/s a CU; the copies
+// alone take 12.1 of them (87 GB/s), and 4.9 us are launch, first loads and outputs. Lines in L1 bring no more than 102
+// GB/s a CU, so neither L2 nor memory is the limit. The LDS is active for 24% of the cycles (bank conflicts 2% of those), the
+// matrix cores for 23%. So what counts is how many bytes the
 // busiest CU copies: us for 64 x 64, 64 x 128, 128 x 64 of this kernel and 128 x 128 below
 //   333 x 4001 x 2112  12.6 14.6 13.8 14.8      512 x 4096 x 4096   18.8 22.0 21.0 20.3
 //   256 x 4096 x 4096  14.6 21.0 20.1 19.7      1024 x 4096 x 4096  33.7 30.7 30.5 24.3
