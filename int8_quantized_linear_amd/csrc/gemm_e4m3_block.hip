@@ -34,8 +34,8 @@ struct BlockGemm {
     const float* ws;
     const float* bias;
     void* y;
-    int rows, N, K, act;   // rows of this launch
-    int64_t M;             // rows of xs
+    int rows, N, K, act;
+    int64_t M;   // rows too, for products past 2^31
 };
 
 template <bool F16>
@@ -401,19 +401,11 @@ Chosen choose(int64_t M, int64_t N, int64_t K) {
 
 template <bool YF16>
 void launch_few(const BlockGemm& g, int c, hipStream_t stream) {
+    // (The rule takes tiles long before the groups of rows pass the grid's 65535 in y: tests/test_block_grids.py.)
     auto go = [&](auto kernel, auto several) {
         const Choice& k = CHOICES[c];
-        // rows in launches whose grid stays within 65535 in y
-        const int64_t most = (int64_t)k.rows * 65535;
-        for (int64_t m = 0; m < g.M; m += most) {
-            BlockGemm p = g;
-            p.xq += m * g.K;
-            p.xs += m;
-            p.y = reinterpret_cast<int8_t*>(g.y) + m * g.N * (YF16 ? 2 : 4);
-            p.rows = (int)(g.M - m < most ? g.M - m : most);
-            const dim3 grid((uint32_t)((g.N + k.cols - 1) / k.cols), (uint32_t)((p.rows + k.rows - 1) / k.rows));
-            (g.M <= k.rows ? kernel : several)<<<grid, dim3(64 * k.waves), 0, stream>>>(p);
-        }
+        const dim3 grid((uint32_t)((g.N + k.cols - 1) / k.cols), (uint32_t)((g.rows + k.rows - 1) / k.rows));
+        (g.rows <= k.rows ? kernel : several)<<<grid, dim3(64 * k.waves), 0, stream>>>(g);
     };
     auto of = [&](auto i) {
         constexpr Choice k = CHOICES[decltype(i)::value];
@@ -431,10 +423,8 @@ void launch_few(const BlockGemm& g, int c, hipStream_t stream) {
 
 template <bool YF16>
 void launch_mid(const BlockGemm& g, hipStream_t stream) {
-    BlockGemm p = g;
-    p.rows = (int)g.M;
     const int64_t tiles = (g.M + 63) / 64 * ((g.N + 63) / 64);
-    gemm_block_mid_kernel<YF16><<<dim3((uint32_t)tiles), dim3(256), 0, stream>>>(p);
+    gemm_block_mid_kernel<YF16><<<dim3((uint32_t)tiles), dim3(256), 0, stream>>>(g);
 }
 
 template <int YMODE>
@@ -460,7 +450,7 @@ extern "C" int ql_gemm_e4m3_block_kernel(int64_t M, int64_t N, int64_t K) { retu
 ql_status launch_gemm_e4m3_block(const uint8_t* xq, const float* x_scale, const uint8_t* wq, const float* w_scale,
                                  const float* bias, int act, void* y, bool y_f16, int64_t M, int64_t N, int64_t K,
                                  hipStream_t stream) {
-    const BlockGemm g{xq, x_scale, wq, w_scale, bias, y, 0, (int)N, (int)K, act, M};
+    const BlockGemm g{xq, x_scale, wq, w_scale, bias, y, (int)M, (int)N, (int)K, act, M};
     const Chosen c = choose(M, N, K);
     if (c.kernel == MID)
         (y_f16 ? launch_mid<true> : launch_mid<false>)(g, stream);
